@@ -75,11 +75,14 @@
 extern "C" {
 #endif
 
-/* 7: adds SSM_HEAD_SCALAR (head_dim field); 6 added strided views (ssm_layout, the layout fields of ssm_scan_args and
+/* 8: adds the short causal convolution (ssm_conv_*), 8-bit activation
+ * checkpoints (ssm_ckpt8_*) and the serving forms over packed rows
+ * (ssm_tokens_*); structs of 7 unchanged.  7 added SSM_HEAD_SCALAR
+ * (head_dim field); 6 added strided views (ssm_layout, the layout fields of ssm_scan_args and
  * pd_scan_args) and the ZOH discretisation (discretization field); 5 added
  * ssm_scan_fwd_noalloc and ssm_roof_probe; 4 added SSM_COMPLEX_DENSE; 3 added
  * ssm_sensitivity_rows and SSM_OP_SENS_ROWS; struct layouts as in 2 */
-#define SSM_ABI_VERSION 7
+#define SSM_ABI_VERSION 8
 
 /* status codes */
 #define SSM_OK               0
@@ -111,6 +114,10 @@ extern "C" {
 #define SSM_OP_COMPLEX_RTRL 5
 #define SSM_OP_OUTPUT_SENS  6
 #define SSM_OP_SENS_ROWS    7
+#define SSM_OP_CONV_FWD     8   /* ssm_conv_args: no workspace             */
+#define SSM_OP_CONV_BWD     9   /* ssm_conv_args                           */
+#define SSM_OP_TOKENS_CONV 10   /* ssm_tokens_conv_args: no workspace      */
+#define SSM_OP_TOKENS_SCAN 11   /* ssm_tokens_scan_args                    */
 
 /* discretisations of SSM_REAL_SELECTIVE (S3M page, section 1.1) */
 #define SSM_EULER 0   /* b_t = delta_t x_t B_t (the default)                               */
@@ -340,7 +347,8 @@ typedef struct {
 } pd_scan_grads;
 
 /* Workspace size in bytes for operation `op` (SSM_OP_*) with `args`
- * (ssm_scan_args* for the ssm_* ops, pd_scan_args* for the pd_* ops).
+ * (ssm_scan_args* for the ssm_* scan ops, pd_scan_args* for the pd_* ops, the
+ * struct of their own for the convolution and the packed-row ops).
  * Host-only; enqueues nothing.  Errors as for the operation itself. */
 int ssm_workspace_bytes(int op, const void* args, size_t* out_bytes);
 
@@ -447,6 +455,144 @@ int pd_scan_fwd(const pd_scan_args* args, const pd_scan_fwd_out* out,
 /* PD backward with the selection from args->sel (or recomputed from logits). */
 int pd_scan_bwd(const pd_scan_args* args, const pd_scan_bwd_in* in,
                 const pd_scan_grads* grads, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Short causal convolution (training form).  The depthwise convolution along
+ * the sequence in front of a selective scan, with the bias and activation of
+ * its layer.  With e = the W-1 inputs before step 0 followed by x,
+ *   p[b,d,t] = bias[d] + sum_{k<W} w[d,k] e[b,d,t+k],
+ *   y = p, or p * sigmoid(p) with silu = 1,
+ *   last[b,d,:] = e[b,d,L..L+W-2]   (what a following segment takes as init).
+ * The backward recomputes p from its input.  The input is x, or x's 8-bit
+ * checkpoint (below) in place of x: the values it stands for then are the
+ * input, widened to float32.
+ * Roles of `layout`: SSM_V_X, SSM_V_GY inputs, SSM_V_Y, SSM_V_GX outputs, all
+ * (B,D,L).  An 8-bit checkpoint is dense.  batch, channels and length may be 0:
+ * tensors with no elements are not touched; with length 0 last is init (or 0)
+ * and ginit is glast (or 0); gw and gbias are 0.
+ * Errors: SSM_ERR_UNSUPPORTED for a width other than 2, 3 or 4; SSM_ERR_SHAPE
+ * where batch * length reaches 2^33.
+ */
+typedef struct {
+    int32_t dtype;           /* of x, y, init, last and their gradients: SSM_F32 or SSM_BF16 */
+    int32_t silu;            /* 0 or 1                                                       */
+    int64_t batch, channels, length, width;
+    const void*   x;         /* (B,D,L) dtype; exactly one of x and x8 is given              */
+    const int8_t* x8;        /* (B,D,L) 8-bit checkpoint of the input                        */
+    const float*  x8_scale;  /* (B,D,ceil(L/SSM_CKPT8_BLOCK)), with x8                       */
+    const float*  w;         /* (D,W) f32, w[d,W-1] for the step itself                      */
+    const float*  bias;      /* nullable (D) f32                                             */
+    const void*   init;      /* nullable (B,D,W-1) dtype: the inputs before step 0 (0)       */
+    const ssm_layout* layout;
+} ssm_conv_args;
+
+typedef struct {
+    void*   y;         /* nullable (B,D,L) dtype                                              */
+    void*   last;      /* nullable (B,D,W-1) dtype                                            */
+    int8_t* x8;        /* nullable (B,D,L): 8-bit checkpoint of x, written in the same pass
+                          (needs args->x); together with x8_scale                            */
+    float*  x8_scale;
+} ssm_conv_fwd_out;
+
+typedef struct {
+    void*  gx;         /* nullable (B,D,L) dtype                                              */
+    float* gw;         /* nullable (D,W)                                                      */
+    float* gbias;      /* nullable (D)                                                        */
+    void*  ginit;      /* nullable (B,D,W-1) dtype                                            */
+} ssm_conv_grads;
+
+int ssm_conv_fwd(const ssm_conv_args* args, const ssm_conv_fwd_out* out, void* stream);
+/* Gradients of Loss = sum <gy, y> + <glast, last> (gy (B,D,L), glast nullable (B,D,W-1), dtype). */
+int ssm_conv_bwd(const ssm_conv_args* args, const void* gy, const void* glast, const ssm_conv_grads* grads,
+                 void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * 8-bit activation checkpoints.  A stream (B,D,L) kept for the backward pass in
+ * one signed byte an element and one float32 scale for every SSM_CKPT8_BLOCK
+ * steps of a row, in place of its 2 or 4 bytes an element.  Per block, in
+ * float32 (each operation rounded to nearest even):
+ *   amax = max |x|,  scale = amax / 127,  q = rint(x * (127 / amax)),
+ * and the block stands for q * scale: off by at most (1/2 + 2^-16) scale.  A
+ * block whose amax is below 2^-100 is all zeros (scale 0); a block that holds a
+ * NaN or an infinity stands for NaN throughout.  ssm_conv_fwd writes it in the
+ * pass that reads x; ssm_conv_fwd and ssm_conv_bwd take it in place of x;
+ * ssm_ckpt8_unpack rounds it to a stream that ssm_scan_bwd takes.
+ */
+#define SSM_CKPT8_BLOCK 64
+typedef struct {
+    int32_t dtype;             /* of the stream                                              */
+    int64_t batch, channels, length;
+    const ssm_layout* layout;  /* ssm_ckpt8_pack: role SSM_V_X; ssm_ckpt8_unpack: role SSM_V_Y */
+} ssm_ckpt8_args;
+int ssm_ckpt8_pack(const ssm_ckpt8_args* args, const void* x, int8_t* x8, float* x8_scale, void* stream);
+int ssm_ckpt8_unpack(const ssm_ckpt8_args* args, const int8_t* x8, const float* x8_scale, void* y, void* stream);
+
+/*
+ * Serving forms: the convolution and the selective scan over packed rows.  The
+ * tokens of all sequences of a call are rows of one matrix, as the projections
+ * around them read and write them: sequence s owns rows seq_start[s] ..
+ * seq_start[s+1]-1 (ascending), in order.  seq_start NULL is the step form:
+ * one row a sequence (tokens == sequences).  What a sequence carries from call to
+ * call lies in a pool of slots; sequence s begins with the state in slot[s] (or
+ * with zeros where fresh[s] is not 0: its slot is not read) and leaves its
+ * state there.
+ *  - A sequence with no rows leaves its slot as it was, fresh or not.
+ *  - slot[s] outside [0, slots) marks an empty place of a padded batch: its rows
+ *    of y and every slot stay as they were.  So does a sequence whose slot an
+ *    earlier sequence of the call has (each slot has one sequence a call), and
+ *    rows that no sequence owns.
+ *  - seq_start, slot and fresh are device memory and are not checked on the
+ *    host: values out of range are never followed out of the buffers, but rows
+ *    of sequences that overlap or descend have unspecified results.
+ *  - Rows: row strides in elements; the row itself is contiguous.  Inputs may be
+ *    slices of wider rows (any stride >= 0), y's stride is at least its row.
+ *  - pool_stride: elements from one slot to the next, at least a slot's own.
+ *  - pool is read and written; it must not overlap any other buffer.
+ */
+typedef struct {
+    int32_t dtype;             /* of x, y and the pool                                       */
+    int32_t silu;              /* 0 or 1                                                     */
+    int64_t tokens, channels, width, sequences, slots;
+    const void*  x;            /* (T,D) dtype                                                */
+    const float* w;            /* (D,W) f32, width 2, 3 or 4                                 */
+    const float* bias;         /* nullable (D) f32                                           */
+    const int32_t* seq_start;  /* nullable (sequences + 1)                                   */
+    const int32_t* slot;       /* nullable (sequences); NULL: sequence s has slot s          */
+    const uint8_t* fresh;      /* nullable (sequences); NULL: every sequence has a state     */
+    void* pool;                /* (slots,D,W-1) dtype: the last W-1 inputs, oldest first     */
+    void* y;                   /* (T,D) dtype                                                */
+    int64_t x_stride, y_stride, pool_stride;
+} ssm_tokens_conv_args;
+
+/* y[t] = act(bias + sum_k w[:,k] e[t+k]), as ssm_conv_fwd with init = the slot and last = the slot. */
+int ssm_tokens_conv(const ssm_tokens_conv_args* args, void* stream);
+
+typedef struct {
+    int32_t dtype;             /* of delta, x, Bm, C, z and y                                */
+    int32_t delta_softplus;    /* as in ssm_scan_args                                        */
+    int64_t tokens, channels, state, sequences, slots;   /* state N in 1..16                 */
+    const void*  delta;        /* (T,D)                                                      */
+    const void*  x;            /* (T,D)                                                      */
+    const float* A;            /* (D,N) f32                                                  */
+    const void*  Bm;           /* (T,N)                                                      */
+    const void*  C;            /* (T,N)                                                      */
+    const float* delta_bias;   /* nullable (D) f32                                           */
+    const float* skip;         /* nullable (D) f32                                           */
+    const void*  z;            /* nullable (T,D) gate                                        */
+    const int32_t* seq_start;  /* as above                                                   */
+    const int32_t* slot;
+    const uint8_t* fresh;
+    float* pool;               /* (slots,D,N) f32: the state h                               */
+    void*  y;                  /* (T,D)                                                      */
+    int64_t delta_stride, x_stride, Bm_stride, C_stride, z_stride, y_stride, pool_stride;
+} ssm_tokens_scan_args;
+
+/* The selective scan (SSM_REAL_SELECTIVE, Euler input term) with its layer's skip and gate:
+ *   h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t,
+ *   y_t = (C_t . h_t + skip x_t) * z_t sigmoid(z_t)     (skip, z: where given).
+ * The states are float32.  The workspace (SSM_OP_TOKENS_SCAN) holds the states that cross from one
+ * range of rows to the next; the step form needs none. */
+int ssm_tokens_scan(const ssm_tokens_scan_args* args, void* ws, size_t ws_bytes, void* stream);
 
 /* Diagnostics: per-kernel timing with HIP events.  After ssm_profile_begin(n)
  * every kernel the entry points enqueue from this thread is bracketed by two

@@ -27,7 +27,9 @@ V_COUNT = 20
 SSM_REAL_SELECTIVE, SSM_REAL_DENSE, SSM_COMPLEX_SHARED, SSM_COMPLEX_DENSE, SSM_HEAD_SCALAR = 0, 1, 2, 3, 4
 _COMPLEX_MODES = (SSM_COMPLEX_SHARED, SSM_COMPLEX_DENSE)
 (SSM_OP_SCAN_FWD, SSM_OP_SCAN_BWD, SSM_OP_IMPULSE, SSM_OP_PD_FWD, SSM_OP_PD_BWD, SSM_OP_COMPLEX_RTRL,
- SSM_OP_OUTPUT_SENS, SSM_OP_SENS_ROWS) = range(8)
+ SSM_OP_OUTPUT_SENS, SSM_OP_SENS_ROWS, SSM_OP_CONV_FWD, SSM_OP_CONV_BWD, SSM_OP_TOKENS_CONV,
+ SSM_OP_TOKENS_SCAN) = range(12)
+SSM_CKPT8_BLOCK = 64   # steps of a row that share one scale of an 8-bit checkpoint
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -105,6 +107,42 @@ class PDGrads(ctypes.Structure):
     _fields_ = [("gd", _vp), ("gb", _vp), ("gC", _vp), ("gh0", _vp), ("glogits", _vp)]
 
 
+class ConvArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("silu", ctypes.c_int32),
+                ("batch", _i64), ("channels", _i64), ("length", _i64), ("width", _i64),
+                ("x", _vp), ("x8", _vp), ("x8_scale", _vp), ("w", _vp), ("bias", _vp), ("init", _vp),
+                ("layout", ctypes.POINTER(Layout))]
+
+
+class ConvFwdOut(ctypes.Structure):
+    _fields_ = [("y", _vp), ("last", _vp), ("x8", _vp), ("x8_scale", _vp)]
+
+
+class ConvGrads(ctypes.Structure):
+    _fields_ = [("gx", _vp), ("gw", _vp), ("gbias", _vp), ("ginit", _vp)]
+
+
+class Ckpt8Args(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", _i64), ("channels", _i64), ("length", _i64),
+                ("layout", ctypes.POINTER(Layout))]
+
+
+class TokensConvArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("silu", ctypes.c_int32),
+                ("tokens", _i64), ("channels", _i64), ("width", _i64), ("sequences", _i64), ("slots", _i64),
+                ("x", _vp), ("w", _vp), ("bias", _vp), ("seq_start", _vp), ("slot", _vp), ("fresh", _vp),
+                ("pool", _vp), ("y", _vp), ("x_stride", _i64), ("y_stride", _i64), ("pool_stride", _i64)]
+
+
+class TokensScanArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("delta_softplus", ctypes.c_int32),
+                ("tokens", _i64), ("channels", _i64), ("state", _i64), ("sequences", _i64), ("slots", _i64),
+                ("delta", _vp), ("x", _vp), ("A", _vp), ("Bm", _vp), ("C", _vp), ("delta_bias", _vp), ("skip", _vp),
+                ("z", _vp), ("seq_start", _vp), ("slot", _vp), ("fresh", _vp), ("pool", _vp), ("y", _vp),
+                ("delta_stride", _i64), ("x_stride", _i64), ("Bm_stride", _i64), ("C_stride", _i64),
+                ("z_stride", _i64), ("y_stride", _i64), ("pool_stride", _i64)]
+
+
 _lib = None
 
 
@@ -129,6 +167,13 @@ def lib():
         L.pd_scan_fwd.argtypes = [ctypes.POINTER(PDArgs), ctypes.POINTER(PDFwdOut), _vp, ctypes.c_size_t, _vp]
         L.pd_scan_bwd.argtypes = [ctypes.POINTER(PDArgs), ctypes.POINTER(PDBwdIn), ctypes.POINTER(PDGrads),
                                   _vp, ctypes.c_size_t, _vp]
+        L.ssm_conv_fwd.argtypes = [ctypes.POINTER(ConvArgs), ctypes.POINTER(ConvFwdOut), _vp]
+        L.ssm_conv_bwd.argtypes = [ctypes.POINTER(ConvArgs), _vp, _vp, ctypes.POINTER(ConvGrads), _vp,
+                                   ctypes.c_size_t, _vp]
+        L.ssm_ckpt8_pack.argtypes = [ctypes.POINTER(Ckpt8Args), _vp, _vp, _vp, _vp]
+        L.ssm_ckpt8_unpack.argtypes = [ctypes.POINTER(Ckpt8Args), _vp, _vp, _vp, _vp]
+        L.ssm_tokens_conv.argtypes = [ctypes.POINTER(TokensConvArgs), _vp]
+        L.ssm_tokens_scan.argtypes = [ctypes.POINTER(TokensScanArgs), _vp, ctypes.c_size_t, _vp]
         L.ssm_status_string.restype = ctypes.c_char_p
         L.ssm_status_string.argtypes = [ctypes.c_int]
         L.ssm_last_error_detail.restype = ctypes.c_char_p
@@ -621,4 +666,280 @@ def pd_scan_bwd(*, gy, gh_last=None, ckpt=None, want=("gd", "gb", "gC", "gh0"), 
     i = PDBwdIn(gy=_ptr(gy), gh_last=_ptr(gh_last), ckpt=_ptr(ckpt), ste_logits=_ptr(ste_logits), tau=float(tau))
     ws, nws = _workspace(SSM_OP_PD_BWD, ctypes.byref(args), dev)
     _check(lib().pd_scan_bwd(ctypes.byref(args), ctypes.byref(i), ctypes.byref(g), _ptr(ws), nws, _stream(dev)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# short causal convolution, 8-bit activation checkpoints
+# ---------------------------------------------------------------------------
+_STREAM = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
+
+
+def _stream_code(dtype, name):
+    if dtype not in _STREAM:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return _STREAM[dtype]
+
+
+class _on_device:
+    """The library launches on the current device: makes the tensors' device current for a call."""
+
+    def __init__(self, dev):
+        _on_gpu(dev)
+        self.dev, self.other = dev.index, None
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if self.dev is not None and self.dev != cur:
+            self.other = cur
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            torch.cuda.set_device(self.other)
+
+
+def _need_ckpt8(ckpt8, dev=None, shape=None):
+    x8, scale = ckpt8
+    _need(x8, "x8", torch.int8, shape, dev)
+    if x8.dim() != 3:
+        raise ValueError(f"x8 has shape {tuple(x8.shape)}; expected (B, D, L)")
+    Bsz, D, L = x8.shape
+    _need(scale, "x8_scale", torch.float32, (Bsz, D, n_chunks(L, SSM_CKPT8_BLOCK)), x8.device)
+    return x8, scale
+
+
+def _conv_args(x, ckpt8, w, bias, init, silu, dtype):
+    """The input is ``x`` (B, D, L), a strided view or dense, or ``ckpt8`` = (x8, x8_scale)."""
+    if (x is None) == (ckpt8 is None):
+        raise ValueError("one of x and ckpt8 is the input")
+    x8 = scale = None
+    if x is not None:
+        _need(x, "x", view=True)
+        shape, dev, st = x.shape, x.device, x.dtype
+        if dtype is not None and dtype != st:
+            raise TypeError(f"x has dtype {st}, expected {dtype}")
+    else:
+        x8, scale = _need_ckpt8(ckpt8)
+        shape, dev, st = x8.shape, x8.device, dtype
+        if st is None:
+            raise TypeError("dtype is required with ckpt8")
+    code = _stream_code(st, "x")
+    if len(shape) != 3:
+        raise ValueError(f"x has shape {tuple(shape)}; expected (B, D, L)")
+    Bsz, D, L = shape
+    _need(w, "w", torch.float32, None, dev)
+    if w is None or w.dim() != 2 or w.shape[0] != D:
+        raise ValueError(f"w must be (D, W) with D={D}")
+    W = w.shape[1]
+    _need(bias, "bias", torch.float32, (D,), dev)
+    _need(init, "init", st, (Bsz, D, W - 1), dev)
+    vw = _Views()
+    if x is not None:
+        vw.set(V_X, x.stride(), _dense_strides(shape))
+    args = ConvArgs(dtype=code, silu=int(bool(silu)), batch=Bsz, channels=D, length=L, width=W, x=_ptr(x), x8=_ptr(x8),
+                    x8_scale=_ptr(scale), w=_ptr(w), bias=_ptr(bias), init=_ptr(init))
+    args._views = vw
+    return args, (Bsz, D, L, W), st, dev
+
+
+def conv_fwd(*, x=None, ckpt8=None, w, bias=None, init=None, silu=False, want_y=True, want_last=False,
+             want_ckpt8=False, dtype=None, out=None):
+    """Short causal depthwise convolution, y = act(bias + sum_k w[:, k] e[..., t + k]) with e = (init | x).
+
+    ``x`` (B, D, L) float32 or bfloat16, any batch and channel stride; ``w`` (D, W) float32, W in 2..4, its
+    last column for the step itself; ``init`` (B, D, W-1) the inputs before step 0.  Returns a dict with y,
+    last (the last W-1 inputs, what a following segment takes as ``init``) and x8, x8_scale (the 8-bit
+    checkpoint of x), those requested.  ``ckpt8`` = (x8, x8_scale) takes the place of x, with ``dtype`` that
+    of y: the convolution's output again from its checkpoint."""
+    args, (Bsz, D, L, W), st, dev = _conv_args(x, ckpt8, w, bias, init, silu, dtype)
+    out = dict(out or {})
+    if want_ckpt8 or out.get("x8") is not None or out.get("x8_scale") is not None:
+        if x is None:
+            raise ValueError("a checkpoint is written from x")
+        _out(out, "x8", (Bsz, D, L), torch.int8, dev)
+        _out(out, "x8_scale", (Bsz, D, n_chunks(L, SSM_CKPT8_BLOCK)), torch.float32, dev)
+    if want_y or out.get("y") is not None:
+        _out(out, "y", (Bsz, D, L), st, dev, view=True)
+        args._views.set(V_Y, out["y"].stride(), _dense_strides((Bsz, D, L)))
+    if want_last or out.get("last") is not None:
+        _out(out, "last", (Bsz, D, W - 1), st, dev)
+    args.layout = args._views.ptr()
+    o = ConvFwdOut(y=_ptr(out.get("y")), last=_ptr(out.get("last")), x8=_ptr(out.get("x8")),
+                   x8_scale=_ptr(out.get("x8_scale")))
+    with _on_device(dev):
+        _check(lib().ssm_conv_fwd(ctypes.byref(args), ctypes.byref(o), _stream(dev)))
+    return out
+
+
+def conv_bwd(*, gy, x=None, ckpt8=None, w, bias=None, init=None, silu=False, glast=None,
+             want=("gx", "gw", "gbias", "ginit"), out=None):
+    """Gradients of <gy, y> + <glast, last> of ``conv_fwd``, from its input or its input's 8-bit checkpoint
+    (then those of the values the checkpoint stands for).  Returns a dict of the gradients named in ``want``."""
+    if gy is None:
+        raise ValueError("gy is required")
+    _need(gy, "gy", view=True)
+    args, (Bsz, D, L, W), st, dev = _conv_args(x, ckpt8, w, bias, init, silu, gy.dtype)
+    _need(gy, "gy", st, (Bsz, D, L), dev, view=True)
+    _need(glast, "glast", st, (Bsz, D, W - 1), dev)
+    args._views.set(V_GY, gy.stride(), _dense_strides((Bsz, D, L)))
+    shapes = {"gx": ((Bsz, D, L), st), "gw": ((D, W), torch.float32), "gbias": ((D,), torch.float32),
+              "ginit": ((Bsz, D, W - 1), st)}
+    out = dict(out or {})
+    for k in [k for k in shapes if k in want or out.get(k) is not None] + [k for k in (*want, *out) if k not in shapes]:
+        if k not in shapes:
+            raise ValueError(f"unknown gradient {k}")
+        _out(out, k, *shapes[k], dev, view=k == "gx")
+    if out.get("gx") is not None:
+        args._views.set(V_GX, out["gx"].stride(), _dense_strides((Bsz, D, L)))
+    args.layout = args._views.ptr()
+    g = ConvGrads(**{f[0]: _ptr(out.get(f[0])) for f in ConvGrads._fields_})
+    with _on_device(dev):
+        ws, nws = _workspace(SSM_OP_CONV_BWD, ctypes.byref(args), dev)
+        _check(lib().ssm_conv_bwd(ctypes.byref(args), _ptr(gy), _ptr(glast), ctypes.byref(g), _ptr(ws), nws,
+                                  _stream(dev)))
+    return out
+
+
+def ckpt8_pack(x, *, out=None):
+    """The 8-bit checkpoint of a stream x (B, D, L): a dict with x8 (B, D, L) int8 and x8_scale
+    (B, D, ceil(L / 64)) float32, one scale for every 64 steps of a row."""
+    _need(x, "x", view=True)
+    code = _stream_code(x.dtype, "x")
+    if x.dim() != 3:
+        raise ValueError(f"x has shape {tuple(x.shape)}; expected (B, D, L)")
+    Bsz, D, L = x.shape
+    out = dict(out or {})
+    _out(out, "x8", (Bsz, D, L), torch.int8, x.device)
+    _out(out, "x8_scale", (Bsz, D, n_chunks(L, SSM_CKPT8_BLOCK)), torch.float32, x.device)
+    vw = _Views()
+    vw.set(V_X, x.stride(), _dense_strides(x.shape))
+    args = Ckpt8Args(dtype=code, batch=Bsz, channels=D, length=L, layout=vw.ptr())
+    with _on_device(x.device):
+        _check(lib().ssm_ckpt8_pack(ctypes.byref(args), _ptr(x), _ptr(out["x8"]), _ptr(out["x8_scale"]),
+                                    _stream(x.device)))
+    return out
+
+
+def ckpt8_unpack(x8, x8_scale, *, dtype=torch.float32, out=None):
+    """The stream (B, D, L) of ``dtype`` that an 8-bit checkpoint stands for (what ``scan_bwd`` and other
+    readers of whole streams take)."""
+    x8, x8_scale = _need_ckpt8((x8, x8_scale))
+    code = _stream_code(dtype, "dtype")
+    Bsz, D, L = x8.shape
+    y = {"y": out}
+    _out(y, "y", (Bsz, D, L), dtype, x8.device, view=True)
+    y = y["y"]
+    vw = _Views()
+    vw.set(V_Y, y.stride(), _dense_strides(y.shape))
+    args = Ckpt8Args(dtype=code, batch=Bsz, channels=D, length=L, layout=vw.ptr())
+    with _on_device(x8.device):
+        _check(lib().ssm_ckpt8_unpack(ctypes.byref(args), _ptr(x8), _ptr(x8_scale), _ptr(y), _stream(x8.device)))
+    return y
+
+
+# ---------------------------------------------------------------------------
+# packed rows: serving forms with pools of states
+# ---------------------------------------------------------------------------
+def _rows(t, name, dtype, shape, dev):
+    """A matrix of rows; its row stride (rows contiguous, any stride from one to the next)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    _need(t, name, dtype, shape, dev, view=True)
+    return t.stride(0)
+
+
+def _sequences(T, pool, inner, pool_dtype, dev, seq_start, slot, fresh):
+    """Checks of the sequences of a call; (sequences, slots, pool stride)."""
+    if not isinstance(pool, torch.Tensor) or pool.dim() != 3 or tuple(pool.shape[1:]) != inner:
+        raise ValueError(f"pool must be (slots, {inner[0]}, {inner[1]})")
+    if pool.dtype != pool_dtype:
+        raise TypeError(f"pool has dtype {pool.dtype}, expected {pool_dtype}")
+    if pool.device != dev:
+        raise ValueError(f"pool is on {pool.device}, expected {dev}")
+    slots = pool.shape[0]
+    if pool.numel() and (pool.stride(2) != 1 and inner[1] > 1 or pool.stride(1) != inner[1] and inner[0] > 1):
+        raise ValueError("pool: every slot must be contiguous")
+    if seq_start is not None:
+        if not isinstance(seq_start, torch.Tensor) or seq_start.dim() != 1 or seq_start.shape[0] < 1:
+            raise ValueError("seq_start must be (sequences + 1,)")
+        S = seq_start.shape[0] - 1
+        _need(seq_start, "seq_start", torch.int32, None, dev)
+    else:
+        S = T
+    _need(slot, "slot", torch.int32, (S,), dev)
+    if fresh is not None and fresh.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"fresh has dtype {fresh.dtype}, expected torch.bool or torch.uint8")
+    _need(fresh, "fresh", None, (S,), dev)
+    return S, slots, pool.stride(0)
+
+
+def tokens_conv(*, x, w, bias=None, silu=False, pool, seq_start=None, slot=None, fresh=None, out=None):
+    """The convolution of ``conv_fwd`` over the packed rows x (T, D) of a batch of sequences.
+
+    Sequence s owns rows seq_start[s] .. seq_start[s+1]-1 (``seq_start`` (S+1,) int32 on the device; None:
+    one row a sequence).  ``pool`` (slots, D, W-1) holds each sequence's last W-1 inputs; sequence s begins
+    with slot[s] (zeros where ``fresh``) and leaves its own there, in place.  A slot of -1 marks an empty
+    place of the batch, which leaves its row as it was.  Returns a dict with y (T, D)."""
+    if x is None:
+        raise ValueError("x is required")
+    _need(x, "x", view=True)
+    code = _stream_code(x.dtype, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}; expected (T, D)")
+    T, D = x.shape
+    dev = x.device
+    _need(w, "w", torch.float32, None, dev)
+    if w is None or w.dim() != 2 or w.shape[0] != D:
+        raise ValueError(f"w must be (D, W) with D={D}")
+    W = w.shape[1]
+    _need(bias, "bias", torch.float32, (D,), dev)
+    S, slots, spool = _sequences(T, pool, (D, W - 1), x.dtype, dev, seq_start, slot, fresh)
+    out = dict(out or {})
+    y = _out(out, "y", (T, D), x.dtype, dev, view=True)
+    args = TokensConvArgs(code, int(bool(silu)), T, D, W, S, slots, x.data_ptr(), w.data_ptr(), _ptr(bias),
+                          _ptr(seq_start), _ptr(slot), _ptr(fresh), pool.data_ptr(), y.data_ptr(), x.stride(0),
+                          y.stride(0), spool)
+    with _on_device(dev):
+        _check(lib().ssm_tokens_conv(ctypes.byref(args), _stream(dev)))
+    return out
+
+
+def tokens_scan(*, delta, x, A, Bm, C, skip=None, z=None, delta_bias=None, delta_softplus=False, pool,
+                seq_start=None, slot=None, fresh=None, out=None):
+    """The selective scan over the packed rows of a batch of sequences, with its layer's skip and gate:
+    y = (C . h + skip * x) * z * sigmoid(z).
+
+    ``delta``, ``x``, ``z`` (T, D) and ``Bm``, ``C`` (T, N) may be slices of wider rows; ``pool``
+    (slots, D, N) float32 holds the states, in place; ``seq_start``, ``slot`` and ``fresh`` as in
+    ``tokens_conv``; ``delta_bias`` and ``delta_softplus`` as in ``scan_fwd``.  Returns a dict with y (T, D)."""
+    if x is None:
+        raise ValueError("x is required")
+    _need(x, "x", view=True)
+    st = x.dtype
+    code = _stream_code(st, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}; expected (T, D)")
+    T, D = x.shape
+    dev = x.device
+    _need(A, "A", torch.float32, None, dev)
+    if A is None or A.dim() != 2 or A.shape[0] != D:
+        raise ValueError(f"A must be (D, N) with D={D}")
+    N = A.shape[1]
+    sdelta = _rows(delta, "delta", st, (T, D), dev)
+    sB = _rows(Bm, "Bm", st, (T, N), dev)
+    sC = _rows(C, "C", st, (T, N), dev)
+    sz = _rows(z, "z", st, (T, D), dev) if z is not None else 0
+    _need(skip, "skip", torch.float32, (D,), dev)
+    _need(delta_bias, "delta_bias", torch.float32, (D,), dev)
+    S, slots, spool = _sequences(T, pool, (D, N), torch.float32, dev, seq_start, slot, fresh)
+    out = dict(out or {})
+    y = _out(out, "y", (T, D), st, dev, view=True)
+    args = TokensScanArgs(code, int(bool(delta_softplus)), T, D, N, S, slots, delta.data_ptr(), x.data_ptr(),
+                          A.data_ptr(), Bm.data_ptr(), C.data_ptr(), _ptr(delta_bias), _ptr(skip), _ptr(z),
+                          _ptr(seq_start), _ptr(slot), _ptr(fresh), pool.data_ptr(), y.data_ptr(), sdelta,
+                          x.stride(0), sB, sC, sz, y.stride(0), spool)
+    with _on_device(dev):
+        ws, nws = _workspace(SSM_OP_TOKENS_SCAN, ctypes.byref(args), dev) if seq_start is not None else (None, 0)
+        _check(lib().ssm_tokens_scan(ctypes.byref(args), _ptr(ws), nws, _stream(dev)))
     return out

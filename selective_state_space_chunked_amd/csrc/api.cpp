@@ -1017,6 +1017,7 @@ int sens_rows_impl(const ssm_scan_args* a, int64_t t0, int32_t rows, void* s, vo
 }  // namespace
 
 #include "api_modes.inc"
+#include "api_layer.inc"
 
 // ===========================================================================
 // allocation-free forward (ssm_scan_fwd_noalloc): the scratch memory the
@@ -1086,6 +1087,12 @@ int ssm_workspace_bytes(int op, const void* args, size_t* out_bytes) {
             return sens_rows_impl((const ssm_scan_args*)args, 0, 0, nullptr, nullptr, 0, nullptr, out_bytes);
         case SSM_OP_COMPLEX_RTRL:
             return rtrl_impl((const ssm_scan_args*)args, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, nullptr, out_bytes);
+        case SSM_OP_CONV_FWD: return conv_fwd_impl((const ssm_conv_args*)args, nullptr, nullptr, out_bytes);
+        case SSM_OP_CONV_BWD:
+            return conv_bwd_impl((const ssm_conv_args*)args, nullptr, nullptr, nullptr, nullptr, 0, nullptr, out_bytes);
+        case SSM_OP_TOKENS_CONV: return tokens_conv_impl((const ssm_tokens_conv_args*)args, nullptr, out_bytes);
+        case SSM_OP_TOKENS_SCAN:
+            return tokens_scan_impl((const ssm_tokens_scan_args*)args, nullptr, 0, nullptr, out_bytes);
         default: return fail(SSM_ERR_UNSUPPORTED, "unknown op %d", op);
     }
 }
@@ -1131,6 +1138,26 @@ int pd_scan_fwd(const pd_scan_args* args, const pd_scan_fwd_out* out, void* ws, 
 int pd_scan_bwd(const pd_scan_args* args, const pd_scan_bwd_in* in, const pd_scan_grads* grads, void* ws,
                 size_t ws_bytes, void* stream) {
     return pd_bwd_impl(args, in, grads, ws, ws_bytes, (hipStream_t)stream, nullptr);
+}
+
+int ssm_conv_fwd(const ssm_conv_args* args, const ssm_conv_fwd_out* out, void* stream) {
+    return conv_fwd_impl(args, out, (hipStream_t)stream, nullptr);
+}
+int ssm_conv_bwd(const ssm_conv_args* args, const void* gy, const void* glast, const ssm_conv_grads* grads, void* ws,
+                 size_t ws_bytes, void* stream) {
+    return conv_bwd_impl(args, gy, glast, grads, ws, ws_bytes, (hipStream_t)stream, nullptr);
+}
+int ssm_ckpt8_pack(const ssm_ckpt8_args* args, const void* x, int8_t* x8, float* x8_scale, void* stream) {
+    return ckpt8_impl(args, x, nullptr, nullptr, x8, x8_scale, nullptr, true, (hipStream_t)stream);
+}
+int ssm_ckpt8_unpack(const ssm_ckpt8_args* args, const int8_t* x8, const float* x8_scale, void* y, void* stream) {
+    return ckpt8_impl(args, nullptr, x8, x8_scale, nullptr, nullptr, y, false, (hipStream_t)stream);
+}
+int ssm_tokens_conv(const ssm_tokens_conv_args* args, void* stream) {
+    return tokens_conv_impl(args, (hipStream_t)stream, nullptr);
+}
+int ssm_tokens_scan(const ssm_tokens_scan_args* args, void* ws, size_t ws_bytes, void* stream) {
+    return tokens_scan_impl(args, ws, ws_bytes, (hipStream_t)stream, nullptr);
 }
 
 int ssm_profile_begin(int max_launches) {

@@ -40,4 +40,19 @@ hipError_t launch_zero_bytes(void* dst, size_t bytes, hipStream_t st) {
     return hipGetLastError();
 }
 
+__global__ __launch_bounds__(256) void copy_u16_kernel(uint16_t* __restrict__ dst, const uint16_t* __restrict__ src,
+                                                       size_t n) {
+    const size_t stride = (size_t)gridDim.x * blockDim.x;
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) dst[i] = src[i];
+}
+
+hipError_t launch_copy_bytes(void* dst, const void* src, size_t bytes, hipStream_t st) {
+    if (!dst || !src || bytes == 0) return hipSuccess;
+    if (bytes % 2) return hipErrorInvalidValue;
+    const size_t n = bytes / 2;
+    const size_t blocks = std::min<size_t>((n + 255) / 256, 4096);
+    copy_u16_kernel<<<(unsigned)blocks, 256, 0, st>>>((uint16_t*)dst, (const uint16_t*)src, n);
+    return hipGetLastError();
+}
+
 }  // namespace ssm

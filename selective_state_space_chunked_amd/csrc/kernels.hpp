@@ -99,6 +99,7 @@ struct SensRowsParams {
 // dst[0..n) = src (or 0 when src is NULL); nothing when dst is NULL or n is 0
 hipError_t launch_fill_copy_f32(float* dst, const float* src, size_t n, hipStream_t st);
 hipError_t launch_zero_bytes(void* dst, size_t bytes, hipStream_t st);  // bytes even
+hipError_t launch_copy_bytes(void* dst, const void* src, size_t bytes, hipStream_t st);  // bytes even
 
 hipError_t launch_sel_fwd(const SelFwdParams& p, int dtype, int kpl, bool summary, hipStream_t st);
 hipError_t launch_sel_bwd(const SelBwdParams& p, int dtype, int kpl, bool summary, hipStream_t st);
@@ -274,5 +275,49 @@ hipError_t launch_pd_combine_rev(const PDParams& p, hipStream_t st);
 // instruction class `kind` for iters * 8 steps; sink holds waves * 64 floats.
 hipError_t launch_roof(int kind, int chains, int waves, int iters, float* sink, hipStream_t st);
 double roof_instrs_per_lane(int kind, int chains, int iters);
+
+
+// ------------------ short causal convolution, 8-bit checkpoints ------------
+constexpr int kConvRun = 8;     // consecutive steps of one lane
+constexpr int kCkptBlock = 64;  // steps that share a scale
+struct ConvParams {
+    const void* x; const int8_t* x8; const float* x8_scale;
+    const float* w; const float* bias; const void* init;
+    const void* gy; const void* glast;
+    void* y; void* last; int8_t* o8; float* o8_scale;   // forward outputs (o8: the checkpoint)
+    void* gx; void* ginit; float* gw; float* gbias;     // backward outputs
+    float* part;                     // (parts, D, W + 1) partial sums of gw and gbias, parts > 1
+    int64_t sx[2], sy[2], sgy[2], sgx[2];   // batch, channel strides (steps contiguous)
+    int B, D, L, W, silu, nrun, nblk;
+    int parts, per_part;             // backward: items (batch row, run) of a channel per workgroup
+    int vx, vy, vgy, vgx;            // 16-byte accesses of each stream
+    int v8;                          // 8-byte accesses of the 8-bit checkpoint
+};
+hipError_t launch_conv_fwd(const ConvParams& p, int dtype, hipStream_t st);
+hipError_t launch_conv_bwd(const ConvParams& p, int dtype, hipStream_t st);
+hipError_t launch_conv_reduce(const ConvParams& p, hipStream_t st);
+hipError_t launch_ckpt8_unpack(const ConvParams& p, int dtype, hipStream_t st);
+
+// ------------------------------- packed rows --------------------------------
+struct Sequences {
+    const int32_t* start; const int32_t* slot; const uint8_t* fresh;
+    int T, S, slots;
+};
+struct TokConvParams {
+    const void* x; const float* w; const float* bias; void* pool; void* y;
+    Sequences q;
+    int64_t sx, sy, spool;
+    int D, W, silu, vec;
+};
+struct TokScanParams {
+    const void* delta; const void* x; const float* A; const void* Bm; const void* C;
+    const void* z; const float* skip; float* pool; void* y;
+    StepXform stepf;
+    Sequences q;
+    int64_t sdelta, sx, sB, sC, sz, sy, spool;
+    int D, N;
+};
+hipError_t launch_tok_conv(const TokConvParams& p, int dtype, hipStream_t st);
+hipError_t launch_tok_scan(const TokScanParams& p, int dtype, hipStream_t st);
 
 }  // namespace ssm
