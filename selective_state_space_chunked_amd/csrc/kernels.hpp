@@ -316,8 +316,20 @@ struct TokScanParams {
     Sequences q;
     int64_t sdelta, sx, sB, sC, sz, sy, spool;
     int D, N;
+    int vec;                         // steps: 16-byte accesses of the states and of A
+    // prompts: ranges of `rows` rows (the last may be shorter); workspace
+    int rows, nrange;
+    float* bc;                       // (T, 2N) B_t and C_t in fp32
+    float *h0, *hsum;                // (nrange - 1, N, D) of the sequence that crosses a range's end: its first
+                                     // state if it begins there, and its state at the end of the range
+    float* dsum;                     // (nrange - 1, D) sum of its step sizes in the range
 };
+// rows a range covers at least, and the waves that are enough to fill the GPU
+constexpr int kTokRowsMin = 32;
+constexpr int kTokWaves = 2048;
 hipError_t launch_tok_conv(const TokConvParams& p, int dtype, hipStream_t st);
-hipError_t launch_tok_scan(const TokScanParams& p, int dtype, hipStream_t st);
+hipError_t launch_tok_bc(const TokScanParams& p, int dtype, hipStream_t st);
+hipError_t launch_tok_scan(const TokScanParams& p, int dtype, bool sum, hipStream_t st);
+hipError_t launch_tok_step(const TokScanParams& p, int dtype, hipStream_t st);
 
 }  // namespace ssm

@@ -1,84 +1,12 @@
-// The short causal convolution and the selective scan over packed rows: the
-// tokens of all sequences of a call are the rows of one matrix, lanes run along
-// the channels, and each sequence's state comes from and returns to its slot of
-// a pool.
+// The short causal convolution over packed rows: the tokens of all sequences of
+// a call are the rows of one matrix, lanes run along the channels, and each
+// sequence's last W-1 inputs come from and return to its slot of a pool.
 #include <algorithm>
 
-#include "common.hpp"
-#include "kernels.hpp"
+#include "tokens.hpp"
 
 namespace ssm {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float sigmoid_f(float v) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
-}
-__device__ __forceinline__ float softplus_t(float v) { return v > 20.0f ? v : log1pf(expf(v)); }
-
-// The last sequence whose first row is at or before row t: -1 before the first
-// one, S from the end of the last one on.  Called by whole waves with one t;
-// each round the 64 lanes probe 64 entries of the ascending list.
-__device__ __forceinline__ int find_seq(const int32_t* start, int S, int t) {
-    int lo = 0, hi = S + 1;   // entries before lo are <= t, from hi on > t
-    const int lane = lane_id();
-    while (hi - lo > 64) {
-        const int step = (hi - lo + 63) / 64;
-        const int i = lo + lane * step;
-        const int c = __popcll(__ballot(i < hi && start[i < hi ? i : lo] <= t));
-        if (c == 0) return lo - 1;
-        const int top = lo + c * step;
-        lo += (c - 1) * step;
-        hi = min(hi, top);
-    }
-    const int i = lo + lane;
-    return lo + __popcll(__ballot(i < hi && start[i < hi ? i : lo] <= t)) - 1;
-}
-
-// The slot of sequence s, or -1 for an empty place: a slot outside the pool, or
-// one that an earlier sequence of the call has.  Called by whole waves with one s.
-__device__ __forceinline__ int slot_of(const Sequences& q, int s) {
-    if (!q.slot) return s < q.slots ? s : -1;
-    const int v = q.slot[s];
-    if (v < 0 || v >= q.slots) return -1;
-    bool taken = false;
-    for (int i = lane_id(); i < s; i += 64) taken |= q.slot[i] == v;
-    return __ballot(taken) ? -1 : v;
-}
-
-// V consecutive elements: one 16-byte access (V elements of T are 16 bytes), or one element
-template <typename T, int V>
-__device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
-    if (V == 1) {
-        v[0] = to_f32(p[0]);
-    } else if (sizeof(T) == 4) {
-        const float4 w = *reinterpret_cast<const float4*>(p);
-        v[0] = w.x; v[1 % V] = w.y; v[2 % V] = w.z; v[3 % V] = w.w;
-    } else {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[(2 * e) % V] = __uint_as_float(ws[e] << 16);
-            v[(2 * e + 1) % V] = __uint_as_float(ws[e] & 0xffff0000u);
-        }
-    }
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
-    if (V == 1) {
-        p[0] = from_f32<T>(v[0]);
-    } else if (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1 % V], v[2 % V], v[3 % V]);
-    } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[e] = (uint32_t)from_f32<bf16_t>(v[(2 * e) % V]) | ((uint32_t)from_f32<bf16_t>(v[(2 * e + 1) % V]) << 16);
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
 
 // ---------------------------------------------------------------------------
 // convolution
@@ -244,77 +172,12 @@ hipError_t tok_conv_w(const TokConvParams& p, hipStream_t st) {
     return hipGetLastError();
 }
 
-// ---------------------------------------------------------------------------
-// selective scan: a lane walks one channel of one sequence, its states in registers
-// ---------------------------------------------------------------------------
-template <typename T>
-__global__ __launch_bounds__(64) void tok_scan_kernel(TokScanParams p, int cblocks) {
-    constexpr int NM = 16;
-    const int cb = blockIdx.x % cblocks, s = blockIdx.x / cblocks;
-    int st = s, en = s + 1;
-    if (p.q.start) {
-        st = p.q.start[s];
-        en = min(p.q.start[s + 1], p.q.T);
-    }
-    if (st < 0 || st >= en) return;
-    const int slot = slot_of(p.q, s);
-    if (slot < 0) return;
-    const int d = cb * 64 + lane_id();
-    if (d >= p.D) return;
-    const int N = p.N;
-    float* pool = p.pool + slot * p.spool + (int64_t)d * N;
-    float h[NM], a[NM];
-    const bool fresh = p.q.fresh && p.q.fresh[s];
-#pragma unroll
-    for (int n = 0; n < NM; ++n) {
-        h[n] = n < N && !fresh ? pool[n] : 0.0f;
-        a[n] = n < N ? p.A[(int64_t)d * N + n] * kLog2e : 0.0f;
-    }
-    const float bias = p.stepf.bias ? p.stepf.bias[d] : 0.0f, skip = p.skip ? p.skip[d] : 0.0f;
-    for (int t = st; t < en; ++t) {
-        float dl = to_f32(((const T*)p.delta)[t * p.sdelta + d]) + bias;
-        if (p.stepf.softplus) dl = softplus_t(dl);
-        const float x = to_f32(((const T*)p.x)[t * p.sx + d]);
-        const T* B = (const T*)p.Bm + t * p.sB;
-        const T* C = (const T*)p.C + t * p.sC;
-        const float u = dl * x;
-        float y = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NM; ++n) {
-            if (n < N) {
-                h[n] = fmaf(__builtin_amdgcn_exp2f(a[n] * dl), h[n], u * to_f32(B[n]));
-                y = fmaf(h[n], to_f32(C[n]), y);
-            }
-        }
-        if (p.skip) y = fmaf(skip, x, y);
-        if (p.z) {
-            const float z = to_f32(((const T*)p.z)[t * p.sz + d]);
-            y *= z * sigmoid_f(z);
-        }
-        ((T*)p.y)[t * p.sy + d] = from_f32<T>(y);
-    }
-#pragma unroll
-    for (int n = 0; n < NM; ++n)
-        if (n < N) pool[n] = h[n];
-}
-
-template <typename T>
-hipError_t tok_scan_t(const TokScanParams& p, hipStream_t st) {
-    const int64_t cblocks = (p.D + 63) / 64, blocks = cblocks * p.q.S;
-    if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
-    tok_scan_kernel<T><<<(unsigned)blocks, 64, 0, st>>>(p, (int)cblocks);
-    return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_tok_conv(const TokConvParams& p, int dtype, hipStream_t st) {
     if (dtype == 1)
         return p.W == 2 ? tok_conv_w<bf16_t, 2>(p, st) : p.W == 3 ? tok_conv_w<bf16_t, 3>(p, st) : tok_conv_w<bf16_t, 4>(p, st);
     return p.W == 2 ? tok_conv_w<float, 2>(p, st) : p.W == 3 ? tok_conv_w<float, 3>(p, st) : tok_conv_w<float, 4>(p, st);
-}
-hipError_t launch_tok_scan(const TokScanParams& p, int dtype, hipStream_t st) {
-    return dtype == 1 ? tok_scan_t<bf16_t>(p, st) : tok_scan_t<float>(p, st);
 }
 
 }  // namespace ssm
