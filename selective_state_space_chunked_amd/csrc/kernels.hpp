@@ -319,17 +319,19 @@ struct TokScanParams {
     int vec;                         // steps: 16-byte accesses of the states and of A
     // prompts: ranges of `rows` rows (the last may be shorter); workspace
     int rows, nrange;
-    float* bc;                       // (T, 2N) B_t and C_t in fp32
     float *h0, *hsum;                // (nrange - 1, N, D) of the sequence that crosses a range's end: its first
                                      // state if it begins there, and its state at the end of the range
     float* dsum;                     // (nrange - 1, D) sum of its step sizes in the range
+    int* through;                    // (nrange - 1) whether it runs through the whole range
 };
-// rows a range covers at least, and the waves that are enough to fill the GPU
+// rows a range covers at least, and the waves the ranges are made for: the second pass's registers
+// allow four on each of the 1024 SIMDs.  Measured at 8192 rows x 2048 channels (both passes and the
+// states between, us): 1024 waves 226, 2048 161, 3072 155, 4096 149, 6144 154.
 constexpr int kTokRowsMin = 32;
-constexpr int kTokWaves = 2048;
+constexpr int kTokWaves = 4096;
 hipError_t launch_tok_conv(const TokConvParams& p, int dtype, hipStream_t st);
-hipError_t launch_tok_bc(const TokScanParams& p, int dtype, hipStream_t st);
 hipError_t launch_tok_scan(const TokScanParams& p, int dtype, bool sum, hipStream_t st);
+hipError_t launch_tok_join(const TokScanParams& p, hipStream_t st);
 hipError_t launch_tok_step(const TokScanParams& p, int dtype, hipStream_t st);
 
 }  // namespace ssm

@@ -14,13 +14,15 @@ __device__ __forceinline__ float sigmoid_f(float v) {
 }
 // log(1 + e^v) from the hardware exp2 and log2 (accurate to an ulp or two where
 // the library function takes several times the instructions; it runs once a
-// channel and row).  With e = e^v and w = 1 + e rounded, log(w) + (e - (w - 1)) / w
-// gives back what the rounding of the sum lost, so small results keep their
-// relative accuracy.  From 20 on it is v (e^-20 is below half an ulp).
+// channel and row).  With e = e^v and w = 1 + e rounded, log(1 + e) is log(w) plus
+// (e - (w - 1)) / w, which the rounding of the sum lost: below w = 2, where it
+// matters against the result, 1 / w may be left out (at most u / 2 of an error
+// of u), above it is below an ulp of log(w).  From 20 on the result is v (e^-20 is
+// below half an ulp).
 __device__ __forceinline__ float softplus_t(float v) {
     const float e = __builtin_amdgcn_exp2f(v * kLog2e);
     const float w = 1.0f + e;
-    const float r = fmaf(__builtin_amdgcn_logf(w), kLn2, (e - (w - 1.0f)) * __builtin_amdgcn_rcpf(w));
+    const float r = fmaf(__builtin_amdgcn_logf(w), kLn2, w < 2.0f ? e - (w - 1.0f) : 0.0f);
     return v > 20.0f ? v : r;
 }
 // float to the stream's type, to nearest even, by the conversion instruction

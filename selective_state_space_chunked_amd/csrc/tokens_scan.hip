@@ -4,17 +4,16 @@
 //
 // Prompts.  A lane holds one channel with its N states; a wave walks 64
 // channels down a range of rows, so the streams are read along the channels as
-// the projections write them, and B_t, C_t are the same for the whole wave: they
-// come as fp32 through the scalar cache and enter the products as scalar
-// operands (one pass turns them into fp32 first).  Per state and row that leaves
-// a multiply and an exp2 for the transition, a multiply and a multiply-add for
-// the state and one multiply-add for y.  Few long sequences do not fill the GPU,
-// so the rows are cut into ranges whatever the sequences' lengths: a first pass
-// leaves, for the sequence that crosses the end of each range, its state there
-// (from zero where it crosses the whole range) and the sum of its step sizes;
-// the second pass composes those of the ranges before it,
+// the projections write them.  B_t, C_t are the same for the whole wave: 16 rows
+// of them at a time go to LDS as fp32 and come back as broadcast 16-byte reads.
+// Per state and row that leaves a multiply and an exp2 for the transition, a
+// multiply and a multiply-add for the state and one multiply-add for y.  Few
+// long sequences do not fill the GPU, so the rows are cut into ranges whatever
+// the sequences' lengths: a first pass leaves, for the sequence that crosses the
+// end of each range, its state there (from zero where it runs through the whole
+// range) and the sum of its step sizes; a small kernel composes them,
 //   h <- exp(A sum delta) h + S,
-// and walks its rows.
+// and the second pass walks every range from the state that enters it.
 //
 // Single tokens.  Bound by the states' traffic: four states a lane, so a wave
 // reads and writes the pool in whole lines.
@@ -25,39 +24,65 @@
 namespace ssm {
 namespace {
 
-typedef __attribute__((address_space(4))) const float sfloat;   // read through the scalar cache
-
-// B_t, C_t of every row in fp32, row t at bc[t * 2N]: B then C
-template <typename T>
-__global__ __launch_bounds__(256) void tok_bc_kernel(TokScanParams p) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int N = p.N;
-    if (i >= (int64_t)p.q.T * 2 * N) return;
-    const int64_t t = i / (2 * N);
-    const int n = (int)(i - t * 2 * N);
-    p.bc[i] = n < N ? to_f32(((const T*)p.Bm)[t * p.sB + n]) : to_f32(((const T*)p.C)[t * p.sC + n - N]);
+// Buffer accesses: the row's address is scalar, a lane adds its byte offset in 32 bits, and offsets
+// from `bytes` on read as zero.  (Kept as flat pointers the compiler spends two vector registers and a
+// 64-bit vector addition on every access.)
+typedef __amdgpu_buffer_rsrc_t buffer_t;
+__device__ __forceinline__ buffer_t buffer_of(const void* row, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(row), 0, bytes, 0x00027000);
 }
+template <typename T> __device__ __forceinline__ T buffer_load(buffer_t r, uint32_t off, uint32_t row = 0);
+template <> __device__ __forceinline__ bf16_t buffer_load<bf16_t>(buffer_t r, uint32_t off, uint32_t row) {
+    return __builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
+}
+template <> __device__ __forceinline__ float buffer_load<float>(buffer_t r, uint32_t off, uint32_t row) {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0));
+}
+__device__ __forceinline__ void buffer_store(buffer_t r, uint32_t off, bf16_t v) {
+    __builtin_amdgcn_raw_buffer_store_b16(v, r, off, 0, 0);
+}
+__device__ __forceinline__ void buffer_store(buffer_t r, uint32_t off, float v) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, off, 0, 0);
+}
+constexpr uint32_t kAll = 0xffffffffu;   // rows of a group: in bounds by their index, no limit wanted
 
+constexpr int kScanWaves = 4;   // of a workgroup: the same rows, neighbouring channels
+constexpr int kTile = 16;   // rows of B and C in LDS
 constexpr int kGrp = 4;   // rows loaded together
 
-template <typename T, int N>
+// FULL: step sizes by softplus, a skip and a gate, as a layer has them; otherwise each as the call says.
+template <typename T, int N, bool FULL>
 struct ScanLane {
-    const T *delta, *x, *z;
+    static constexpr int NQ = N <= 4 ? 4 : N <= 8 ? 8 : 16;   // places of B, then of C, in a row of LDS
+    static constexpr int kLds = kTile * 2 * NQ;               // floats of LDS a wave
+    static constexpr int kStage = kTile * NQ / 64;            // loads of a lane for a tile of B, and of C
+    const T *delta, *x, *z, *B, *C;
     T* y;
-    sfloat* bc;
-    int64_t sdelta, sx, sz, sy;
+    int64_t sdelta, sx, sz, sy, sB, sC;
+    uint32_t bd, bx, bz, by;  // bytes from one row to the next
+    uint32_t row_bytes, db;   // of a row's channels; byte offset of the lane's
+    int rows;
+    uint32_t ob, oc;          // byte offset of the lane's element of B and of C in a tile
+    float *put, *lds;
     float a[N], h[N], bias, skip, dsum;
     int softplus;
     bool skips, gates;
 
-    __device__ __forceinline__ ScanLane(const TokScanParams& p, int d) {
-        delta = (const T*)p.delta + d;
-        x = (const T*)p.x + d;
+    __device__ __forceinline__ ScanLane(const TokScanParams& p, int d, float* lds_) {
+        delta = (const T*)p.delta; x = (const T*)p.x; y = (T*)p.y; B = (const T*)p.Bm; C = (const T*)p.C;
         gates = p.z != nullptr;
-        z = gates ? (const T*)p.z + d : x;   // without a gate: read and not used
-        y = (T*)p.y + d;
-        bc = (sfloat*)(uintptr_t)p.bc;
-        sdelta = p.sdelta; sx = p.sx; sz = gates ? p.sz : p.sx; sy = p.sy;
+        z = gates ? (const T*)p.z : x;   // without a gate: read and not used
+        rows = p.q.T;
+        db = (uint32_t)d * sizeof(T);
+        sdelta = p.sdelta; sx = p.sx; sz = gates ? p.sz : p.sx; sy = p.sy; sB = p.sB; sC = p.sC;
+        bd = (uint32_t)sdelta * sizeof(T); bx = (uint32_t)sx * sizeof(T);
+        row_bytes = (uint32_t)p.D * sizeof(T);
+        bz = (uint32_t)sz * sizeof(T); by = max((uint32_t)sy * (uint32_t)sizeof(T), row_bytes);
+        const int lane = lane_id(), n = lane % NQ, r = lane / NQ;
+        ob = n < N ? (uint32_t)(r * (int)sB + n) * sizeof(T) : 0x7fffffffu;   // places past the states read as 0
+        oc = n < N ? (uint32_t)(r * (int)sC + n) * sizeof(T) : 0x7fffffffu;
+        lds = lds_;
+        put = lds_ + r * 2 * NQ + n;
 #pragma unroll
         for (int n = 0; n < N; ++n) a[n] = p.A[(int64_t)d * N + n] * kLog2e;
         bias = p.stepf.bias ? p.stepf.bias[d] : 0.0f;
@@ -66,60 +91,128 @@ struct ScanLane {
         softplus = p.stepf.softplus;
     }
     template <bool OUT>
-    __device__ __forceinline__ void row(int t, float d, float xv, float zv) {
-        sfloat* r = bc + (int64_t)t * (2 * N);
-        const float u = d * xv;
+    __device__ __forceinline__ void row(int i, buffer_t yg, uint32_t yo, float dl, float xv, float zv) {
+        float b[NQ], c[NQ];
+        const float4* r = reinterpret_cast<const float4*>(lds + i * 2 * NQ);
+#pragma unroll
+        for (int q = 0; q < (N + 3) / 4; ++q) {
+            const float4 v = r[q];
+            b[4 * q] = v.x; b[4 * q + 1] = v.y; b[4 * q + 2] = v.z; b[4 * q + 3] = v.w;
+            if (OUT) {
+                const float4 w = r[NQ / 4 + q];
+                c[4 * q] = w.x; c[4 * q + 1] = w.y; c[4 * q + 2] = w.z; c[4 * q + 3] = w.w;
+            }
+        }
+        const float u = dl * xv;
         float o = 0.0f;
-        if (!OUT) dsum += d;
+        if (!OUT) dsum += dl;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            h[n] = fmaf(__builtin_amdgcn_exp2f(a[n] * d), h[n], u * r[n]);
-            if (OUT) o = fmaf(h[n], r[N + n], o);
+            h[n] = fmaf(__builtin_amdgcn_exp2f(a[n] * dl), h[n], u * b[n]);
+            if (OUT) o = fmaf(h[n], c[n], o);
         }
         if (OUT) {
-            if (skips) o = fmaf(skip, xv, o);
-            if (gates) o *= zv * sigmoid_f(zv);
-            y[(int64_t)t * sy] = to_stream<T>(o);
+            if (FULL || skips) o = fmaf(skip, xv, o);
+            if (FULL || gates) o *= zv * sigmoid_f(zv);
+            buffer_store(yg, yo, to_stream<T>(o));
         }
     }
-    // rows [t0, t1), t0 < t1: the next group's loads are under way while a group is computed
+    // rows [t0, t1), t0 < t1: the next group's streams and the next tile's B and C are under way
+    // while a group is computed
     template <bool OUT>
     __device__ __forceinline__ void walk(int t0, int t1) {
-        T rd[kGrp], rx[kGrp], rz[kGrp];
-        auto load = [&](int t) {
+        T rd[kGrp], rx[kGrp], rz[kGrp], rb[kStage], rc[kStage];
+        const T *pd = delta + t0 * sdelta, *px = x + t0 * sx, *pz = z + t0 * sz;
+        T* py = y + t0 * sy;
+        int tl = t0;   // the row of pd, px, pz
+        auto load = [&] {   // rows tl .. tl+3 (past the last row of all, the last one again)
+            const buffer_t d_ = buffer_of(pd, kAll), x_ = buffer_of(px, kAll), z_ = buffer_of(pz, kAll);
+            if (tl + kGrp <= rows) {
 #pragma unroll
-            for (int g = 0; g < kGrp; ++g) {
-                const int64_t r = min(t + g, t1 - 1);
-                rd[g] = delta[r * sdelta];
-                rx[g] = x[r * sx];
-                if (OUT) rz[g] = z[r * sz];
-            }
-        };
-        load(t0);
-        for (int t = t0; t < t1; t += kGrp) {
-            float dl[kGrp], xv[kGrp], zv[kGrp];
-#pragma unroll
-            for (int g = 0; g < kGrp; ++g) {
-                dl[g] = to_f32(rd[g]) + bias;
-                xv[g] = to_f32(rx[g]);
-                zv[g] = OUT ? to_f32(rz[g]) : 0.0f;
-            }
-            load(min(t + kGrp, t1 - 1));
-            if (softplus) {
-#pragma unroll
-                for (int g = 0; g < kGrp; ++g) dl[g] = softplus_t(dl[g]);
-            }
-            if (t + kGrp <= t1) {
-#pragma unroll
-                for (int g = 0; g < kGrp; ++g) row<OUT>(t + g, dl[g], xv[g], zv[g]);
+                for (int g = 0; g < kGrp; ++g) {
+                    rd[g] = buffer_load<T>(d_, db, g * bd);
+                    rx[g] = buffer_load<T>(x_, db, g * bx);
+                    if (OUT) rz[g] = buffer_load<T>(z_, db, g * bz);
+                }
             } else {
 #pragma unroll
-                for (int g = 0; g < kGrp - 1; ++g)
-                    if (t + g < t1) row<OUT>(t + g, dl[g], xv[g], zv[g]);
+                for (int g = 0; g < kGrp; ++g) {
+                    const uint32_t r = max(min(g, rows - 1 - tl), 0);
+                    rd[g] = buffer_load<T>(d_, db, r * bd);
+                    rx[g] = buffer_load<T>(x_, db, r * bx);
+                    if (OUT) rz[g] = buffer_load<T>(z_, db, r * bz);
+                }
+            }
+            const int64_t on = tl + kGrp < rows ? kGrp : 0;
+            tl += (int)on;
+            pd += on * sdelta; px += on * sx; pz += on * sz;
+        };
+        auto load_bc = [&](int t) {   // rows from t1 on are past the buffers' ends
+            const int64_t left = t1 - 1 - t;
+            const uint32_t eb = (uint32_t)(min(left, (int64_t)kTile - 1) * sB + N) * sizeof(T);
+            const uint32_t ec = (uint32_t)(min(left, (int64_t)kTile - 1) * sC + N) * sizeof(T);
+            const buffer_t bb = buffer_of(B + t * sB, eb), cb = buffer_of(C + t * sC, ec);
+#pragma unroll
+            for (int q = 0; q < kStage; ++q) {
+                rb[q] = buffer_load<T>(bb, ob + (uint32_t)(q * (64 / NQ) * (int)sB) * sizeof(T));
+                if (OUT) rc[q] = buffer_load<T>(cb, oc + (uint32_t)(q * (64 / NQ) * (int)sC) * sizeof(T));
+            }
+        };
+        auto stage = [&] {   // a wave's own tile: its LDS accesses complete in order, nothing to wait for
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int q = 0; q < kStage; ++q) {
+                put[q * (64 / NQ) * 2 * NQ] = to_f32(rb[q]);
+                if (OUT) put[q * (64 / NQ) * 2 * NQ + NQ] = to_f32(rc[q]);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        };
+        load_bc(t0);
+        load();
+        for (int tt = t0; tt < t1; tt += kTile) {
+            stage();
+            if (tt + kTile < t1) load_bc(tt + kTile);
+            const int n = min(kTile, t1 - tt);
+#pragma unroll 1
+            for (int i = 0; i < n; i += kGrp) {
+                // rows from t1 on are identity steps: step size and input 0, B and C read as 0, y past the
+                // end of its buffer
+                float dl[kGrp], xv[kGrp], zv[kGrp];
+#pragma unroll
+                for (int g = 0; g < kGrp; ++g) {
+                    dl[g] = to_f32(rd[g]) + bias;
+                    xv[g] = i + g < n ? to_f32(rx[g]) : 0.0f;
+                    zv[g] = OUT ? to_f32(rz[g]) : 0.0f;
+                }
+                load();
+#pragma unroll
+                for (int g = 0; g < kGrp; ++g) {
+                    if (FULL || softplus) dl[g] = softplus_t(dl[g]);
+                    dl[g] = i + g < n ? dl[g] : 0.0f;
+                }
+                const buffer_t yg = buffer_of(py, (uint32_t)(min(kGrp, n - i) - 1) * by + row_bytes);
+#pragma unroll
+                for (int g = 0; g < kGrp; ++g) row<OUT>(i + g, yg, db + g * by, dl[g], xv[g], zv[g]);
+                py += kGrp * sy;
             }
         }
     }
 };
+// a range's states in the workspace, [n][d]
+template <int N>
+__device__ __forceinline__ void get_range(const float* base, int D, int d, float (&h)[N]) {
+    const buffer_t b = buffer_of(base, kAll);
+#pragma unroll
+    for (int n = 0; n < N; ++n) h[n] = buffer_load<float>(b, (uint32_t)d * 4, (uint32_t)(n * D) * 4);
+}
+template <int N>
+__device__ __forceinline__ void put_range(float* base, int D, int d, const float (&h)[N]) {
+    const buffer_t b = buffer_of(base, kAll);
+#pragma unroll
+    for (int n = 0; n < N; ++n) buffer_store(b, (uint32_t)d * 4 + (uint32_t)(n * D) * 4, h[n]);
+}
 template <int N>
 __device__ __forceinline__ void load_states(const float* p, float (&h)[N]) {
 #pragma unroll
@@ -136,47 +229,100 @@ __device__ __forceinline__ Range_ rows_of(const TokScanParams& p, int c) {
 }
 
 // First pass, ranges 0 .. nrange-2.
-template <typename T, int N>
-__global__ __launch_bounds__(256) void tok_scan_sum_kernel(TokScanParams p, int cblocks) {
-    const int cb = blockIdx.x % cblocks;
-    const int c = uniform((blockIdx.x / cblocks) * 4 + (threadIdx.x >> 6));
-    if (c >= p.nrange - 1) return;
+template <typename T, int N, bool FULL>
+__global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_sum_kernel(TokScanParams p, int gblocks) {
+    const int cb = uniform((blockIdx.x % gblocks) * (blockDim.x >> 6) + (threadIdx.x >> 6));
+    const int c = blockIdx.x / gblocks;
+    if (cb * 64 >= p.D) return;
     const Range_ r = rows_of(p, c);
     const int s = uniform(find_seq(p.q.start, p.q.S, r.r1 - 1));
-    if (s < 0 || s >= p.q.S) return;
-    const int st = uniform(p.q.start[s]), en = uniform(min(p.q.start[s + 1], p.q.T));
-    if (st < 0 || en <= r.r1) return;   // none crosses the end
-    const int slot = uniform(slot_of(p.q, s));
-    if (slot < 0) return;
+    int st = 0, en = 0, slot = -1;
+    if (s >= 0 && s < p.q.S) {
+        st = uniform(p.q.start[s]);
+        en = uniform(min(p.q.start[s + 1], p.q.T));
+        if (st >= 0 && en > r.r1) slot = uniform(slot_of(p.q, s));
+    }
+    if (cb == 0 && lane_id() == 0) p.through[c] = slot >= 0 && st < r.r0;
+    if (slot < 0) return;   // none crosses the end
     // lanes past the last channel repeat it: the same values to the same places, without a branch a row
     const int d = min(cb * 64 + lane_id(), p.D - 1);
-    ScanLane<T, N> l(p, d);
-    const int64_t at = (int64_t)c * N * p.D + d;
+    __shared__ __align__(16) float lds[kScanWaves * ScanLane<T, N, FULL>::kLds];
+    ScanLane<T, N, FULL> l(p, d, lds + (threadIdx.x >> 6) * ScanLane<T, N, FULL>::kLds);
+    const int64_t at = (int64_t)c * N * p.D;
 #pragma unroll
     for (int n = 0; n < N; ++n) l.h[n] = 0.0f;
     l.dsum = 0.0f;
     if (st >= r.r0) {   // it begins here: its first state, kept for the second pass (which may find it overwritten)
         if (!(p.q.fresh && p.q.fresh[s])) load_states<N>(p.pool + slot * p.spool + (int64_t)d * N, l.h);
-#pragma unroll
-        for (int n = 0; n < N; ++n) p.h0[at + (int64_t)n * p.D] = l.h[n];
+        put_range<N>(p.h0 + at, p.D, d, l.h);
     }
     l.template walk<false>(max(st, r.r0), r.r1);
-#pragma unroll
-    for (int n = 0; n < N; ++n) p.hsum[at + (int64_t)n * p.D] = l.h[n];
+    put_range<N>(p.hsum + at, p.D, d, l.h);
     p.dsum[(int64_t)c * p.D + d] = l.dsum;
 }
 
+// Between the passes: the states at the ranges' ends, from those that each range leaves alone,
+//   h <- exp(A dsum) h + S where the sequence runs through the whole range, S where it begins there.
+// A workgroup takes 64 channels of one state; its 16 waves take the ranges in 16 runs, compose
+// each, then each composes the runs before its own and goes over its ranges again.
+constexpr int kRuns = 16;
+__global__ __launch_bounds__(64 * kRuns) void tok_scan_join_kernel(TokScanParams p) {
+    __shared__ float sh[kRuns][64], ss[kRuns][64];
+    const int n = blockIdx.x % p.N, lane = lane_id(), w = uniform(threadIdx.x >> 6);
+    const int d = min((int)(blockIdx.x / p.N) * 64 + lane, p.D - 1);
+    const float a = p.A[(int64_t)d * p.N + n] * kLog2e;
+    const int ends = p.nrange - 1, per = (ends + kRuns - 1) / kRuns;
+    const int k0 = min(w * per, ends), k1 = min(k0 + per, ends);
+    float* S = p.hsum + (int64_t)n * p.D + d;
+    const int64_t step = (int64_t)p.N * p.D;
+    auto go = [&](float h, bool keep, float* sum) {
+        bool all = true;
+        float ds = 0.0f;
+        for (int k = k0; k < k1; k += 8) {
+            float s[8], e[8];
+            int f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = min(k + i, k1 - 1);
+                s[i] = S[j * step];
+                e[i] = p.dsum[(int64_t)j * p.D + d];
+                f[i] = p.through[j];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (k + i >= k1) break;
+                h = f[i] ? fmaf(__builtin_amdgcn_exp2f(a * e[i]), h, s[i]) : s[i];
+                ds += e[i];
+                all = all && f[i];
+                if (keep) S[(k + i) * step] = h;
+            }
+        }
+        // the run as a map: through a run with a beginning in it nothing comes
+        if (sum) *sum = all ? __builtin_amdgcn_exp2f(a * ds) : -1.0f;
+        return h;
+    };
+    float decay;
+    const float h = go(0.0f, false, &decay);
+    sh[w][lane] = h;
+    ss[w][lane] = decay;
+    __syncthreads();
+    float in = 0.0f;
+    for (int i = 0; i < w; ++i) in = ss[i][lane] < 0.0f ? sh[i][lane] : fmaf(ss[i][lane], in, sh[i][lane]);
+    go(in, true, nullptr);
+}
+
 // Second pass: every row's output and every sequence's last state.
-template <typename T, int N>
-__global__ __launch_bounds__(256) void tok_scan_kernel(TokScanParams p, int cblocks) {
-    const int cb = blockIdx.x % cblocks;
-    const int c = uniform((blockIdx.x / cblocks) * 4 + (threadIdx.x >> 6));
-    if (c >= p.nrange) return;
+template <typename T, int N, bool FULL>
+__global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_kernel(TokScanParams p, int gblocks) {
+    const int cb = uniform((blockIdx.x % gblocks) * (blockDim.x >> 6) + (threadIdx.x >> 6));
+    const int c = blockIdx.x / gblocks;
+    if (cb * 64 >= p.D) return;
     const Range_ r = rows_of(p, c);
     int s = uniform(find_seq(p.q.start, p.q.S, r.r0));
     if (s >= p.q.S) return;
     const int d = min(cb * 64 + lane_id(), p.D - 1);
-    ScanLane<T, N> l(p, d);
+    __shared__ __align__(16) float lds[kScanWaves * ScanLane<T, N, FULL>::kLds];
+    ScanLane<T, N, FULL> l(p, d, lds + (threadIdx.x >> 6) * ScanLane<T, N, FULL>::kLds);
     if (s < 0) s = 0;
     for (; s < p.q.S; ++s) {
         const int st = uniform(p.q.start[s]);
@@ -189,17 +335,9 @@ __global__ __launch_bounds__(256) void tok_scan_kernel(TokScanParams p, int cblo
 #pragma unroll
         for (int n = 0; n < N; ++n) l.h[n] = 0.0f;
         if (st < r.r0) {   // from the ranges before: the state that crosses into this one
-            for (int k = st / p.rows; k < c; ++k) {
-                const float ds = p.dsum[(int64_t)k * p.D + d];
-                const float* S = p.hsum + (int64_t)k * N * p.D + d;
-#pragma unroll
-                for (int n = 0; n < N; ++n)
-                    l.h[n] = fmaf(__builtin_amdgcn_exp2f(l.a[n] * ds), l.h[n], S[(int64_t)n * p.D]);
-            }
+            get_range<N>(p.hsum + (int64_t)(c - 1) * N * p.D, p.D, d, l.h);
         } else if (en > r.r1) {
-            const float* S = p.h0 + (int64_t)c * N * p.D + d;
-#pragma unroll
-            for (int n = 0; n < N; ++n) l.h[n] = S[(int64_t)n * p.D];
+            get_range<N>(p.h0 + (int64_t)c * N * p.D, p.D, d, l.h);
         } else if (!(p.q.fresh && p.q.fresh[s])) {
             load_states<N>(pool, l.h);
         }
@@ -305,11 +443,16 @@ hipError_t tok_step(const TokScanParams& p, hipStream_t st) {
 template <typename T, int N>
 hipError_t tok_scan_n(const TokScanParams& p, bool sum, hipStream_t st) {
     const int64_t cblocks = ((int64_t)p.D + 63) / 64;
-    const int64_t groups = ((int64_t)(sum ? p.nrange - 1 : p.nrange) + 3) / 4;
-    if (cblocks * groups >= (1LL << 31)) return hipErrorInvalidValue;
-    const unsigned g = (unsigned)(cblocks * groups);
-    if (sum) tok_scan_sum_kernel<T, N><<<g, 256, 0, st>>>(p, (int)cblocks);
-    else tok_scan_kernel<T, N><<<g, 256, 0, st>>>(p, (int)cblocks);
+    const int64_t gblocks = (cblocks + kScanWaves - 1) / kScanWaves;   // workgroups along the channels
+    const int waves = (int)((cblocks + gblocks - 1) / gblocks);
+    const int64_t blocks = gblocks * (sum ? p.nrange - 1 : p.nrange);
+    if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
+    const unsigned g = (unsigned)blocks, t = 64 * waves;
+    const int gb = (int)gblocks;
+    if (sum && p.stepf.softplus) tok_scan_sum_kernel<T, N, true><<<g, t, 0, st>>>(p, gb);
+    else if (sum) tok_scan_sum_kernel<T, N, false><<<g, t, 0, st>>>(p, gb);
+    else if (p.skip && p.z && p.stepf.softplus) tok_scan_kernel<T, N, true><<<g, t, 0, st>>>(p, gb);
+    else tok_scan_kernel<T, N, false><<<g, t, 0, st>>>(p, gb);
     return hipGetLastError();
 }
 template <typename T>
@@ -328,11 +471,9 @@ hipError_t tok_scan_t(const TokScanParams& p, bool sum, hipStream_t st) {
 hipError_t launch_tok_step(const TokScanParams& p, int dtype, hipStream_t st) {
     return dtype == 1 ? tok_step<bf16_t>(p, st) : tok_step<float>(p, st);
 }
-hipError_t launch_tok_bc(const TokScanParams& p, int dtype, hipStream_t st) {
-    const int64_t blocks = ((int64_t)p.q.T * 2 * p.N + 255) / 256;
-    if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
-    if (dtype == 1) tok_bc_kernel<bf16_t><<<(unsigned)blocks, 256, 0, st>>>(p);
-    else tok_bc_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(p);
+hipError_t launch_tok_join(const TokScanParams& p, hipStream_t st) {
+    const int64_t blocks = ((int64_t)p.D + 63) / 64 * p.N;
+    tok_scan_join_kernel<<<(unsigned)blocks, 64 * kRuns, 0, st>>>(p);
     return hipGetLastError();
 }
 hipError_t launch_tok_scan(const TokScanParams& p, int dtype, bool sum, hipStream_t st) {
