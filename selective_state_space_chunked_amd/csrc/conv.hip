@@ -22,6 +22,35 @@ __device__ __forceinline__ float sigmoid_f(float v) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
 }
 
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// a run to a stream: float to bf16 by the conversion instruction, to nearest even
+__device__ __forceinline__ void store_stream(float* p, const float (&v)[kConvRun], bool vec, int n) {
+    store_run<kConvRun>(p, v, vec, n);
+}
+__device__ __forceinline__ void store_stream(bf16_t* p, const float (&v)[kConvRun], bool vec, int n) {
+    uint32_t w[kConvRun / 2];
+#pragma unroll
+    for (int j = 0; j < kConvRun / 2; ++j)
+        w[j] = (uint32_t)__builtin_bit_cast(bf16_t, (__bf16)v[2 * j]) |
+               ((uint32_t)__builtin_bit_cast(bf16_t, (__bf16)v[2 * j + 1]) << 16);
+    if (vec && n >= kConvRun) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kConvRun; ++j)
+            if (j < n) p[j] = (bf16_t)(w[j / 2] >> (16 * (j & 1)));
+    }
+}
+
+// A lane's left and right neighbour in the wave (lane 0, lane 63: `edge`).
+__device__ __forceinline__ float from_left(float v, float edge) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(edge), __float_as_int(v), 0x138, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float from_right(float v, float edge) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(edge), __float_as_int(v), 0x130, 0xf, 0xf, false));
+}
+
 // One row's input: the stream itself, or the values its 8-bit checkpoint stands for.
 template <typename T, bool X8>
 struct Row {
@@ -48,12 +77,20 @@ __device__ __forceinline__ Row<T, X8> row_of(const ConvParams& p, int b, int d) 
     o.W = p.W;
     return o;
 }
-// steps t0 .. t0+7 of the row (steps past the end 0)
+// eight bytes of a checkpoint
+__device__ __forceinline__ void unpack8(const int8_t* q, float scale, float (&v)[kConvRun]) {
+    const uint2 w = *reinterpret_cast<const uint2*>(q);
+#pragma unroll
+    for (int j = 0; j < kConvRun; ++j) v[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3))) * scale;
+}
+// steps t0 .. t0+7 of the row (steps past the end 0); vec: 16 (checkpoint: 8) bytes at once
 template <typename T, bool X8>
 __device__ __forceinline__ void load_x(const Row<T, X8>& r, int t0, float (&v)[kConvRun], bool vec) {
-    if (X8 || t0 + kConvRun > r.L) {
+    if (t0 + kConvRun > r.L || (X8 && !vec)) {
 #pragma unroll
         for (int j = 0; j < kConvRun; ++j) v[j] = t0 + j < r.L ? r.at(t0 + j) : 0.0f;
+    } else if (X8) {
+        unpack8(r.q + t0, r.s[t0 / kCkptBlock], v);
     } else {
         load_run<kConvRun>(r.x + t0, v, vec);
     }
@@ -81,7 +118,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int segs) {
     const int t0 = run * kConvRun;
     float e[kConvRun + W - 1];
     float v[kConvRun] = {};
-    if (act) load_x(in, t0, v, p.vx);
+    if (act) load_x(in, t0, v, X8 ? p.v8 : p.vx);
     if (P8) {
         int m = 0;
 #pragma unroll
@@ -116,8 +153,13 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int segs) {
         for (int i = 0; i < W - 1; ++i) last[i] = from_f32<T>(in.at(p.L - (W - 1) + i));
     }
     if (!p.y) return;
+    // the W-1 steps before a lane's own are the left neighbour's last ones
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i) e[i] = in.at(t0 - (W - 1) + i);
+    for (int i = 0; i < W - 1; ++i) e[i] = from_left(v[kConvRun - (W - 1) + i], 0.0f);
+    if (lane_id() == 0 || threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) e[i] = in.at(t0 - (W - 1) + i);
+    }
 #pragma unroll
     for (int j = 0; j < kConvRun; ++j) e[W - 1 + j] = v[j];
     float w[W];
@@ -132,13 +174,130 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int segs) {
         for (int k = 0; k < W; ++k) a = fmaf(w[k], e[j + k], a);
         o[j] = p.silu ? a * sigmoid_f(a) : a;
     }
-    store_run<kConvRun>((T*)p.y + b * p.sy[0] + d * p.sy[1] + t0, o, p.vy, p.L - t0);
+    store_stream((T*)p.y + b * p.sy[0] + d * p.sy[1] + t0, o, p.vy, p.L - t0);
 }
+
+// gy act'(p) of the step whose window is e[0..W-1]
+template <int W>
+__device__ __forceinline__ float grad_pre(const float* e, const float (&w)[W], float bias, float gy, int silu) {
+    float a = bias;
+#pragma unroll
+    for (int k = 0; k < W; ++k) a = fmaf(w[k], e[k], a);
+    if (!silu) return gy;
+    const float s = sigmoid_f(a);
+    return gy * s * fmaf(a, 1.0f - s, 1.0f);
+}
+
+// A run of eight steps as loaded, turned into floats where it is used (so loads stay under way meanwhile).
+template <typename T> struct Run;
+template <> struct Run<bf16_t> {
+    uint4 r;
+    __device__ __forceinline__ void load(const bf16_t* p) { r = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void load(const bf16_t* p, int n) {   // the first n
+        uint32_t w[4] = {};
+#pragma unroll
+        for (int j = 0; j < kConvRun; ++j)
+            if (j < n) w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+        r = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void get(float (&v)[kConvRun]) const {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(w[e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+    }
+};
+template <> struct Run<float> {
+    float4 r[2];
+    __device__ __forceinline__ void load(const float* p) {
+        r[0] = *reinterpret_cast<const float4*>(p);
+        r[1] = *reinterpret_cast<const float4*>(p + 4);
+    }
+    __device__ __forceinline__ void load(const float* p, int n) {
+        float v[kConvRun];
+#pragma unroll
+        for (int j = 0; j < kConvRun; ++j) v[j] = j < n ? p[j] : 0.0f;
+        r[0] = make_float4(v[0], v[1], v[2], v[3]);
+        r[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    __device__ __forceinline__ void get(float (&v)[kConvRun]) const {
+        v[0] = r[0].x; v[1] = r[0].y; v[2] = r[0].z; v[3] = r[0].w;
+        v[4] = r[1].x; v[5] = r[1].y; v[6] = r[1].z; v[7] = r[1].w;
+    }
+};
+struct Run8 {
+    uint2 r;
+    float s;
+    __device__ __forceinline__ void load(const int8_t* p, const float* sc) {
+        r = *reinterpret_cast<const uint2*>(p);
+        s = *sc;
+    }
+    __device__ __forceinline__ void load(const int8_t* p, const float* sc, int n) {
+        uint32_t w[2] = {};
+        s = n > 0 ? *sc : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kConvRun; ++j)
+            if (j < n) w[j / 4] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
+        r = make_uint2(w[0], w[1]);
+    }
+    __device__ __forceinline__ void get(float (&v)[kConvRun]) const {
+#pragma unroll
+        for (int j = 0; j < kConvRun; ++j) v[j] = (float)(int8_t)((j < 4 ? r.x : r.y) >> (8 * (j & 3))) * s;
+    }
+};
+
+// What a lane has of its run (an item: batch row and run), loaded a tile ahead.
+template <typename T, int W, bool X8>
+struct BwdTile {
+    static constexpr int H = W - 1, R = kConvRun;
+    int b, run, n;      // n: steps from the run's first one on, 0 for a lane without an item
+    bool full;          // every lane's run is whole
+    Run<T> g;
+    Run<T> x;
+    Run8 q;
+    float halo;         // lane i < H: the input H - i steps before lane 0's run (0 where the row begins there)
+    const T* gy;
+
+    __device__ __forceinline__ void load(const ConvParams& p, int d, int item, int end) {
+        const int lane = lane_id();
+        const bool act = item < end;
+        b = act ? item / p.nrun : 0;
+        run = act ? item - b * p.nrun : 0;
+        n = act ? p.L - run * R : 0;
+        full = __all(n >= R);
+        const Row<T, X8> in = row_of<T, X8>(p, b, d);
+        gy = (const T*)p.gy + b * p.sgy[0] + d * p.sgy[1] + run * R;
+        if (full && p.vgy) g.load(gy);
+        else g.load(gy, n);
+        if (X8) {
+            if (full && p.v8) q.load(in.q + run * R, in.s + run * R / kCkptBlock);
+            else q.load(in.q + run * R, in.s + run * R / kCkptBlock, n);
+        } else {
+            if (full && p.vx) x.load(in.x + run * R);
+            else x.load(in.x + run * R, n);
+        }
+        const int b0 = uniform(b), t0 = uniform(run) * R - H + lane;   // lane 0's item
+        halo = 0.0f;
+        if (lane < H && t0 >= 0) halo = row_of<T, X8>(p, b0, d).at(t0);
+    }
+    __device__ __forceinline__ void get_x(float (&v)[R]) const {
+        if (X8) q.get(v);
+        else x.get(v);
+    }
+};
 
 // Backward: a workgroup takes the items (batch row, run) [part * per_part, ..)
 // of one channel and leaves its sums of gw and gbias: no atomics, one order.
+// Neighbouring lanes hold neighbouring items, so the inputs before a run and the
+// gradients after it come from the lanes beside it.  A wave goes through its
+// items from the last to the first, 64 at a time, so the gradients after a tile
+// are those of the tile before; the next tile's loads are under way while one is
+// computed.
 template <typename T, int W, bool X8>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
+    constexpr int H = W - 1, R = kConvRun;
     const int d = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
     const int items = p.B * p.nrun;
     const int i0 = part * p.per_part, i1 = min(i0 + p.per_part, items);
@@ -146,46 +305,91 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
 #pragma unroll
     for (int k = 0; k < W; ++k) w[k] = p.w[(int64_t)d * W + k];
     const float bias = p.bias ? p.bias[d] : 0.0f;
-    constexpr int H = W - 1, R = kConvRun;
+    const int lane = lane_id();
     float acc[W + 1] = {};
-    for (int it = i0 + (int)threadIdx.x; it < i1; it += 256) {
-        const int b = it / p.nrun, run = it % p.nrun, t0 = run * R;
-        const Row<T, X8> in = row_of<T, X8>(p, b, d);
-        const T* gy = (const T*)p.gy + b * p.sgy[0] + d * p.sgy[1];
-        float v[R], g[R];
-        load_x(in, t0, v, p.vx);
-        const int n = p.L - t0;   // steps from t0 on
-        if (n >= R) load_run<R>(gy + t0, g, p.vgy);
-        else load_run_masked<T, R>(gy + t0, g, n);
-        float e[R + 2 * H], gp[R + H];
+    const int tiles = (i1 - i0 + 63) / 64, per = (tiles + 3) / 4;   // of a wave
+    const int ta = uniform((int)threadIdx.x >> 6) * per, tb = min(ta + per, tiles);
+    BwdTile<T, W, X8> c, nx;
+    float after[H] = {};   // the first H gradients of the tile to the right
+    if (ta < tb) c.load(p, d, i0 + (tb - 1) * 64 + lane, i1);
+    for (int k = tb - 1; k >= ta; --k) {
+        if (k > ta) nx.load(p, d, i0 + (k - 1) * 64 + lane, i1);
+        const int n = c.n;
+        const bool ends = c.run == p.nrun - 1;   // no gradients after the row's last run
+        float v[R], g[R], e[R + H], gp[R + H];
+        c.get_x(v);
+        c.g.get(g);
 #pragma unroll
-        for (int i = 0; i < H; ++i) e[i] = in.at(t0 - H + i);
+        for (int i = 0; i < H; ++i) {
+            const float edge = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(c.halo), i));
+            e[i] = from_left(v[R - H + i], edge);
+            e[i] = c.run == 0 ? 0.0f : e[i];
+        }
+        if (p.init && c.run == 0 && n > 0) {
+            const T* init = (const T*)p.init + ((int64_t)c.b * p.D + d) * H;
+#pragma unroll
+            for (int i = 0; i < H; ++i) e[i] = to_f32(init[i]);
+        }
 #pragma unroll
         for (int j = 0; j < R; ++j) e[H + j] = v[j];
 #pragma unroll
-        for (int i = 0; i < H; ++i) e[H + R + i] = R + i < n ? in.at(t0 + R + i) : 0.0f;
+        for (int j = 0; j < R; ++j) gp[j] = grad_pre<W>(e + j, w, bias, g[j], p.silu);
+        if (!c.full) {
 #pragma unroll
-        for (int j = 0; j < R + H; ++j) {
-            float a = bias;
+            for (int j = 0; j < R; ++j) gp[j] = j < n ? gp[j] : 0.0f;
+        }
+        if (k == tb - 1) {   // the item after a wave's last one is another wave's: its first gradients again
+            const bool right = n > R && (lane == 63 || i0 + k * 64 + lane + 1 >= i1);
+            float q[H] = {};
+            if (right) {
+                const Row<T, X8> in = row_of<T, X8>(p, c.b, d);
+                float f[2 * H], gr[H];
 #pragma unroll
-            for (int k = 0; k < W; ++k) a = fmaf(w[k], e[j + k], a);
-            const float go = j < R ? g[j < R ? j : 0] : (j < n ? to_f32(gy[t0 + j]) : 0.0f);
-            float q = go;
-            if (p.silu) {
-                const float s = sigmoid_f(a);
-                q = go * s * fmaf(a, 1.0f - s, 1.0f);
+                for (int i = 0; i < H; ++i) {
+                    f[i] = v[R - H + i];
+                    const bool has = R + i < n;
+                    f[H + i] = has ? in.at(c.run * R + R + i) : 0.0f;
+                    gr[i] = has ? to_f32(c.gy[R + i]) : 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const float a = grad_pre<W>(f + i, w, bias, gr[i], p.silu);
+                    q[i] = R + i < n ? a : 0.0f;
+                }
             }
-            gp[j] = j < n ? q : 0.0f;
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float a = from_right(gp[i], 0.0f);
+                gp[R + i] = right ? q[i] : ends ? 0.0f : a;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float a = from_right(gp[i], after[i]);
+                gp[R + i] = ends ? 0.0f : a;
+            }
         }
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            if (j < n) {   // steps past the end add nothing, whatever lies there
+        for (int i = 0; i < H; ++i)
+            after[i] = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(gp[i])));
+        if (c.full) {
 #pragma unroll
-                for (int k = 0; k < W; ++k) acc[k] = fmaf(gp[j], e[j + k], acc[k]);
+            for (int j = 0; j < R; ++j) {
+#pragma unroll
+                for (int q = 0; q < W; ++q) acc[q] = fmaf(gp[j], e[j + q], acc[q]);
                 acc[W] += gp[j];
             }
+        } else {
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                if (j < n) {   // steps past the end add nothing, whatever lies there
+#pragma unroll
+                    for (int q = 0; q < W; ++q) acc[q] = fmaf(gp[j], e[j + q], acc[q]);
+                    acc[W] += gp[j];
+                }
+            }
         }
-        const int64_t row = (int64_t)b * p.D + d;
+        const int64_t row = (int64_t)c.b * p.D + d;
         const T* gl = p.glast ? (const T*)p.glast + row * H : nullptr;
         if (p.gx) {
             float o[R];
@@ -193,27 +397,33 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
             for (int j = 0; j < R; ++j) {
                 float a = 0.0f;
 #pragma unroll
-                for (int k = 0; k < W; ++k) a = fmaf(w[k], gp[j + H - k], a);
-                if (gl && j < n && j + H >= n) a += to_f32(gl[j + H - n]);
+                for (int q = 0; q < W; ++q) a = fmaf(w[q], gp[j + H - q], a);
                 o[j] = a;
             }
-            store_run<R>((T*)p.gx + b * p.sgx[0] + d * p.sgx[1] + t0, o, p.vgx, n);
+            if (gl && n > 0 && n < R + H) {   // the last W-1 steps
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    if (j < n && j + H >= n) o[j] += to_f32(gl[j + H - n]);
+            }
+            T* gx = (T*)p.gx + c.b * p.sgx[0] + d * p.sgx[1] + c.run * R;
+            if (c.full) store_stream(gx, o, p.vgx, R);
+            else store_stream(gx, o, p.vgx, n);
         }
-        if (p.ginit && run == 0) {
+        if (p.ginit && c.run == 0 && n > 0) {
             T* gi = (T*)p.ginit + row * H;
 #pragma unroll
             for (int j = 0; j < H; ++j) {
                 float a = 0.0f;
 #pragma unroll
-                for (int k = 0; k <= j; ++k) a = fmaf(w[k], gp[j - k], a);
+                for (int q = 0; q <= j; ++q) a = fmaf(w[q], gp[j - q], a);
                 if (gl && j >= n) a += to_f32(gl[j - n]);
                 gi[j] = from_f32<T>(a);
             }
         }
+        c = nx;
     }
     if (!p.gw && !p.gbias) return;
     __shared__ float sum[4][W + 1];
-    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int k = 0; k <= W; ++k) {
         float a = acc[k];
@@ -252,9 +462,13 @@ __global__ __launch_bounds__(256) void ckpt8_unpack_kernel(ConvParams p, int seg
     const float s = p.x8_scale[row * p.nblk + run / 8];
     const int n = p.L - t0;
     float v[kConvRun];
+    if (p.v8) {
+        unpack8(q, s, v);
+    } else {
 #pragma unroll
-    for (int j = 0; j < kConvRun; ++j) v[j] = j < n ? (float)q[j] * s : 0.0f;
-    store_run<kConvRun>((T*)p.y + b * p.sy[0] + d * p.sy[1] + t0, v, p.vy, n);
+        for (int j = 0; j < kConvRun; ++j) v[j] = j < n ? (float)q[j] * s : 0.0f;
+    }
+    store_stream((T*)p.y + b * p.sy[0] + d * p.sy[1] + t0, v, p.vy, n);
 }
 
 // lanes along the row and rows per workgroup; blocks along the row
