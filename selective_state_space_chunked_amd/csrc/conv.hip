@@ -83,98 +83,12 @@ __device__ __forceinline__ void unpack8(const int8_t* q, float scale, float (&v)
 #pragma unroll
     for (int j = 0; j < kConvRun; ++j) v[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3))) * scale;
 }
-// steps t0 .. t0+7 of the row (steps past the end 0); vec: 16 (checkpoint: 8) bytes at once
-template <typename T, bool X8>
-__device__ __forceinline__ void load_x(const Row<T, X8>& r, int t0, float (&v)[kConvRun], bool vec) {
-    if (t0 + kConvRun > r.L || (X8 && !vec)) {
-#pragma unroll
-        for (int j = 0; j < kConvRun; ++j) v[j] = t0 + j < r.L ? r.at(t0 + j) : 0.0f;
-    } else if (X8) {
-        unpack8(r.q + t0, r.s[t0 / kCkptBlock], v);
-    } else {
-        load_run<kConvRun>(r.x + t0, v, vec);
-    }
-}
-
 // max |x| of a checkpoint block as a bit pattern: of non-negative floats the
 // integers order as the values do, infinity above all numbers and NaN above it.
 __device__ __forceinline__ int block_max(int m) {   // over aligned groups of 8 lanes
     m = max(m, dpp_i<SSM_DPP_QUAD(1, 0, 3, 2)>(0, m));
     m = max(m, dpp_i<SSM_DPP_QUAD(2, 3, 0, 1)>(0, m));
     return max(m, dpp_i<SSM_DPP_ROW_HALF_MIRROR>(0, m));
-}
-
-// Forward: block (TX lanes along the row, 256 / TX rows).  With P8 the eight
-// lanes of a 64-step block agree on its scale (TX >= 8).
-template <typename T, int W, bool X8, bool P8>
-__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int segs) {
-    const int64_t rb = blockIdx.x / segs;
-    const int run = (int)(blockIdx.x % segs) * blockDim.x + threadIdx.x;
-    const int64_t row = rb * blockDim.y + threadIdx.y;
-    const bool act = row < (int64_t)p.B * p.D && run < p.nrun;
-    if (!P8 && !act) return;
-    const int b = act ? (int)(row / p.D) : 0, d = act ? (int)(row % p.D) : 0;
-    const Row<T, X8> in = row_of<T, X8>(p, b, d);
-    const int t0 = run * kConvRun;
-    float e[kConvRun + W - 1];
-    float v[kConvRun] = {};
-    if (act) load_x(in, t0, v, X8 ? p.v8 : p.vx);
-    if (P8) {
-        int m = 0;
-#pragma unroll
-        for (int j = 0; j < kConvRun; ++j) m = max(m, __float_as_int(v[j]) & 0x7fffffff);
-        m = block_max(m);
-        const float amax = __int_as_float(m);
-        const bool bad = m >= 0x7f800000, zero = amax < kTiny8;
-        const float scale = bad ? __int_as_float(0x7fc00000) : zero ? 0.0f : amax / 127.0f;
-        const float inv = bad || zero ? 0.0f : 127.0f / amax;
-        if (act) {
-            int8_t* o = p.o8 + row * p.L + t0;
-            uint32_t w0 = 0, w1 = 0;
-#pragma unroll
-            for (int j = 0; j < kConvRun; ++j) {
-                const int q = bad ? 0 : (int)rintf(v[j] * inv);
-                if (j < 4) w0 |= (uint32_t)(q & 255) << (8 * j);
-                else w1 |= (uint32_t)(q & 255) << (8 * (j - 4));
-            }
-            if (p.v8) {
-                *reinterpret_cast<uint2*>(o) = make_uint2(w0, w1);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kConvRun; ++j)
-                    if (t0 + j < p.L) o[j] = (int8_t)((j < 4 ? w0 >> (8 * j) : w1 >> (8 * (j - 4))) & 255);
-            }
-            if ((run & 7) == 0) p.o8_scale[row * p.nblk + run / 8] = scale;
-        }
-    }
-    if (!act) return;
-    if (p.last && run == 0) {
-        T* last = (T*)p.last + row * (W - 1);
-        for (int i = 0; i < W - 1; ++i) last[i] = from_f32<T>(in.at(p.L - (W - 1) + i));
-    }
-    if (!p.y) return;
-    // the W-1 steps before a lane's own are the left neighbour's last ones
-#pragma unroll
-    for (int i = 0; i < W - 1; ++i) e[i] = from_left(v[kConvRun - (W - 1) + i], 0.0f);
-    if (lane_id() == 0 || threadIdx.x == 0) {
-#pragma unroll
-        for (int i = 0; i < W - 1; ++i) e[i] = in.at(t0 - (W - 1) + i);
-    }
-#pragma unroll
-    for (int j = 0; j < kConvRun; ++j) e[W - 1 + j] = v[j];
-    float w[W];
-#pragma unroll
-    for (int k = 0; k < W; ++k) w[k] = p.w[(int64_t)d * W + k];
-    const float bias = p.bias ? p.bias[d] : 0.0f;
-    float o[kConvRun];
-#pragma unroll
-    for (int j = 0; j < kConvRun; ++j) {
-        float a = bias;
-#pragma unroll
-        for (int k = 0; k < W; ++k) a = fmaf(w[k], e[j + k], a);
-        o[j] = p.silu ? a * sigmoid_f(a) : a;
-    }
-    store_stream((T*)p.y + b * p.sy[0] + d * p.sy[1] + t0, o, p.vy, p.L - t0);
 }
 
 // gy act'(p) of the step whose window is e[0..W-1]
@@ -248,27 +162,144 @@ struct Run8 {
     }
 };
 
-// What a lane has of its run (an item: batch row and run), loaded a tile ahead.
+// Forward: a workgroup takes TX lanes' runs of TY rows (TX * TY = 256), UNITS neighbouring groups of rows, with all
+// loads issued before the first is used; the grid runs along the steps first, so the workgroups under way sweep
+// the streams in order.  With P8 the eight lanes of a 64-step block agree on its scale (TX >= 8).
+template <typename T, int W, bool X8, bool P8, int UNITS>
+__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int dblocks) {
+    constexpr int H = W - 1, R = kConvRun;
+    const int run = blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.z, t0 = run * R;
+    // the W-1 steps before a lane's own are the left neighbour's last ones, but for these lanes
+    const bool first = lane_id() == 0 || threadIdx.x == 0;
+    for (int db = blockIdx.y; db < dblocks; db += gridDim.y) {
+        Run<T> x[UNITS];
+        Run8 q[UNITS];
+        float left[UNITS][H], w[UNITS][W], bias[UNITS];
+        int n[UNITS];
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int d = (db * UNITS + u) * blockDim.y + threadIdx.y;
+            n[u] = d < p.D && run < p.nrun ? p.L - t0 : 0;
+            const Row<T, X8> in = row_of<T, X8>(p, b, n[u] > 0 ? d : 0);
+            if (X8) {
+                if (n[u] >= R && p.v8) q[u].load(in.q + t0, in.s + t0 / kCkptBlock);
+                else q[u].load(in.q + t0, in.s + t0 / kCkptBlock, n[u]);
+            } else {
+                if (n[u] >= R && p.vx) x[u].load(in.x + t0);
+                else x[u].load(in.x + t0, n[u]);
+            }
+            const int dw = n[u] > 0 && p.y ? d : 0;
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[u][k] = p.y ? p.w[(int64_t)dw * W + k] : 0.0f;
+            bias[u] = p.y && p.bias ? p.bias[dw] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < H; ++i) left[u][i] = 0.0f;
+            if (first && n[u] > 0 && p.y) {
+                if (run > 0 || p.init) {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) left[u][i] = in.at(t0 - H + i);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int d = (db * UNITS + u) * blockDim.y + threadIdx.y;
+            const int64_t row = (int64_t)b * p.D + d;
+            float v[R], e[R + H];
+            if (X8) q[u].get(v);
+            else x[u].get(v);
+            if (P8) {
+                int m = 0;
+#pragma unroll
+                for (int j = 0; j < R; ++j) m = max(m, __float_as_int(v[j]) & 0x7fffffff);   // past the end: 0
+                m = block_max(m);
+                const float amax = __int_as_float(m);
+                const bool bad = m >= 0x7f800000, zero = amax < kTiny8;
+                const float scale = bad ? __int_as_float(0x7fc00000) : zero ? 0.0f : amax / 127.0f;
+                const float inv = bad || zero ? 0.0f : 127.0f / amax;
+                if (n[u] > 0) {
+                    int8_t* o = p.o8 + row * p.L + t0;
+                    uint32_t w0 = 0, w1 = 0;
+#pragma unroll
+                    for (int j = 0; j < R; ++j) {
+                        const int k = bad ? 0 : (int)rintf(v[j] * inv);
+                        if (j < 4) w0 |= (uint32_t)(k & 255) << (8 * j);
+                        else w1 |= (uint32_t)(k & 255) << (8 * (j - 4));
+                    }
+                    if (p.v8) {
+                        *reinterpret_cast<uint2*>(o) = make_uint2(w0, w1);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < R; ++j)
+                            if (j < n[u]) o[j] = (int8_t)((j < 4 ? w0 >> (8 * j) : w1 >> (8 * (j - 4))) & 255);
+                    }
+                    if ((run & 7) == 0) p.o8_scale[row * p.nblk + run / 8] = scale;
+                }
+            }
+            if (p.last && run == 0 && n[u] > 0) {
+                const Row<T, X8> in = row_of<T, X8>(p, b, d);
+                T* last = (T*)p.last + row * H;
+                for (int i = 0; i < H; ++i) last[i] = from_f32<T>(in.at(p.L - H + i));
+            }
+            if (!p.y) continue;
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                e[i] = from_left(v[R - H + i], 0.0f);
+                e[i] = first ? left[u][i] : e[i];
+            }
+#pragma unroll
+            for (int j = 0; j < R; ++j) e[H + j] = v[j];
+            if (n[u] <= 0) continue;
+            float o[R];
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                float a = bias[u];
+#pragma unroll
+                for (int k = 0; k < W; ++k) a = fmaf(w[u][k], e[j + k], a);
+                o[j] = p.silu ? a * sigmoid_f(a) : a;
+            }
+            store_stream((T*)p.y + b * p.sy[0] + d * p.sy[1] + t0, o, p.vy, n[u]);
+        }
+    }
+}
+
+// A lane's item of one channel: batch row and run, item = row * runs + run.  It moves by a workgroup's 256
+// items at a time without a division: q rows and r runs, and one more row where the runs underflow.
+struct Place {
+    int item, b, run;
+    __device__ __forceinline__ void set(int i, int nrun) {
+        item = i;
+        b = i / nrun;
+        run = i - b * nrun;
+    }
+    __device__ __forceinline__ void back(int nrun, int q, int r) {
+        item -= 256;
+        b -= q;
+        run -= r;
+        const bool w = run < 0;
+        b -= w ? 1 : 0;
+        run += w ? nrun : 0;
+    }
+};
+// What a lane has of its run, loaded a step ahead.
 template <typename T, int W, bool X8>
 struct BwdTile {
     static constexpr int H = W - 1, R = kConvRun;
     int b, run, n;      // n: steps from the run's first one on, 0 for a lane without an item
     bool full;          // every lane's run is whole
-    Run<T> g;
-    Run<T> x;
+    Run<T> g, x;
     Run8 q;
-    float halo;         // lane i < H: the input H - i steps before lane 0's run (0 where the row begins there)
-    const T* gy;
+    float halo;         // lane i < H: the input H - i steps before lane 0's run
 
-    __device__ __forceinline__ void load(const ConvParams& p, int d, int item, int end) {
+    __device__ __forceinline__ void load(const ConvParams& p, int d, const Place& at, int end) {
         const int lane = lane_id();
-        const bool act = item < end;
-        b = act ? item / p.nrun : 0;
-        run = act ? item - b * p.nrun : 0;
+        const bool act = at.item < end;
+        b = act ? at.b : 0;
+        run = act ? at.run : 0;
         n = act ? p.L - run * R : 0;
         full = __all(n >= R);
         const Row<T, X8> in = row_of<T, X8>(p, b, d);
-        gy = (const T*)p.gy + b * p.sgy[0] + d * p.sgy[1] + run * R;
+        const T* gy = (const T*)p.gy + b * p.sgy[0] + d * p.sgy[1] + run * R;
         if (full && p.vgy) g.load(gy);
         else g.load(gy, n);
         if (X8) {
@@ -278,9 +309,9 @@ struct BwdTile {
             if (full && p.vx) x.load(in.x + run * R);
             else x.load(in.x + run * R, n);
         }
-        const int b0 = uniform(b), t0 = uniform(run) * R - H + lane;   // lane 0's item
+        const int t0 = uniform(run) * R - H + lane;   // in lane 0's row
         halo = 0.0f;
-        if (lane < H && t0 >= 0) halo = row_of<T, X8>(p, b0, d).at(t0);
+        if (lane < H && t0 >= 0 && t0 < p.L) halo = row_of<T, X8>(p, uniform(b), d).at(t0);
     }
     __device__ __forceinline__ void get_x(float (&v)[R]) const {
         if (X8) q.get(v);
@@ -288,34 +319,41 @@ struct BwdTile {
     }
 };
 
+// workgroup barrier that waits for LDS accesses only: loads and stores of global memory stay under way
+__device__ __forceinline__ void lds_barrier() { __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // Backward: a workgroup takes the items (batch row, run) [part * per_part, ..)
 // of one channel and leaves its sums of gw and gbias: no atomics, one order.
 // Neighbouring lanes hold neighbouring items, so the inputs before a run and the
-// gradients after it come from the lanes beside it.  A wave goes through its
-// items from the last to the first, 64 at a time, so the gradients after a tile
-// are those of the tile before; the next tile's loads are under way while one is
-// computed.
+// gradients after it come from the lanes beside it, between waves through LDS.
+// The items are taken 256 at a time from the last to the first, so the gradients
+// after a group are those of the group before; the next group's loads are under
+// way while one is computed.
 template <typename T, int W, bool X8>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
     constexpr int H = W - 1, R = kConvRun;
-    const int d = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+    const int d = blockIdx.x % p.D, part = blockIdx.x / p.D;
     const int items = p.B * p.nrun;
     const int i0 = part * p.per_part, i1 = min(i0 + p.per_part, items);
     float w[W];
 #pragma unroll
     for (int k = 0; k < W; ++k) w[k] = p.w[(int64_t)d * W + k];
     const float bias = p.bias ? p.bias[d] : 0.0f;
-    const int lane = lane_id();
+    const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
+    __shared__ float begin[2][4][4];   // each wave's first H gradients, of this group and the last one
     float acc[W + 1] = {};
-    const int tiles = (i1 - i0 + 63) / 64, per = (tiles + 3) / 4;   // of a wave
-    const int ta = uniform((int)threadIdx.x >> 6) * per, tb = min(ta + per, tiles);
+    const int groups = (i1 - i0 + 255) / 256, q256 = 256 / p.nrun, r256 = 256 - q256 * p.nrun;
     BwdTile<T, W, X8> c, nx;
-    float after[H] = {};   // the first H gradients of the tile to the right
-    if (ta < tb) c.load(p, d, i0 + (tb - 1) * 64 + lane, i1);
-    for (int k = tb - 1; k >= ta; --k) {
-        if (k > ta) nx.load(p, d, i0 + (k - 1) * 64 + lane, i1);
-        const int n = c.n;
-        const bool ends = c.run == p.nrun - 1;   // no gradients after the row's last run
+    Place at;
+    at.set(i0 + (groups - 1) * 256 + (int)threadIdx.x, p.nrun);
+    c.load(p, d, at, i1);
+    float after[H] = {};   // wave 3: the first H gradients of the group to the right
+    for (int k = groups - 1; k >= 0; --k) {
+        if (k > 0) {
+            at.back(p.nrun, q256, r256);
+            nx.load(p, d, at, i1);
+        }
+        const int n = c.n, item = i0 + k * 256 + (int)threadIdx.x;
         float v[R], g[R], e[R + H], gp[R + H];
         c.get_x(v);
         c.g.get(g);
@@ -338,40 +376,36 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
 #pragma unroll
             for (int j = 0; j < R; ++j) gp[j] = j < n ? gp[j] : 0.0f;
         }
-        if (k == tb - 1) {   // the item after a wave's last one is another wave's: its first gradients again
-            const bool right = n > R && (lane == 63 || i0 + k * 64 + lane + 1 >= i1);
-            float q[H] = {};
-            if (right) {
-                const Row<T, X8> in = row_of<T, X8>(p, c.b, d);
-                float f[2 * H], gr[H];
+        if (lane == 0) {
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    f[i] = v[R - H + i];
-                    const bool has = R + i < n;
-                    f[H + i] = has ? in.at(c.run * R + R + i) : 0.0f;
-                    gr[i] = has ? to_f32(c.gy[R + i]) : 0.0f;
-                }
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    const float a = grad_pre<W>(f + i, w, bias, gr[i], p.silu);
-                    q[i] = R + i < n ? a : 0.0f;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const float a = from_right(gp[i], 0.0f);
-                gp[R + i] = right ? q[i] : ends ? 0.0f : a;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const float a = from_right(gp[i], after[i]);
-                gp[R + i] = ends ? 0.0f : a;
-            }
+            for (int i = 0; i < H; ++i) begin[k & 1][wave][i] = gp[i];
         }
+        lds_barrier();
+        float edge[H];
 #pragma unroll
-        for (int i = 0; i < H; ++i)
-            after[i] = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(gp[i])));
+        for (int i = 0; i < H; ++i) {
+            edge[i] = wave < 3 ? begin[k & 1][wave < 3 ? wave + 1 : 0][i] : after[i];
+            after[i] = begin[k & 1][0][i];   // written again two barriers on
+            gp[R + i] = from_right(gp[i], edge[i]);
+        }
+        if (k == groups - 1 && item + 1 == i1 && n > R) {   // the next item is another workgroup's: its first gradients again
+            const Row<T, X8> in = row_of<T, X8>(p, c.b, d);
+            const T* gy = (const T*)p.gy + c.b * p.sgy[0] + d * p.sgy[1];
+            float f[2 * H], gr[H];
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const int t = c.run * R + R + i;
+                f[i] = v[R - H + i];
+                f[H + i] = t < p.L ? in.at(t) : 0.0f;
+                gr[i] = t < p.L ? to_f32(gy[t]) : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < H; ++i) gp[R + i] = grad_pre<W>(f + i, w, bias, gr[i], p.silu);
+        }
+        if (n < R + H) {   // none after the row's last step
+#pragma unroll
+            for (int i = 0; i < H; ++i) gp[R + i] = R + i < n ? gp[R + i] : 0.0f;
+        }
         if (c.full) {
 #pragma unroll
             for (int j = 0; j < R; ++j) {
@@ -489,13 +523,22 @@ bool row_grid(const ConvParams& p, RowGrid* g) {
     return true;
 }
 
+template <typename T, int W, int UNITS>
+void conv_fwd_u(const ConvParams& p, int tx, int segs, hipStream_t st) {
+    const int rows = UNITS * (256 / tx), dblocks = (p.D + rows - 1) / rows;
+    const dim3 g(segs, std::min(dblocks, 65535), p.B), t(tx, 256 / tx);
+    if (p.o8) conv_fwd_kernel<T, W, false, true, UNITS><<<g, t, 0, st>>>(p, dblocks);
+    else if (p.x8) conv_fwd_kernel<T, W, true, false, UNITS><<<g, t, 0, st>>>(p, dblocks);
+    else conv_fwd_kernel<T, W, false, false, UNITS><<<g, t, 0, st>>>(p, dblocks);
+}
 template <typename T, int W>
 hipError_t conv_fwd_w(const ConvParams& p, hipStream_t st) {
-    RowGrid g;
-    if (!row_grid(p, &g)) return hipErrorInvalidValue;
-    if (p.o8) conv_fwd_kernel<T, W, false, true><<<g.grid, g.block, 0, st>>>(p, g.segs);
-    else if (p.x8) conv_fwd_kernel<T, W, true, false><<<g.grid, g.block, 0, st>>>(p, g.segs);
-    else conv_fwd_kernel<T, W, false, false><<<g.grid, g.block, 0, st>>>(p, g.segs);
+    int tx = 8;   // the lanes of a checkpoint block stay together
+    while (tx < 256 && tx < p.nrun) tx *= 2;
+    const int ty = 256 / tx, segs = (p.nrun + tx - 1) / tx;
+    // two units a workgroup where there are workgroups enough for it
+    if ((int64_t)segs * ((p.D + ty - 1) / ty) * p.B >= 4096) conv_fwd_u<T, W, 2>(p, tx, segs, st);
+    else conv_fwd_u<T, W, 1>(p, tx, segs, st);
     return hipGetLastError();
 }
 template <typename T, int W>

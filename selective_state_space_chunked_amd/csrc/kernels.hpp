@@ -280,6 +280,9 @@ double roof_instrs_per_lane(int kind, int chains, int iters);
 // ------------------ short causal convolution, 8-bit checkpoints ------------
 constexpr int kConvRun = 8;     // consecutive steps of one lane
 constexpr int kCkptBlock = 64;  // steps that share a scale
+// backward: groups of 256 items a workgroup takes at most, and the workgroups there should be before it takes more
+// than one (B=8 D=2048 L=4096 bf16, kernel us with 1, 2, 4, 8 groups: 135, 100, 95, 90)
+constexpr int kConvGroups = 8, kConvWG = 4096;
 struct ConvParams {
     const void* x; const int8_t* x8; const float* x8_scale;
     const float* w; const float* bias; const void* init;
