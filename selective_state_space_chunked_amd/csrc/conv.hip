@@ -169,12 +169,11 @@ template <typename T, int W, bool X8, bool P8, int UNITS>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int dblocks) {
     constexpr int H = W - 1, R = kConvRun;
     const int run = blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.z, t0 = run * R;
-    // the W-1 steps before a lane's own are the left neighbour's last ones, but for these lanes
-    const bool first = lane_id() == 0 || threadIdx.x == 0;
+    // the W-1 steps before a lane's own are the left neighbour's last ones
     for (int db = blockIdx.y; db < dblocks; db += gridDim.y) {
         Run<T> x[UNITS];
         Run8 q[UNITS];
-        float left[UNITS][H], w[UNITS][W], bias[UNITS];
+        float left[UNITS][H], w[UNITS][W], bias[UNITS], halo[UNITS];
         int n[UNITS];
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
@@ -194,12 +193,15 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int dblocks
             bias[u] = p.y && p.bias ? p.bias[dw] : 0.0f;
 #pragma unroll
             for (int i = 0; i < H; ++i) left[u][i] = 0.0f;
-            if (first && n[u] > 0 && p.y) {
-                if (run > 0 || p.init) {
+            if (p.init && run == 0 && n[u] > 0) {
+                const T* init = (const T*)p.init + ((int64_t)b * p.D + d) * H;
 #pragma unroll
-                    for (int i = 0; i < H; ++i) left[u][i] = in.at(t0 - H + i);
-                }
+                for (int i = 0; i < H; ++i) left[u][i] = to_f32(init[i]);
             }
+            // lane i < H: the input H - i steps before lane 0's run, where the wave begins inside a row
+            const int th = uniform(t0) - H + lane_id(), n0 = uniform(n[u]), d0 = uniform(d);
+            halo[u] = 0.0f;
+            if (lane_id() < H && th >= 0 && n0 > 0 && p.y) halo[u] = row_of<T, X8>(p, b, d0).at(th);
         }
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
@@ -244,8 +246,9 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int dblocks
             if (!p.y) continue;
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                e[i] = from_left(v[R - H + i], 0.0f);
-                e[i] = first ? left[u][i] : e[i];
+                const float edge = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(halo[u]), i));
+                e[i] = from_left(v[R - H + i], edge);
+                e[i] = run == 0 ? left[u][i] : e[i];
             }
 #pragma unroll
             for (int j = 0; j < R; ++j) e[H + j] = v[j];
