@@ -24,18 +24,31 @@ __device__ __forceinline__ float sigmoid_f(float v) {
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// Accesses of 16 and 8 bytes at any element's address (global memory takes them unaligned): rows need not
+// start at 16-byte units.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2), aligned(1)));
+typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
+
 // a run to a stream: float to bf16 by the conversion instruction, to nearest even
-__device__ __forceinline__ void store_stream(float* p, const float (&v)[kConvRun], bool vec, int n) {
-    store_run<kConvRun>(p, v, vec, n);
+__device__ __forceinline__ void store_stream(float* p, const float (&v)[kConvRun], int n) {
+    if (n >= kConvRun) {
+        *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+        for (int j = 0; j < kConvRun; ++j)
+            if (j < n) p[j] = v[j];
+    }
 }
-__device__ __forceinline__ void store_stream(bf16_t* p, const float (&v)[kConvRun], bool vec, int n) {
+__device__ __forceinline__ void store_stream(bf16_t* p, const float (&v)[kConvRun], int n) {
     uint32_t w[kConvRun / 2];
 #pragma unroll
     for (int j = 0; j < kConvRun / 2; ++j)
         w[j] = (uint32_t)__builtin_bit_cast(bf16_t, (__bf16)v[2 * j]) |
                ((uint32_t)__builtin_bit_cast(bf16_t, (__bf16)v[2 * j + 1]) << 16);
-    if (vec && n >= kConvRun) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (n >= kConvRun) {
+        *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
     } else {
 #pragma unroll
         for (int j = 0; j < kConvRun; ++j)
@@ -77,12 +90,6 @@ __device__ __forceinline__ Row<T, X8> row_of(const ConvParams& p, int b, int d) 
     o.W = p.W;
     return o;
 }
-// eight bytes of a checkpoint
-__device__ __forceinline__ void unpack8(const int8_t* q, float scale, float (&v)[kConvRun]) {
-    const uint2 w = *reinterpret_cast<const uint2*>(q);
-#pragma unroll
-    for (int j = 0; j < kConvRun; ++j) v[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3))) * scale;
-}
 // max |x| of a checkpoint block as a bit pattern: of non-negative floats the
 // integers order as the values do, infinity above all numbers and NaN above it.
 __device__ __forceinline__ int block_max(int m) {   // over aligned groups of 8 lanes
@@ -105,14 +112,14 @@ __device__ __forceinline__ float grad_pre(const float* e, const float (&w)[W], f
 // A run of eight steps as loaded, turned into floats where it is used (so loads stay under way meanwhile).
 template <typename T> struct Run;
 template <> struct Run<bf16_t> {
-    uint4 r;
-    __device__ __forceinline__ void load(const bf16_t* p) { r = *reinterpret_cast<const uint4*>(p); }
+    u32x4 r;
+    __device__ __forceinline__ void load(const bf16_t* p) { r = *reinterpret_cast<const u32x4*>(p); }
     __device__ __forceinline__ void load(const bf16_t* p, int n) {   // the first n
         uint32_t w[4] = {};
 #pragma unroll
         for (int j = 0; j < kConvRun; ++j)
             if (j < n) w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
-        r = make_uint4(w[0], w[1], w[2], w[3]);
+        r = u32x4{w[0], w[1], w[2], w[3]};
     }
     __device__ __forceinline__ void get(float (&v)[kConvRun]) const {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -124,17 +131,17 @@ template <> struct Run<bf16_t> {
     }
 };
 template <> struct Run<float> {
-    float4 r[2];
+    f32x4 r[2];
     __device__ __forceinline__ void load(const float* p) {
-        r[0] = *reinterpret_cast<const float4*>(p);
-        r[1] = *reinterpret_cast<const float4*>(p + 4);
+        r[0] = *reinterpret_cast<const f32x4*>(p);
+        r[1] = *reinterpret_cast<const f32x4*>(p + 4);
     }
     __device__ __forceinline__ void load(const float* p, int n) {
         float v[kConvRun];
 #pragma unroll
         for (int j = 0; j < kConvRun; ++j) v[j] = j < n ? p[j] : 0.0f;
-        r[0] = make_float4(v[0], v[1], v[2], v[3]);
-        r[1] = make_float4(v[4], v[5], v[6], v[7]);
+        r[0] = f32x4{v[0], v[1], v[2], v[3]};
+        r[1] = f32x4{v[4], v[5], v[6], v[7]};
     }
     __device__ __forceinline__ void get(float (&v)[kConvRun]) const {
         v[0] = r[0].x; v[1] = r[0].y; v[2] = r[0].z; v[3] = r[0].w;
@@ -142,10 +149,10 @@ template <> struct Run<float> {
     }
 };
 struct Run8 {
-    uint2 r;
+    u32x2 r;
     float s;
     __device__ __forceinline__ void load(const int8_t* p, const float* sc) {
-        r = *reinterpret_cast<const uint2*>(p);
+        r = *reinterpret_cast<const u32x2*>(p);
         s = *sc;
     }
     __device__ __forceinline__ void load(const int8_t* p, const float* sc, int n) {
@@ -154,7 +161,7 @@ struct Run8 {
 #pragma unroll
         for (int j = 0; j < kConvRun; ++j)
             if (j < n) w[j / 4] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
-        r = make_uint2(w[0], w[1]);
+        r = u32x2{w[0], w[1]};
     }
     __device__ __forceinline__ void get(float (&v)[kConvRun]) const {
 #pragma unroll
@@ -181,10 +188,10 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int dblocks
             n[u] = d < p.D && run < p.nrun ? p.L - t0 : 0;
             const Row<T, X8> in = row_of<T, X8>(p, b, n[u] > 0 ? d : 0);
             if (X8) {
-                if (n[u] >= R && p.v8) q[u].load(in.q + t0, in.s + t0 / kCkptBlock);
+                if (n[u] >= R) q[u].load(in.q + t0, in.s + t0 / kCkptBlock);
                 else q[u].load(in.q + t0, in.s + t0 / kCkptBlock, n[u]);
             } else {
-                if (n[u] >= R && p.vx) x[u].load(in.x + t0);
+                if (n[u] >= R) x[u].load(in.x + t0);
                 else x[u].load(in.x + t0, n[u]);
             }
             const int dw = n[u] > 0 && p.y ? d : 0;
@@ -228,8 +235,8 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int dblocks
                         if (j < 4) w0 |= (uint32_t)(k & 255) << (8 * j);
                         else w1 |= (uint32_t)(k & 255) << (8 * (j - 4));
                     }
-                    if (p.v8) {
-                        *reinterpret_cast<uint2*>(o) = make_uint2(w0, w1);
+                    if (n[u] >= R) {
+                        *reinterpret_cast<u32x2*>(o) = u32x2{w0, w1};
                     } else {
 #pragma unroll
                         for (int j = 0; j < R; ++j)
@@ -261,7 +268,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int dblocks
                 for (int k = 0; k < W; ++k) a = fmaf(w[u][k], e[j + k], a);
                 o[j] = p.silu ? a * sigmoid_f(a) : a;
             }
-            store_stream((T*)p.y + b * p.sy[0] + d * p.sy[1] + t0, o, p.vy, n[u]);
+            store_stream((T*)p.y + b * p.sy[0] + d * p.sy[1] + t0, o, n[u]);
         }
     }
 }
@@ -303,13 +310,13 @@ struct BwdTile {
         full = __all(n >= R);
         const Row<T, X8> in = row_of<T, X8>(p, b, d);
         const T* gy = (const T*)p.gy + b * p.sgy[0] + d * p.sgy[1] + run * R;
-        if (full && p.vgy) g.load(gy);
+        if (full) g.load(gy);
         else g.load(gy, n);
         if (X8) {
-            if (full && p.v8) q.load(in.q + run * R, in.s + run * R / kCkptBlock);
+            if (full) q.load(in.q + run * R, in.s + run * R / kCkptBlock);
             else q.load(in.q + run * R, in.s + run * R / kCkptBlock, n);
         } else {
-            if (full && p.vx) x.load(in.x + run * R);
+            if (full) x.load(in.x + run * R);
             else x.load(in.x + run * R, n);
         }
         const int t0 = uniform(run) * R - H + lane;   // in lane 0's row
@@ -443,8 +450,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
                     if (j < n && j + H >= n) o[j] += to_f32(gl[j + H - n]);
             }
             T* gx = (T*)p.gx + c.b * p.sgx[0] + d * p.sgx[1] + c.run * R;
-            if (c.full) store_stream(gx, o, p.vgx, R);
-            else store_stream(gx, o, p.vgx, n);
+            if (c.full) store_stream(gx, o, R);
+            else store_stream(gx, o, n);
         }
         if (p.ginit && c.run == 0 && n > 0) {
             T* gi = (T*)p.ginit + row * H;
@@ -488,60 +495,71 @@ __global__ __launch_bounds__(256) void conv_reduce_kernel(ConvParams p) {
     else if (p.gbias) p.gbias[d] = a;
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void ckpt8_unpack_kernel(ConvParams p, int segs) {
-    const int64_t rb = blockIdx.x / segs;
-    const int run = (int)(blockIdx.x % segs) * blockDim.x + threadIdx.x;
-    const int64_t row = rb * blockDim.y + threadIdx.y;
-    if (row >= (int64_t)p.B * p.D || run >= p.nrun) return;
-    const int b = (int)(row / p.D), d = (int)(row % p.D), t0 = run * kConvRun;
-    const int8_t* q = p.x8 + row * p.L + t0;
-    const float s = p.x8_scale[row * p.nblk + run / 8];
-    const int n = p.L - t0;
-    float v[kConvRun];
-    if (p.v8) {
-        unpack8(q, s, v);
-    } else {
+// the stream that a checkpoint stands for; workgroups as in the forward
+template <typename T, int UNITS>
+__global__ __launch_bounds__(256) void ckpt8_unpack_kernel(ConvParams p, int dblocks) {
+    constexpr int R = kConvRun;
+    const int run = blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.z, t0 = run * R;
+    for (int db = blockIdx.y; db < dblocks; db += gridDim.y) {
+        Run8 q[UNITS];
+        int n[UNITS];
 #pragma unroll
-        for (int j = 0; j < kConvRun; ++j) v[j] = j < n ? (float)q[j] * s : 0.0f;
+        for (int u = 0; u < UNITS; ++u) {
+            const int d = (db * UNITS + u) * blockDim.y + threadIdx.y;
+            n[u] = d < p.D && run < p.nrun ? p.L - t0 : 0;
+            const int64_t row = (int64_t)b * p.D + (n[u] > 0 ? d : 0);
+            const int8_t* x8 = p.x8 + row * p.L + t0;
+            const float* s = p.x8_scale + row * p.nblk + run / (kCkptBlock / R);
+            if (n[u] >= R) q[u].load(x8, s);
+            else q[u].load(x8, s, n[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int d = (db * UNITS + u) * blockDim.y + threadIdx.y;
+            float v[R];
+            q[u].get(v);
+            if (n[u] > 0) store_stream((T*)p.y + b * p.sy[0] + d * p.sy[1] + t0, v, n[u]);
+        }
     }
-    store_stream((T*)p.y + b * p.sy[0] + d * p.sy[1] + t0, v, p.vy, n);
 }
 
-// lanes along the row and rows per workgroup; blocks along the row
+// Lanes along a row's runs (at least 8: the lanes of a checkpoint block stay together), and whether there are
+// workgroups enough to take two units each.
 struct RowGrid {
-    dim3 block;
-    int segs;
-    unsigned grid;
+    int tx, segs;
+    bool two;
+    explicit RowGrid(const ConvParams& p) {
+        tx = 8;
+        while (tx < 256 && tx < p.nrun) tx *= 2;
+        const int ty = 256 / tx;
+        segs = (p.nrun + tx - 1) / tx;
+        two = (int64_t)segs * ((p.D + ty - 1) / ty) * p.B >= 4096;
+    }
+    dim3 block() const { return dim3(tx, 256 / tx); }
+    int dblocks(const ConvParams& p, int units) const { return (p.D + units * (256 / tx) - 1) / (units * (256 / tx)); }
+    dim3 grid(const ConvParams& p, int units) const { return dim3(segs, std::min(dblocks(p, units), 65535), p.B); }
 };
-bool row_grid(const ConvParams& p, RowGrid* g) {
-    int tx = 8;   // the lanes of a checkpoint block stay together
-    while (tx < 256 && tx < p.nrun) tx *= 2;
-    g->block = dim3(tx, 256 / tx);
-    g->segs = (p.nrun + tx - 1) / tx;
-    const int64_t rows = (int64_t)p.B * p.D, per = 256 / tx;
-    const int64_t blocks = (rows + per - 1) / per * g->segs;
-    if (blocks <= 0 || blocks >= (1LL << 31)) return false;
-    g->grid = (unsigned)blocks;
-    return true;
-}
 
 template <typename T, int W, int UNITS>
-void conv_fwd_u(const ConvParams& p, int tx, int segs, hipStream_t st) {
-    const int rows = UNITS * (256 / tx), dblocks = (p.D + rows - 1) / rows;
-    const dim3 g(segs, std::min(dblocks, 65535), p.B), t(tx, 256 / tx);
-    if (p.o8) conv_fwd_kernel<T, W, false, true, UNITS><<<g, t, 0, st>>>(p, dblocks);
-    else if (p.x8) conv_fwd_kernel<T, W, true, false, UNITS><<<g, t, 0, st>>>(p, dblocks);
-    else conv_fwd_kernel<T, W, false, false, UNITS><<<g, t, 0, st>>>(p, dblocks);
+void conv_fwd_u(const ConvParams& p, const RowGrid& r, hipStream_t st) {
+    const dim3 g = r.grid(p, UNITS), t = r.block();
+    const int db = r.dblocks(p, UNITS);
+    if (p.o8) conv_fwd_kernel<T, W, false, true, UNITS><<<g, t, 0, st>>>(p, db);
+    else if (p.x8) conv_fwd_kernel<T, W, true, false, UNITS><<<g, t, 0, st>>>(p, db);
+    else conv_fwd_kernel<T, W, false, false, UNITS><<<g, t, 0, st>>>(p, db);
 }
 template <typename T, int W>
 hipError_t conv_fwd_w(const ConvParams& p, hipStream_t st) {
-    int tx = 8;   // the lanes of a checkpoint block stay together
-    while (tx < 256 && tx < p.nrun) tx *= 2;
-    const int ty = 256 / tx, segs = (p.nrun + tx - 1) / tx;
-    // two units a workgroup where there are workgroups enough for it
-    if ((int64_t)segs * ((p.D + ty - 1) / ty) * p.B >= 4096) conv_fwd_u<T, W, 2>(p, tx, segs, st);
-    else conv_fwd_u<T, W, 1>(p, tx, segs, st);
+    const RowGrid r(p);
+    if (r.two) conv_fwd_u<T, W, 2>(p, r, st);
+    else conv_fwd_u<T, W, 1>(p, r, st);
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t unpack_t(const ConvParams& p, hipStream_t st) {
+    const RowGrid r(p);
+    if (r.two) ckpt8_unpack_kernel<T, 2><<<r.grid(p, 2), r.block(), 0, st>>>(p, r.dblocks(p, 2));
+    else ckpt8_unpack_kernel<T, 1><<<r.grid(p, 1), r.block(), 0, st>>>(p, r.dblocks(p, 1));
     return hipGetLastError();
 }
 template <typename T, int W>
@@ -571,11 +589,7 @@ hipError_t launch_conv_reduce(const ConvParams& p, hipStream_t st) {
     return hipGetLastError();
 }
 hipError_t launch_ckpt8_unpack(const ConvParams& p, int dtype, hipStream_t st) {
-    RowGrid g;
-    if (!row_grid(p, &g)) return hipErrorInvalidValue;
-    if (dtype == 1) ckpt8_unpack_kernel<bf16_t><<<g.grid, g.block, 0, st>>>(p, g.segs);
-    else ckpt8_unpack_kernel<float><<<g.grid, g.block, 0, st>>>(p, g.segs);
-    return hipGetLastError();
+    return dtype == 1 ? unpack_t<bf16_t>(p, st) : unpack_t<float>(p, st);
 }
 
 }  // namespace ssm

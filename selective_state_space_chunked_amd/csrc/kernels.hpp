@@ -293,8 +293,6 @@ struct ConvParams {
     int64_t sx[2], sy[2], sgy[2], sgx[2];   // batch, channel strides (steps contiguous)
     int B, D, L, W, silu, nrun, nblk;
     int parts, per_part;             // backward: items (batch row, run) of a channel per workgroup
-    int vx, vy, vgy, vgx;            // 16-byte accesses of each stream
-    int v8;                          // 8-byte accesses of the 8-bit checkpoint
 };
 hipError_t launch_conv_fwd(const ConvParams& p, int dtype, hipStream_t st);
 hipError_t launch_conv_bwd(const ConvParams& p, int dtype, hipStream_t st);
@@ -310,7 +308,7 @@ struct TokConvParams {
     const void* x; const float* w; const float* bias; void* pool; void* y;
     Sequences q;
     int64_t sx, sy, spool;
-    int D, W, silu, vec;
+    int D, W, silu;
 };
 struct TokScanParams {
     const void* delta; const void* x; const float* A; const void* Bm; const void* C;

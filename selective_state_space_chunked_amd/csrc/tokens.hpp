@@ -54,48 +54,87 @@ __device__ __forceinline__ int find_seq(const int32_t* start, int S, int t) {
     return lo + __popcll(__ballot(i < hi && start[i < hi ? i : lo] <= t)) - 1;
 }
 
+// The slot that sequence s names, or -1 where it is outside the pool.
+__device__ __forceinline__ int slot_named(const Sequences& q, int s) {
+    const int v = q.slot ? q.slot[s] : s;
+    return v >= 0 && v < q.slots ? v : -1;
+}
+// Whether an earlier sequence of the call has the same slot.  Called by whole waves with one s.
+__device__ __forceinline__ bool slot_taken(const Sequences& q, int s, int v) {
+    if (!q.slot) return false;
+    bool taken = false;
+    for (int i = lane_id(); i < s; i += 256) {   // four probes under way
+        int u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = i + 64 * k < s ? q.slot[i + 64 * k] : -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) taken |= u[k] == v;
+    }
+    return __ballot(taken) != 0;
+}
 // The slot of sequence s, or -1 for an empty place: a slot outside the pool, or
 // one that an earlier sequence of the call has.  Called by whole waves with one s.
 __device__ __forceinline__ int slot_of(const Sequences& q, int s) {
-    if (!q.slot) return s < q.slots ? s : -1;
-    const int v = q.slot[s];
-    if (v < 0 || v >= q.slots) return -1;
-    bool taken = false;
-    for (int i = lane_id(); i < s; i += 64) taken |= q.slot[i] == v;
-    return __ballot(taken) ? -1 : v;
+    const int v = uniform(slot_named(q, s));
+    return v < 0 || slot_taken(q, s, v) ? -1 : v;
 }
 
-// V consecutive elements: one 16-byte access (V elements of T are 16 bytes), or one element
-template <typename T, int V>
-__device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
-    if (V == 1) {
-        v[0] = to_f32(p[0]);
-    } else if (sizeof(T) == 4) {
-        const float4 w = *reinterpret_cast<const float4*>(p);
-        v[0] = w.x; v[1 % V] = w.y; v[2 % V] = w.z; v[3 % V] = w.w;
-    } else {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+// Sixteen bytes of consecutive elements at any element's address (global memory
+// takes unaligned accesses), as floats and back.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+    static constexpr int V = 4;
+    f32x4 r;
+    __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const f32x4*>(p); }
+    __device__ __forceinline__ void load(const float* p, int n) {   // the first n, the others 0
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[(2 * e) % V] = __uint_as_float(ws[e] << 16);
-            v[(2 * e + 1) % V] = __uint_as_float(ws[e] & 0xffff0000u);
-        }
+        for (int e = 0; e < 4; ++e) r[e] = e < n ? p[e] : 0.0f;
     }
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
-    if (V == 1) {
-        p[0] = from_f32<T>(v[0]);
-    } else if (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1 % V], v[2 % V], v[3 % V]);
-    } else {
-        uint32_t w[4];
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = r[e];
+    }
+    __device__ __forceinline__ void set(const float (&v)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = v[e];
+    }
+    __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<f32x4*>(p) = r; }
+    __device__ __forceinline__ void store(float* p, int n) const {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            w[e] = (uint32_t)from_f32<bf16_t>(v[(2 * e) % V]) | ((uint32_t)from_f32<bf16_t>(v[(2 * e + 1) % V]) << 16);
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (e < n) p[e] = r[e];
     }
-}
+};
+template <> struct Vec<bf16_t> {
+    static constexpr int V = 8;
+    u32x4 r;
+    __device__ __forceinline__ void load(const bf16_t* p) { r = *reinterpret_cast<const u32x4*>(p); }
+    __device__ __forceinline__ void load(const bf16_t* p, int n) {
+        r = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) r[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(r[e] << 16);
+            v[2 * e + 1] = __uint_as_float(r[e] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            r[e] = (uint32_t)to_stream<bf16_t>(v[2 * e]) | ((uint32_t)to_stream<bf16_t>(v[2 * e + 1]) << 16);
+    }
+    __device__ __forceinline__ void store(bf16_t* p) const { *reinterpret_cast<u32x4*>(p) = r; }
+    __device__ __forceinline__ void store(bf16_t* p, int n) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) p[e] = (bf16_t)(r[e / 2] >> (16 * (e & 1)));
+    }
+};
 
 }  // namespace ssm

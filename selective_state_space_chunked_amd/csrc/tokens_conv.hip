@@ -1,6 +1,11 @@
 // The short causal convolution over packed rows: the tokens of all sequences of
-// a call are the rows of one matrix, lanes run along the channels, and each
-// sequence's last W-1 inputs come from and return to its slot of a pool.
+// a call are the rows of one matrix, and each sequence's last W-1 inputs come
+// from and return to its slot of a pool.
+//
+// A lane takes 16 bytes of neighbouring channels (8 in bf16, 4 in fp32), so a
+// wave reads and writes whole lines of a row, and keeps the W-1 inputs before
+// its row in registers while it walks down a run of rows.  A few operations an
+// element: bound by HBM, single tokens by the latency of their loads.
 #include <algorithm>
 
 #include "tokens.hpp"
@@ -8,132 +13,160 @@
 namespace ssm {
 namespace {
 
-// ---------------------------------------------------------------------------
-// convolution
-// ---------------------------------------------------------------------------
-// A wave takes 64 * V channels of a run of kTokRun rows.  A sequence's first
-// W-1 rows and its new state belong to the run its first row lies in (which then
-// reaches past its end where the sequence starts in its last rows), so only
-// that wave reads and writes the slot.
-constexpr int kTokRun = 16;
+// A wave takes the runs of kTokRun rows.  A sequence's first W-1 rows and its new
+// state belong to the run its first row lies in (which then reaches past its end
+// where the sequence starts in its last rows), so only that wave reads and
+// writes the slot.
+constexpr int kTokRun = 32;
+constexpr int kTokGrp = 4;   // rows whose loads are issued together
 
-template <typename T, int W, int V>
+// FULL: every lane has all its channels.
+template <typename T, int W, bool FULL>
 struct ConvLane {
-    const T* x; T* y; T* pool;
+    static constexpr int V = Vec<T>::V, H = W - 1;
+    const T* x;
+    T *y, *pool;
     int64_t sx, sy, spool;
     float w[V][W], bias[V];
-    int silu;
-    bool act;
-    float win[W - 1][V];   // the W-1 inputs before the next row
+    int silu, cnt;     // channels of the lane, 0 past the last one
+    float win[H][V];   // the inputs before the next row
 
-    __device__ __forceinline__ void load_row(int t, float (&v)[V]) const { load_v<T, V>(x + t * sx, v); }
-    __device__ __forceinline__ void step(int t) {
+    __device__ __forceinline__ ConvLane(const TokConvParams& p, int c0) {
+        cnt = max(min(V, p.D - c0), 0);
+        const int c = cnt > 0 ? c0 : 0;
+        x = (const T*)p.x + c;
+        y = (T*)p.y + c;
+        pool = (T*)p.pool + (int64_t)c * H;
+        sx = p.sx; sy = p.sy; spool = p.spool; silu = p.silu;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int ci = FULL || i < cnt ? c + i : c;
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[i][k] = p.w[(int64_t)ci * W + k];
+            bias[i] = p.bias ? p.bias[ci] : 0.0f;
+        }
+    }
+    __device__ __forceinline__ void load_row(int t, Vec<T>& v) const {
+        if (FULL) v.load(x + t * sx);
+        else v.load(x + t * sx, cnt);
+    }
+    __device__ __forceinline__ void row(int t, const Vec<T>& r) {
         float v[V], o[V];
-        load_row(t, v);
+        r.get(v);
 #pragma unroll
         for (int c = 0; c < V; ++c) {
             float a = bias[c];
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) a = fmaf(w[c][k], win[k][c], a);
-            a = fmaf(w[c][W - 1], v[c], a);
+            for (int k = 0; k < H; ++k) a = fmaf(w[c][k], win[k][c], a);
+            a = fmaf(w[c][H], v[c], a);
             o[c] = silu ? a * sigmoid_f(a) : a;
 #pragma unroll
-            for (int k = 0; k + 1 < W - 1; ++k) win[k][c] = win[k + 1][c];
-            win[W - 2][c] = v[c];
+            for (int k = 0; k + 1 < H; ++k) win[k][c] = win[k + 1][c];
+            win[H - 1][c] = v[c];
         }
-        if (act) store_v<T, V>(y + t * sy, o);
+        Vec<T> q;
+        q.set(o);
+        if (FULL) q.store(y + t * sy);
+        else q.store(y + t * sy, cnt);
     }
-    // the slot's inputs (or zeros), oldest first
-    __device__ __forceinline__ void load_state(int slot, bool fresh, float (&h)[V * (W - 1)]) const {
+    // rows [t0, t1): the next group's loads are under way while a group is computed
+    __device__ __forceinline__ void walk(int t0, int t1) {
+        Vec<T> r[kTokGrp], nx[kTokGrp];
+        auto load = [&](int t, Vec<T>(&v)[kTokGrp]) {
 #pragma unroll
-        for (int i = 0; i < V * (W - 1); ++i) h[i] = 0.0f;
-        if (fresh) return;
+            for (int g = 0; g < kTokGrp; ++g)
+                if (t + g < t1) load_row(t + g, v[g]);
+        };
+        load(t0, r);
+        for (int t = t0; t < t1; t += kTokGrp) {
+            if (t + kTokGrp < t1) load(t + kTokGrp, nx);
+#pragma unroll
+            for (int g = 0; g < kTokGrp; ++g)
+                if (t + g < t1) row(t + g, r[g]);
+#pragma unroll
+            for (int g = 0; g < kTokGrp; ++g) r[g] = nx[g];
+        }
+    }
+    // the slot's inputs, [channel][oldest first]
+    __device__ __forceinline__ void load_state(int slot, Vec<T> (&h)[H]) const {
         const T* s = pool + slot * spool;
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) {
-            float v[V];
-            load_v<T, V>(s + i * V, v);
-#pragma unroll
-            for (int c = 0; c < V; ++c) h[i * V + c] = v[c];
+        for (int i = 0; i < H; ++i) {
+            if (FULL) h[i].load(s + i * V);
+            else h[i].load(s + i * V, cnt * H - i * V);
         }
     }
-    __device__ __forceinline__ void store_state(int slot, const float (&h)[V * (W - 1)]) const {
-        if (!act) return;
+    __device__ __forceinline__ void store_state(int slot, const float (&h)[V * H]) const {
         T* s = pool + slot * spool;
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) {
+        for (int i = 0; i < H; ++i) {
             float v[V];
 #pragma unroll
             for (int c = 0; c < V; ++c) v[c] = h[i * V + c];
-            store_v<T, V>(s + i * V, v);
+            Vec<T> q;
+            q.set(v);
+            if (FULL) q.store(s + i * V);
+            else q.store(s + i * V, cnt * H - i * V);
         }
     }
-};
-
-template <typename T, int W, int V, bool STEP>
-__global__ __launch_bounds__(256) void tok_conv_kernel(TokConvParams p, int cblocks) {
-    const int cb = blockIdx.x % cblocks;
-    const int64_t unit = (int64_t)(blockIdx.x / cblocks) * 4 + (threadIdx.x >> 6);   // run of rows, or sequence
-    const int c0 = (cb * 64 + lane_id()) * V;
-    ConvLane<T, W, V> l;
-    l.act = c0 < p.D;
-    const int c = l.act ? c0 : 0;
-    l.x = (const T*)p.x + c; l.y = (T*)p.y + c; l.pool = (T*)p.pool + (int64_t)c * (W - 1);
-    l.sx = p.sx; l.sy = p.sy; l.spool = p.spool; l.silu = p.silu;
+    // The window a sequence begins with and the state it leaves: its last H inputs, of the rows and, where it is
+    // shorter, the state before.
+    __device__ __forceinline__ void begin(const Vec<T> (&old)[H], bool fresh, int st, int len, float (&nh)[V * H]) {
+        float h[V * H];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < H; ++i) {
+            float v[V];
+            old[i].get(v);
 #pragma unroll
-        for (int k = 0; k < W; ++k) l.w[i][k] = p.w[(int64_t)(c + i) * W + k];
-        l.bias[i] = p.bias ? p.bias[c + i] : 0.0f;
-    }
-    float h[V * (W - 1)];
-    auto begin = [&](int s, int slot, int st, int len) {   // window and new state of a sequence
-        l.load_state(slot, p.q.fresh && p.q.fresh[s], h);
+            for (int c = 0; c < V; ++c) h[i * V + c] = fresh ? 0.0f : v[c];
+        }
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i)
+        for (int i = 0; i < H; ++i)
 #pragma unroll
-            for (int e = 0; e < V; ++e) l.win[i][e] = h[e * (W - 1) + i];
-        float nh[V * (W - 1)];
+            for (int e = 0; e < V; ++e) win[i][e] = h[e * H + i];
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) {
-            const int at = len - (W - 1) + i;   // place of the input in the sequence
+        for (int i = 0; i < H; ++i) {
+            const int at = len - H + i;   // place of the input in the sequence
             float v[V];
             if (at >= 0) {
-                l.load_row(st + at, v);
+                Vec<T> r;
+                load_row(st + at, r);
+                r.get(v);
             } else {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     v[e] = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < W - 1; ++k) v[e] = k == len + i ? h[e * (W - 1) + k] : v[e];
+                    for (int k = 0; k < H; ++k) v[e] = k == len + i ? h[e * H + k] : v[e];
                 }
             }
 #pragma unroll
-            for (int e = 0; e < V; ++e) nh[e * (W - 1) + i] = v[e];
+            for (int e = 0; e < V; ++e) nh[e * H + i] = v[e];
         }
-        l.store_state(slot, nh);
-    };
-    if (STEP) {
-        if (unit >= p.q.S) return;
-        const int slot = slot_of(p.q, (int)unit);
-        if (slot < 0) return;
-        begin((int)unit, slot, (int)unit, 1);
-        l.step((int)unit);
-        return;
     }
+};
+
+template <typename T, int W, bool FULL>
+__device__ __forceinline__ void rows_of_wave(const TokConvParams& p, int c0, int64_t unit) {
+    ConvLane<T, W, FULL> l(p, c0);
+    constexpr int H = W - 1, V = Vec<T>::V;
     const int r0 = (int)min(unit * kTokRun, (int64_t)p.q.T), r1 = min(r0 + kTokRun, p.q.T);
     if (r0 >= r1) return;
     const int32_t* start = p.q.start;
-    int s = find_seq(start, p.q.S, r0);
+    int s = uniform(find_seq(start, p.q.S, r0));
     if (s >= p.q.S) return;
     if (s >= 0) {   // the sequence that runs into this range
-        const int st = start[s], en = min(start[s + 1], p.q.T);
+        const int st = uniform(start[s]), en = uniform(min(start[s + 1], p.q.T));
         if (st >= 0 && st < r0) {
-            const int t0 = max(r0, st + W - 1), t1 = min(en, r1);
+            const int t0 = max(r0, st + H), t1 = min(en, r1);
             if (t0 < t1 && slot_of(p.q, s) >= 0) {
 #pragma unroll
-                for (int i = 0; i < W - 1; ++i) l.load_row(t0 - (W - 1) + i, l.win[i]);
-                for (int t = t0; t < t1; ++t) l.step(t);
+                for (int i = 0; i < H; ++i) {
+                    Vec<T> r;
+                    l.load_row(t0 - H + i, r);
+                    r.get(l.win[i]);
+                }
+                l.walk(t0, t1);
             }
         }
         if (st < r0) ++s;
@@ -141,34 +174,65 @@ __global__ __launch_bounds__(256) void tok_conv_kernel(TokConvParams p, int cblo
         s = 0;
     }
     for (; s < p.q.S; ++s) {   // sequences whose first row lies in this range
-        const int st = start[s];
+        const int st = uniform(start[s]);
         if (st >= r1) break;
-        const int en = min(start[s + 1], p.q.T);
+        const int en = uniform(min(start[s + 1], p.q.T));
         if (st < r0 || en <= st) continue;
-        const int slot = slot_of(p.q, s);
+        const int slot = uniform(slot_of(p.q, s));
         if (slot < 0) continue;
-        begin(s, slot, st, en - st);
-        const int t1 = min(en, max(r1, st + W - 1));
-        for (int t = st; t < t1; ++t) l.step(t);
+        Vec<T> old[H];
+        float nh[V * H];
+        l.load_state(slot, old);
+        l.begin(old, p.q.fresh && p.q.fresh[s], st, en - st, nh);
+        l.store_state(slot, nh);
+        l.walk(st, min(en, max(r1, st + H)));
     }
+}
+template <typename T, int W>
+__global__ __launch_bounds__(256) void tok_conv_kernel(TokConvParams p, int cblocks) {
+    constexpr int V = Vec<T>::V;
+    const int cb = blockIdx.x % cblocks;
+    const int64_t unit = (int64_t)(blockIdx.x / cblocks) * 4 + uniform(threadIdx.x >> 6);
+    const int c0 = (cb * 64 + lane_id()) * V;
+    if ((cb + 1) * 64 * V <= p.D) rows_of_wave<T, W, true>(p, c0, unit);
+    else rows_of_wave<T, W, false>(p, c0, unit);
+}
+
+// One row a sequence: the state is loaded from the slot that is named, and what
+// decides whether the sequence has it comes in meanwhile.
+template <typename T, int W, bool FULL>
+__device__ __forceinline__ void step_of_wave(const TokConvParams& p, int c0, int s) {
+    constexpr int H = W - 1, V = Vec<T>::V;
+    const int slot = uniform(slot_named(p.q, s));
+    ConvLane<T, W, FULL> l(p, c0);
+    Vec<T> old[H], r;
+    l.load_row(s, r);
+    if (slot < 0) return;
+    l.load_state(slot, old);
+    const bool fresh = p.q.fresh && p.q.fresh[s];
+    if (slot_taken(p.q, s, slot)) return;
+    float nh[V * H];
+    l.begin(old, fresh, s, 1, nh);
+    l.store_state(slot, nh);
+    l.row(s, r);
+}
+template <typename T, int W>
+__global__ __launch_bounds__(64) void tok_conv_step_kernel(TokConvParams p, int cblocks) {
+    constexpr int V = Vec<T>::V;
+    const int cb = blockIdx.x % cblocks, s = blockIdx.x / cblocks;
+    const int c0 = (cb * 64 + lane_id()) * V;
+    if ((cb + 1) * 64 * V <= p.D) step_of_wave<T, W, true>(p, c0, s);
+    else step_of_wave<T, W, false>(p, c0, s);
 }
 
 template <typename T, int W>
 hipError_t tok_conv_w(const TokConvParams& p, hipStream_t st) {
-    constexpr int V = 16 / (int)sizeof(T);
-    const int64_t v = p.vec ? V : 1;
-    const int64_t cblocks = (p.D + 64 * v - 1) / (64 * v);
-    const int64_t units = p.q.start ? ((int64_t)p.q.T + kTokRun - 1) / kTokRun : p.q.S;
-    const int64_t blocks = cblocks * ((units + 3) / 4);
+    const int64_t wide = 64 * Vec<T>::V, cblocks = (p.D + wide - 1) / wide;
+    const int64_t units = p.q.start ? (((int64_t)p.q.T + kTokRun - 1) / kTokRun + 3) / 4 : p.q.S;
+    const int64_t blocks = cblocks * units;
     if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
-    const unsigned g = (unsigned)blocks;
-    if (p.vec) {
-        if (p.q.start) tok_conv_kernel<T, W, V, false><<<g, 256, 0, st>>>(p, (int)cblocks);
-        else tok_conv_kernel<T, W, V, true><<<g, 256, 0, st>>>(p, (int)cblocks);
-    } else {
-        if (p.q.start) tok_conv_kernel<T, W, 1, false><<<g, 256, 0, st>>>(p, (int)cblocks);
-        else tok_conv_kernel<T, W, 1, true><<<g, 256, 0, st>>>(p, (int)cblocks);
-    }
+    if (p.q.start) tok_conv_kernel<T, W><<<(unsigned)blocks, 256, 0, st>>>(p, (int)cblocks);
+    else tok_conv_step_kernel<T, W><<<(unsigned)blocks, 64, 0, st>>>(p, (int)cblocks);
     return hipGetLastError();
 }
 

@@ -359,7 +359,8 @@ __global__ __launch_bounds__(256) void tok_step_kernel(TokScanParams p, int cblo
     const bool act = d0 < p.D;
     const int d = act ? d0 : 0, n0 = 4 * q, N = p.N;
     const bool four = n0 + 4 <= N;   // VEC: all of a lane's states or (N = 12) none
-    const int slot = uniform(slot_of(p.q, s));
+    // the state is loaded from the slot that is named; whether the sequence has it comes in meanwhile
+    const int slot = uniform(slot_named(p.q, s));
     if (slot < 0) return;
     const int64_t t = s;
     float* pool = p.pool + slot * p.spool + (int64_t)d * N + n0;
@@ -401,6 +402,7 @@ __global__ __launch_bounds__(256) void tok_step_kernel(TokScanParams p, int cblo
             y = fmaf(h[e], c[e], y);
         }
     }
+    if (slot_taken(p.q, s, slot)) return;
     if (Q > 1) y += dpp<SSM_DPP_QUAD(1, 0, 3, 2)>(0.0f, y);
     if (Q > 2) y += dpp<SSM_DPP_QUAD(2, 3, 0, 1)>(0.0f, y);
     if (!act) return;
