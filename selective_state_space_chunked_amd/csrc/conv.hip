@@ -98,6 +98,18 @@ __device__ __forceinline__ int block_max(int m) {   // over aligned groups of 8 
     return max(m, dpp_i<SSM_DPP_ROW_HALF_MIRROR>(0, m));
 }
 
+// rint(v inv) in the low byte: the product rounded to fp32, then to a whole number by adding 1.5 * 2^23 (where
+// the spacing of fp32 is 1), to nearest even both times
+__device__ __forceinline__ uint32_t nearest_byte(float v, float inv) {
+#pragma clang fp contract(off)
+    const float q = v * inv;
+    return __float_as_uint(q + 12582912.0f);
+}
+__device__ __forceinline__ uint32_t four_bytes(const uint32_t* k) {
+    const uint32_t lo = __builtin_amdgcn_perm(k[1], k[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(k[3], k[2], 0x0c0c0400u);
+    return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+
 // gy act'(p) of the step whose window is e[0..W-1]
 template <int W>
 __device__ __forceinline__ float grad_pre(const float* e, const float (&w)[W], float bias, float gy, int silu) {
@@ -163,9 +175,13 @@ struct Run8 {
             if (j < n) w[j / 4] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
         r = u32x2{w[0], w[1]};
     }
+    // q s as (q + 128) s - 128 s: the sum of unsigned bytes is one conversion, and the multiply-add rounds the
+    // exact q s once
     __device__ __forceinline__ void get(float (&v)[kConvRun]) const {
+        const uint32_t w[2] = {r.x ^ 0x80808080u, r.y ^ 0x80808080u};
+        const float off = -128.0f * s;
 #pragma unroll
-        for (int j = 0; j < kConvRun; ++j) v[j] = (float)(int8_t)((j < 4 ? r.x : r.y) >> (8 * (j & 3))) * s;
+        for (int j = 0; j < kConvRun; ++j) v[j] = fmaf((float)((w[j / 4] >> (8 * (j & 3))) & 255u), s, off);
     }
 };
 
@@ -228,13 +244,10 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int dblocks
                 const float inv = bad || zero ? 0.0f : 127.0f / amax;
                 if (n[u] > 0) {
                     int8_t* o = p.o8 + row * p.L + t0;
-                    uint32_t w0 = 0, w1 = 0;
+                    uint32_t k[R];
 #pragma unroll
-                    for (int j = 0; j < R; ++j) {
-                        const int k = bad ? 0 : (int)rintf(v[j] * inv);
-                        if (j < 4) w0 |= (uint32_t)(k & 255) << (8 * j);
-                        else w1 |= (uint32_t)(k & 255) << (8 * (j - 4));
-                    }
+                    for (int j = 0; j < R; ++j) k[j] = nearest_byte(v[j], inv);
+                    const uint32_t w0 = bad ? 0 : four_bytes(k), w1 = bad ? 0 : four_bytes(k + 4);
                     if (n[u] >= R) {
                         *reinterpret_cast<u32x2*>(o) = u32x2{w0, w1};
                     } else {
@@ -273,24 +286,6 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int dblocks
     }
 }
 
-// A lane's item of one channel: batch row and run, item = row * runs + run.  It moves by a workgroup's 256
-// items at a time without a division: q rows and r runs, and one more row where the runs underflow.
-struct Place {
-    int item, b, run;
-    __device__ __forceinline__ void set(int i, int nrun) {
-        item = i;
-        b = i / nrun;
-        run = i - b * nrun;
-    }
-    __device__ __forceinline__ void back(int nrun, int q, int r) {
-        item -= 256;
-        b -= q;
-        run -= r;
-        const bool w = run < 0;
-        b -= w ? 1 : 0;
-        run += w ? nrun : 0;
-    }
-};
 // What a lane has of its run, loaded a step ahead.
 template <typename T, int W, bool X8>
 struct BwdTile {
@@ -300,32 +295,73 @@ struct BwdTile {
     Run<T> g, x;
     Run8 q;
     float halo;         // lane i < H: the input H - i steps before lane 0's run
-
-    __device__ __forceinline__ void load(const ConvParams& p, int d, const Place& at, int end) {
-        const int lane = lane_id();
-        const bool act = at.item < end;
-        b = act ? at.b : 0;
-        run = act ? at.run : 0;
-        n = act ? p.L - run * R : 0;
-        full = __all(n >= R);
-        const Row<T, X8> in = row_of<T, X8>(p, b, d);
-        const T* gy = (const T*)p.gy + b * p.sgy[0] + d * p.sgy[1] + run * R;
-        if (full) g.load(gy);
-        else g.load(gy, n);
-        if (X8) {
-            if (full) q.load(in.q + run * R, in.s + run * R / kCkptBlock);
-            else q.load(in.q + run * R, in.s + run * R / kCkptBlock, n);
-        } else {
-            if (full) x.load(in.x + run * R);
-            else x.load(in.x + run * R, n);
-        }
-        const int t0 = uniform(run) * R - H + lane;   // in lane 0's row
-        halo = 0.0f;
-        if (lane < H && t0 >= 0 && t0 < p.L) halo = row_of<T, X8>(p, uniform(b), d).at(t0);
-    }
+    T* gx;
     __device__ __forceinline__ void get_x(float (&v)[R]) const {
         if (X8) q.get(v);
         else x.get(v);
+    }
+};
+// A lane's item of one channel, batch row and run (item = row * runs + run), and the streams' pointers there.  It
+// moves back by a workgroup's 256 items without a division or a product: q rows and r runs, and one more row where
+// the runs underflow.
+template <typename T, int W, bool X8>
+struct BwdAt {
+    static constexpr int H = W - 1, R = kConvRun;
+    int item, b, run, q, r;
+    const T *x, *gy;
+    const int8_t* x8;
+    const float* s;
+    T* gx;
+    int64_t mx, mg, mo;   // elements back for q rows and r runs
+
+    __device__ __forceinline__ BwdAt(const ConvParams& p, int d, int i) {
+        item = i;
+        b = i / p.nrun;
+        run = i - b * p.nrun;
+        q = 256 / p.nrun;
+        r = 256 - q * p.nrun;
+        x = (const T*)p.x + b * p.sx[0] + d * p.sx[1] + run * R;
+        gy = (const T*)p.gy + b * p.sgy[0] + d * p.sgy[1] + run * R;
+        gx = (T*)p.gx + b * p.sgx[0] + d * p.sgx[1] + run * R;
+        x8 = p.x8 + ((int64_t)b * p.D + d) * p.L + run * R;
+        mx = X8 ? q * ((int64_t)p.D * p.L) + r * R : q * p.sx[0] + r * R;
+        mg = q * p.sgy[0] + r * R;
+        mo = q * p.sgx[0] + r * R;
+    }
+    __device__ __forceinline__ void back(const ConvParams& p) {
+        item -= 256;
+        b -= q;
+        run -= r;
+        const bool w = run < 0;
+        b -= w ? 1 : 0;
+        run += w ? p.nrun : 0;
+        const int64_t row = (int64_t)p.nrun * R;
+        if (X8) x8 -= mx + (w ? (int64_t)p.D * p.L - row : 0);
+        else x -= mx + (w ? p.sx[0] - row : 0);
+        gy -= mg + (w ? p.sgy[0] - row : 0);
+        gx -= mo + (w ? p.sgx[0] - row : 0);
+    }
+    __device__ __forceinline__ void load(const ConvParams& p, int d, int end, BwdTile<T, W, X8>& t) const {
+        const int lane = lane_id();
+        const bool act = item < end;
+        t.b = act ? b : 0;
+        t.run = act ? run : 0;
+        t.n = act ? p.L - run * R : 0;
+        t.full = __all(t.n >= R);
+        t.gx = gx;
+        if (t.full) t.g.load(gy);
+        else t.g.load(gy, t.n);
+        if (X8) {
+            const float* sc = p.x8_scale + ((int64_t)b * p.D + d) * p.nblk + run / (kCkptBlock / R);
+            if (t.full) t.q.load(x8, sc);
+            else t.q.load(x8, sc, t.n);
+        } else {
+            if (t.full) t.x.load(x);
+            else t.x.load(x, t.n);
+        }
+        const int t0 = uniform(t.run) * R - H + lane;   // in lane 0's row
+        t.halo = 0.0f;
+        if (lane < H && t0 >= 0 && t0 < p.L) t.halo = row_of<T, X8>(p, uniform(t.b), d).at(t0);
     }
 };
 
@@ -352,16 +388,15 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
     const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
     __shared__ float begin[2][4][4];   // each wave's first H gradients, of this group and the last one
     float acc[W + 1] = {};
-    const int groups = (i1 - i0 + 255) / 256, q256 = 256 / p.nrun, r256 = 256 - q256 * p.nrun;
+    const int groups = (i1 - i0 + 255) / 256;
     BwdTile<T, W, X8> c, nx;
-    Place at;
-    at.set(i0 + (groups - 1) * 256 + (int)threadIdx.x, p.nrun);
-    c.load(p, d, at, i1);
+    BwdAt<T, W, X8> at(p, d, i0 + (groups - 1) * 256 + (int)threadIdx.x);
+    at.load(p, d, i1, c);
     float after[H] = {};   // wave 3: the first H gradients of the group to the right
     for (int k = groups - 1; k >= 0; --k) {
         if (k > 0) {
-            at.back(p.nrun, q256, r256);
-            nx.load(p, d, at, i1);
+            at.back(p);
+            at.load(p, d, i1, nx);
         }
         const int n = c.n, item = i0 + k * 256 + (int)threadIdx.x;
         float v[R], g[R], e[R + H], gp[R + H];
@@ -449,9 +484,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
                 for (int j = 0; j < R; ++j)
                     if (j < n && j + H >= n) o[j] += to_f32(gl[j + H - n]);
             }
-            T* gx = (T*)p.gx + c.b * p.sgx[0] + d * p.sgx[1] + c.run * R;
-            if (c.full) store_stream(gx, o, R);
-            else store_stream(gx, o, n);
+            if (c.full) store_stream(c.gx, o, R);
+            else store_stream(c.gx, o, n);
         }
         if (p.ginit && c.run == 0 && n > 0) {
             T* gi = (T*)p.ginit + row * H;
