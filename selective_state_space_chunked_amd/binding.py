@@ -11,7 +11,9 @@ the library is missing or a call fails, this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -167,13 +169,12 @@ def lib():
         L.pd_scan_fwd.argtypes = [ctypes.POINTER(PDArgs), ctypes.POINTER(PDFwdOut), _vp, ctypes.c_size_t, _vp]
         L.pd_scan_bwd.argtypes = [ctypes.POINTER(PDArgs), ctypes.POINTER(PDBwdIn), ctypes.POINTER(PDGrads),
                                   _vp, ctypes.c_size_t, _vp]
-        L.ssm_conv_fwd.argtypes = [ctypes.POINTER(ConvArgs), ctypes.POINTER(ConvFwdOut), _vp]
-        L.ssm_conv_bwd.argtypes = [ctypes.POINTER(ConvArgs), _vp, _vp, ctypes.POINTER(ConvGrads), _vp,
-                                   ctypes.c_size_t, _vp]
-        L.ssm_ckpt8_pack.argtypes = [ctypes.POINTER(Ckpt8Args), _vp, _vp, _vp, _vp]
-        L.ssm_ckpt8_unpack.argtypes = [ctypes.POINTER(Ckpt8Args), _vp, _vp, _vp, _vp]
-        L.ssm_tokens_conv.argtypes = [ctypes.POINTER(TokensConvArgs), _vp]
-        L.ssm_tokens_scan.argtypes = [ctypes.POINTER(TokensScanArgs), _vp, ctypes.c_size_t, _vp]
+        L.ssm_conv_fwd.argtypes = [_vp, _vp, _vp]
+        L.ssm_conv_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+        L.ssm_ckpt8_pack.argtypes = [_vp, _vp, _vp, _vp, _vp]
+        L.ssm_ckpt8_unpack.argtypes = [_vp, _vp, _vp, _vp, _vp]
+        L.ssm_tokens_conv.argtypes = [_vp, _vp]
+        L.ssm_tokens_scan.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
         L.ssm_status_string.restype = ctypes.c_char_p
         L.ssm_status_string.argtypes = [ctypes.c_int]
         L.ssm_last_error_detail.restype = ctypes.c_char_p
@@ -671,8 +672,18 @@ def pd_scan_bwd(*, gy, gh_last=None, ckpt=None, want=("gd", "gb", "gC", "gh0"), 
 
 # ---------------------------------------------------------------------------
 # short causal convolution, 8-bit activation checkpoints
+#
+# Single tokens and small layers are bound by what a call costs the host, so
+# these functions check a tensor by one short predicate (the checks that name
+# what is wrong run only where it fails) and pass their structs as packed bytes.
 # ---------------------------------------------------------------------------
 _STREAM = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
+_F32 = torch.float32
+_CONV_ARGS = struct.Struct("@iiqqqqPPPPPPP")      # ConvArgs
+_FOUR_PTRS = struct.Struct("@PPPP")               # ConvFwdOut, ConvGrads
+_CKPT8_ARGS = struct.Struct("@i4xqqqP")           # Ckpt8Args
+_TOKENS_CONV_ARGS = struct.Struct("@iiqqqqqPPPPPPPPqqq")            # TokensConvArgs
+_TOKENS_SCAN_ARGS = struct.Struct("@iiqqqqqPPPPPPPPPPPPPqqqqqqq")   # TokensScanArgs
 
 
 def _stream_code(dtype, name):
@@ -681,66 +692,95 @@ def _stream_code(dtype, name):
     return _STREAM[dtype]
 
 
-class _on_device:
-    """The library launches on the current device: makes the tensors' device current for a call."""
+def _dense(t, name, dtype, shape, dev):
+    """Address of a dense tensor of this type, shape and device; 0 for None."""
+    if t is None:
+        return 0
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape, dev)
+    return t.data_ptr()
 
-    def __init__(self, dev):
+
+def _new(out, key, dtype, shape, dev):
+    """Address of out[key]: the caller's dense tensor, or a new one."""
+    t = out.get(key)
+    if t is None:
+        t = out[key] = torch.empty(shape, dtype=dtype, device=dev) if _allocator is None else _alloc(shape, dtype, dev)
+        return t.data_ptr()
+    return _dense(t, f"out[{key!r}]", dtype, shape, dev)
+
+
+def _streams(views):
+    """The layout of the (B, D, L) streams that are not dense: [(role, tensor), ..] -> Layout or None."""
+    vw = None
+    for role, t in views:
+        if t is not None and not t.is_contiguous():
+            vw = vw or _Views()
+            vw.set(role, t.stride(), _dense_strides(t.shape))
+    return vw.lay if vw is not None and vw.any else None
+
+
+def _launch(dev, fn, *args):
+    """Calls the library on the tensors' device (it launches on the current one) and its current stream."""
+    if dev.type != "cuda":
         _on_gpu(dev)
-        self.dev, self.other = dev.index, None
-
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if self.dev is not None and self.dev != cur:
-            self.other = cur
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        if self.other is not None:
-            torch.cuda.set_device(self.other)
+    cur = torch.cuda.current_device()
+    if dev.index is None or dev.index == cur:
+        rc = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(dev))
+    if rc:
+        _check(rc)
 
 
-def _need_ckpt8(ckpt8, dev=None, shape=None):
+def _need_ckpt8(ckpt8):
     x8, scale = ckpt8
-    _need(x8, "x8", torch.int8, shape, dev)
-    if x8.dim() != 3:
-        raise ValueError(f"x8 has shape {tuple(x8.shape)}; expected (B, D, L)")
+    _need(x8, "x8", torch.int8)
+    if x8 is None or x8.dim() != 3:
+        raise ValueError("x8 must be (B, D, L)")
     Bsz, D, L = x8.shape
-    _need(scale, "x8_scale", torch.float32, (Bsz, D, n_chunks(L, SSM_CKPT8_BLOCK)), x8.device)
+    _need(scale, "x8_scale", _F32, (Bsz, D, n_chunks(L, SSM_CKPT8_BLOCK)), x8.device)
+    if scale is None:
+        raise ValueError("x8_scale is required")
     return x8, scale
 
 
-def _conv_args(x, ckpt8, w, bias, init, silu, dtype):
-    """The input is ``x`` (B, D, L), a strided view or dense, or ``ckpt8`` = (x8, x8_scale)."""
+def _conv_args(x, ckpt8, w, bias, init, silu, st):
+    """Sizes, type and device of a call, and its packed arguments once a layout is known.  The input is ``x``
+    (B, D, L), a strided view or dense, or ``ckpt8`` = (x8, x8_scale)."""
     if (x is None) == (ckpt8 is None):
         raise ValueError("one of x and ckpt8 is the input")
-    x8 = scale = None
+    x8 = scale = 0
     if x is not None:
-        _need(x, "x", view=True)
-        shape, dev, st = x.shape, x.device, x.dtype
-        if dtype is not None and dtype != st:
-            raise TypeError(f"x has dtype {st}, expected {dtype}")
+        if not (isinstance(x, torch.Tensor) and x.dim() == 3 and (x.is_contiguous() or x.shape[2] <= 1
+                                                                  or x.stride(2) == 1)):
+            _need(x, "x", view=True)
+            if x.dim() != 3:
+                raise ValueError(f"x has shape {tuple(x.shape)}; expected (B, D, L)")
+        if st is not None and x.dtype is not st:
+            raise TypeError(f"x has dtype {x.dtype}, expected {st}")
+        shape, dev, st, xp = x.shape, x.device, x.dtype, x.data_ptr()
     else:
-        x8, scale = _need_ckpt8(ckpt8)
-        shape, dev, st = x8.shape, x8.device, dtype
+        q, sc = _need_ckpt8(ckpt8)
+        shape, dev, xp, x8, scale = q.shape, q.device, 0, q.data_ptr(), sc.data_ptr()
         if st is None:
             raise TypeError("dtype is required with ckpt8")
     code = _stream_code(st, "x")
-    if len(shape) != 3:
-        raise ValueError(f"x has shape {tuple(shape)}; expected (B, D, L)")
     Bsz, D, L = shape
-    _need(w, "w", torch.float32, None, dev)
-    if w is None or w.dim() != 2 or w.shape[0] != D:
+    if not (isinstance(w, torch.Tensor) and w.dim() == 2 and w.shape[0] == D):
         raise ValueError(f"w must be (D, W) with D={D}")
     W = w.shape[1]
-    _need(bias, "bias", torch.float32, (D,), dev)
-    _need(init, "init", st, (Bsz, D, W - 1), dev)
-    vw = _Views()
-    if x is not None:
-        vw.set(V_X, x.stride(), _dense_strides(shape))
-    args = ConvArgs(dtype=code, silu=int(bool(silu)), batch=Bsz, channels=D, length=L, width=W, x=_ptr(x), x8=_ptr(x8),
-                    x8_scale=_ptr(scale), w=_ptr(w), bias=_ptr(bias), init=_ptr(init))
-    args._views = vw
-    return args, (Bsz, D, L, W), st, dev
+    wp = _dense(w, "w", _F32, (D, W), dev)
+    bp = _dense(bias, "bias", _F32, (D,), dev)
+    ip = _dense(init, "init", st, (Bsz, D, W - 1), dev)
+
+    def packed(layout):
+        return _CONV_ARGS.pack(code, 1 if silu else 0, Bsz, D, L, W, xp, x8, scale, wp, bp, ip,
+                               0 if layout is None else ctypes.addressof(layout))
+
+    return packed, shape, W, st, dev
 
 
 def conv_fwd(*, x=None, ckpt8=None, w, bias=None, init=None, silu=False, want_y=True, want_last=False,
@@ -752,52 +792,81 @@ def conv_fwd(*, x=None, ckpt8=None, w, bias=None, init=None, silu=False, want_y=
     last (the last W-1 inputs, what a following segment takes as ``init``) and x8, x8_scale (the 8-bit
     checkpoint of x), those requested.  ``ckpt8`` = (x8, x8_scale) takes the place of x, with ``dtype`` that
     of y: the convolution's output again from its checkpoint."""
-    args, (Bsz, D, L, W), st, dev = _conv_args(x, ckpt8, w, bias, init, silu, dtype)
-    out = dict(out or {})
+    packed, shape, W, st, dev = _conv_args(x, ckpt8, w, bias, init, silu, dtype)
+    Bsz, D, L = shape
+    out = dict(out) if out else {}
+    y = last = x8 = scale = 0
     if want_ckpt8 or out.get("x8") is not None or out.get("x8_scale") is not None:
         if x is None:
             raise ValueError("a checkpoint is written from x")
-        _out(out, "x8", (Bsz, D, L), torch.int8, dev)
-        _out(out, "x8_scale", (Bsz, D, n_chunks(L, SSM_CKPT8_BLOCK)), torch.float32, dev)
-    if want_y or out.get("y") is not None:
-        _out(out, "y", (Bsz, D, L), st, dev, view=True)
-        args._views.set(V_Y, out["y"].stride(), _dense_strides((Bsz, D, L)))
+        x8 = _new(out, "x8", torch.int8, (Bsz, D, L), dev)
+        scale = _new(out, "x8_scale", _F32, (Bsz, D, n_chunks(L, SSM_CKPT8_BLOCK)), dev)
+    if out.get("y") is not None:
+        y = _out(out, "y", (Bsz, D, L), st, dev, view=True).data_ptr()
+    elif want_y:
+        y = _new(out, "y", st, (Bsz, D, L), dev)
     if want_last or out.get("last") is not None:
-        _out(out, "last", (Bsz, D, W - 1), st, dev)
-    args.layout = args._views.ptr()
-    o = ConvFwdOut(y=_ptr(out.get("y")), last=_ptr(out.get("last")), x8=_ptr(out.get("x8")),
-                   x8_scale=_ptr(out.get("x8_scale")))
-    with _on_device(dev):
-        _check(lib().ssm_conv_fwd(ctypes.byref(args), ctypes.byref(o), _stream(dev)))
+        last = _new(out, "last", st, (Bsz, D, W - 1), dev)
+    lay = _streams(((V_X, x), (V_Y, out.get("y"))))
+    _launch(dev, lib().ssm_conv_fwd, packed(lay), _FOUR_PTRS.pack(y, last, x8, scale))
     return out
 
 
-def conv_bwd(*, gy, x=None, ckpt8=None, w, bias=None, init=None, silu=False, glast=None,
-             want=("gx", "gw", "gbias", "ginit"), out=None):
+_CONV_GRADS = ("gx", "gw", "gbias", "ginit")
+
+
+@functools.lru_cache(maxsize=1024)
+def _conv_bwd_bytes(Bsz, D, L, W):
+    args = ConvArgs(dtype=SSM_F32, batch=Bsz, channels=D, length=L, width=W, x=256, w=256)   # sizes only
+    n = ctypes.c_size_t(0)
+    _check(lib().ssm_workspace_bytes(SSM_OP_CONV_BWD, ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def _scratch(n, dev):
+    """A workspace of n bytes, 256-byte aligned: (tensor, address)."""
+    if n == 0:
+        return None, 0
+    t = torch.empty((n + 256,), dtype=torch.uint8, device=dev) if _allocator is None else \
+        _alloc((n + 256,), torch.uint8, dev, "workspace")
+    p = t.data_ptr()
+    return t, p + (-p) % 256
+
+
+def conv_bwd(*, gy, x=None, ckpt8=None, w, bias=None, init=None, silu=False, glast=None, want=_CONV_GRADS, out=None):
     """Gradients of <gy, y> + <glast, last> of ``conv_fwd``, from its input or its input's 8-bit checkpoint
     (then those of the values the checkpoint stands for).  Returns a dict of the gradients named in ``want``."""
-    if gy is None:
-        raise ValueError("gy is required")
-    _need(gy, "gy", view=True)
-    args, (Bsz, D, L, W), st, dev = _conv_args(x, ckpt8, w, bias, init, silu, gy.dtype)
-    _need(gy, "gy", st, (Bsz, D, L), dev, view=True)
-    _need(glast, "glast", st, (Bsz, D, W - 1), dev)
-    args._views.set(V_GY, gy.stride(), _dense_strides((Bsz, D, L)))
-    shapes = {"gx": ((Bsz, D, L), st), "gw": ((D, W), torch.float32), "gbias": ((D,), torch.float32),
-              "ginit": ((Bsz, D, W - 1), st)}
-    out = dict(out or {})
-    for k in [k for k in shapes if k in want or out.get(k) is not None] + [k for k in (*want, *out) if k not in shapes]:
-        if k not in shapes:
+    if not isinstance(gy, torch.Tensor):
+        raise ValueError("gy must be a torch.Tensor")
+    packed, shape, W, st, dev = _conv_args(x, ckpt8, w, bias, init, silu, gy.dtype)
+    Bsz, D, L = shape
+    if gy.is_contiguous():
+        gp = _dense(gy, "gy", st, shape, dev)
+    else:
+        gp = _need(gy, "gy", st, shape, dev, view=True).data_ptr()
+    lp = _dense(glast, "glast", st, (Bsz, D, W - 1), dev)
+    out = dict(out) if out else {}
+    for k in (*want, *out):
+        if k not in _CONV_GRADS:
             raise ValueError(f"unknown gradient {k}")
-        _out(out, k, *shapes[k], dev, view=k == "gx")
+    gx = gw = gb = gi = 0
     if out.get("gx") is not None:
-        args._views.set(V_GX, out["gx"].stride(), _dense_strides((Bsz, D, L)))
-    args.layout = args._views.ptr()
-    g = ConvGrads(**{f[0]: _ptr(out.get(f[0])) for f in ConvGrads._fields_})
-    with _on_device(dev):
-        ws, nws = _workspace(SSM_OP_CONV_BWD, ctypes.byref(args), dev)
-        _check(lib().ssm_conv_bwd(ctypes.byref(args), _ptr(gy), _ptr(glast), ctypes.byref(g), _ptr(ws), nws,
-                                  _stream(dev)))
+        gx = _out(out, "gx", shape, st, dev, view=True).data_ptr()
+    elif "gx" in want:
+        gx = _new(out, "gx", st, (Bsz, D, L), dev)
+    if "gw" in want or out.get("gw") is not None:
+        gw = _new(out, "gw", _F32, (D, W), dev)
+    if "gbias" in want or out.get("gbias") is not None:
+        gb = _new(out, "gbias", _F32, (D,), dev)
+    if "ginit" in want or out.get("ginit") is not None:
+        gi = _new(out, "ginit", st, (Bsz, D, W - 1), dev)
+    lay = _streams(((V_X, x), (V_GY, gy), (V_GX, out.get("gx"))))
+    args = packed(lay)
+    if dev.type != "cuda":
+        _on_gpu(dev)
+    nws = _conv_bwd_bytes(Bsz, D, L, W)
+    ws, wp = _scratch(nws, dev)
+    _launch(dev, lib().ssm_conv_bwd, args, gp, lp, _FOUR_PTRS.pack(gx, gw, gb, gi), wp, nws)
     return out
 
 
@@ -809,15 +878,13 @@ def ckpt8_pack(x, *, out=None):
     if x.dim() != 3:
         raise ValueError(f"x has shape {tuple(x.shape)}; expected (B, D, L)")
     Bsz, D, L = x.shape
-    out = dict(out or {})
-    _out(out, "x8", (Bsz, D, L), torch.int8, x.device)
-    _out(out, "x8_scale", (Bsz, D, n_chunks(L, SSM_CKPT8_BLOCK)), torch.float32, x.device)
-    vw = _Views()
-    vw.set(V_X, x.stride(), _dense_strides(x.shape))
-    args = Ckpt8Args(dtype=code, batch=Bsz, channels=D, length=L, layout=vw.ptr())
-    with _on_device(x.device):
-        _check(lib().ssm_ckpt8_pack(ctypes.byref(args), _ptr(x), _ptr(out["x8"]), _ptr(out["x8_scale"]),
-                                    _stream(x.device)))
+    dev = x.device
+    out = dict(out) if out else {}
+    x8 = _new(out, "x8", torch.int8, (Bsz, D, L), dev)
+    scale = _new(out, "x8_scale", _F32, (Bsz, D, n_chunks(L, SSM_CKPT8_BLOCK)), dev)
+    lay = _streams(((V_X, x),))
+    args = _CKPT8_ARGS.pack(code, Bsz, D, L, 0 if lay is None else ctypes.addressof(lay))
+    _launch(dev, lib().ssm_ckpt8_pack, args, x.data_ptr(), x8, scale)
     return out
 
 
@@ -827,51 +894,79 @@ def ckpt8_unpack(x8, x8_scale, *, dtype=torch.float32, out=None):
     x8, x8_scale = _need_ckpt8((x8, x8_scale))
     code = _stream_code(dtype, "dtype")
     Bsz, D, L = x8.shape
+    dev = x8.device
     y = {"y": out}
-    _out(y, "y", (Bsz, D, L), dtype, x8.device, view=True)
+    if out is None:
+        _new(y, "y", dtype, (Bsz, D, L), dev)
+    else:
+        _out(y, "y", (Bsz, D, L), dtype, dev, view=True)
     y = y["y"]
-    vw = _Views()
-    vw.set(V_Y, y.stride(), _dense_strides(y.shape))
-    args = Ckpt8Args(dtype=code, batch=Bsz, channels=D, length=L, layout=vw.ptr())
-    with _on_device(x8.device):
-        _check(lib().ssm_ckpt8_unpack(ctypes.byref(args), _ptr(x8), _ptr(x8_scale), _ptr(y), _stream(x8.device)))
+    lay = _streams(((V_Y, y),))
+    args = _CKPT8_ARGS.pack(code, Bsz, D, L, 0 if lay is None else ctypes.addressof(lay))
+    _launch(dev, lib().ssm_ckpt8_unpack, args, x8.data_ptr(), x8_scale.data_ptr(), y.data_ptr())
     return y
 
 
 # ---------------------------------------------------------------------------
 # packed rows: serving forms with pools of states
 # ---------------------------------------------------------------------------
-def _rows(t, name, dtype, shape, dev):
-    """A matrix of rows; its row stride (rows contiguous, any stride from one to the next)."""
+def _rows(t, name, dtype, T, D, dev):
+    """A matrix of rows: (address, row stride); rows contiguous, any stride from one to the next."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 2 and t.device == dev:
+        r, c = t.shape
+        if r == T and c == D:
+            s0, s1 = t.stride()
+            if s1 == 1 or D <= 1:
+                return t.data_ptr(), s0
     if t is None:
         raise ValueError(f"{name} is required")
-    _need(t, name, dtype, shape, dev, view=True)
-    return t.stride(0)
+    _need(t, name, dtype, (T, D), dev, view=True)
+    return t.data_ptr(), t.stride(0)
+
+
+def _y_rows(out, dtype, T, D, dev):
+    y = out.get("y")
+    if y is None:
+        return _new(out, "y", dtype, (T, D), dev), D
+    p, s = _rows(y, "out['y']", dtype, T, D, dev)
+    if T > 1 and s < D:
+        raise ValueError("out['y']: an output view needs distinct elements (no stride 0)")
+    return p, s
 
 
 def _sequences(T, pool, inner, pool_dtype, dev, seq_start, slot, fresh):
-    """Checks of the sequences of a call; (sequences, slots, pool stride)."""
-    if not isinstance(pool, torch.Tensor) or pool.dim() != 3 or tuple(pool.shape[1:]) != inner:
+    """Checks of the sequences of a call; (sequences, slots, pool stride, addresses of seq_start, slot, fresh)."""
+    if not isinstance(pool, torch.Tensor) or pool.dim() != 3 or pool.shape[1:] != inner:
         raise ValueError(f"pool must be (slots, {inner[0]}, {inner[1]})")
-    if pool.dtype != pool_dtype:
+    if pool.dtype is not pool_dtype:
         raise TypeError(f"pool has dtype {pool.dtype}, expected {pool_dtype}")
     if pool.device != dev:
         raise ValueError(f"pool is on {pool.device}, expected {dev}")
-    slots = pool.shape[0]
-    if pool.numel() and (pool.stride(2) != 1 and inner[1] > 1 or pool.stride(1) != inner[1] and inner[0] > 1):
+    st = pool.stride()
+    if pool.numel() and (st[2] != 1 and inner[1] > 1 or st[1] != inner[1] and inner[0] > 1):
         raise ValueError("pool: every slot must be contiguous")
+    S, start = T, 0
     if seq_start is not None:
         if not isinstance(seq_start, torch.Tensor) or seq_start.dim() != 1 or seq_start.shape[0] < 1:
             raise ValueError("seq_start must be (sequences + 1,)")
         S = seq_start.shape[0] - 1
-        _need(seq_start, "seq_start", torch.int32, None, dev)
-    else:
-        S = T
-    _need(slot, "slot", torch.int32, (S,), dev)
-    if fresh is not None and fresh.dtype not in (torch.bool, torch.uint8):
-        raise TypeError(f"fresh has dtype {fresh.dtype}, expected torch.bool or torch.uint8")
-    _need(fresh, "fresh", None, (S,), dev)
-    return S, slots, pool.stride(0)
+        start = _dense(seq_start, "seq_start", torch.int32, (S + 1,), dev)
+    sl = _dense(slot, "slot", torch.int32, (S,), dev)
+    fr = 0
+    if fresh is not None:
+        if fresh.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"fresh has dtype {fresh.dtype}, expected torch.bool or torch.uint8")
+        fr = _dense(fresh, "fresh", fresh.dtype, (S,), dev)
+    return S, pool.shape[0], st[0], start, sl, fr
+
+
+def _row_input(x):
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("x must be a torch.Tensor")
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}; expected (T, D)")
+    T, D = x.shape
+    return T, D, x.dtype, _stream_code(x.dtype, "x"), x.device
 
 
 def tokens_conv(*, x, w, bias=None, silu=False, pool, seq_start=None, slot=None, fresh=None, out=None):
@@ -881,28 +976,30 @@ def tokens_conv(*, x, w, bias=None, silu=False, pool, seq_start=None, slot=None,
     one row a sequence).  ``pool`` (slots, D, W-1) holds each sequence's last W-1 inputs; sequence s begins
     with slot[s] (zeros where ``fresh``) and leaves its own there, in place.  A slot of -1 marks an empty
     place of the batch, which leaves its row as it was.  Returns a dict with y (T, D)."""
-    if x is None:
-        raise ValueError("x is required")
-    _need(x, "x", view=True)
-    code = _stream_code(x.dtype, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x has shape {tuple(x.shape)}; expected (T, D)")
-    T, D = x.shape
-    dev = x.device
-    _need(w, "w", torch.float32, None, dev)
-    if w is None or w.dim() != 2 or w.shape[0] != D:
+    T, D, st, code, dev = _row_input(x)
+    xp, sx = _rows(x, "x", st, T, D, dev)
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[0] != D:
         raise ValueError(f"w must be (D, W) with D={D}")
     W = w.shape[1]
-    _need(bias, "bias", torch.float32, (D,), dev)
-    S, slots, spool = _sequences(T, pool, (D, W - 1), x.dtype, dev, seq_start, slot, fresh)
-    out = dict(out or {})
-    y = _out(out, "y", (T, D), x.dtype, dev, view=True)
-    args = TokensConvArgs(code, int(bool(silu)), T, D, W, S, slots, x.data_ptr(), w.data_ptr(), _ptr(bias),
-                          _ptr(seq_start), _ptr(slot), _ptr(fresh), pool.data_ptr(), y.data_ptr(), x.stride(0),
-                          y.stride(0), spool)
-    with _on_device(dev):
-        _check(lib().ssm_tokens_conv(ctypes.byref(args), _stream(dev)))
+    wp = _dense(w, "w", _F32, (D, W), dev)
+    bp = _dense(bias, "bias", _F32, (D,), dev)
+    S, slots, spool, start, sl, fr = _sequences(T, pool, (D, W - 1), st, dev, seq_start, slot, fresh)
+    out = dict(out) if out else {}
+    yp, sy = _y_rows(out, st, T, D, dev)
+    args = _TOKENS_CONV_ARGS.pack(code, 1 if silu else 0, T, D, W, S, slots, xp, wp, bp, start, sl, fr,
+                                  pool.data_ptr(), yp, sx, sy, spool)
+    _launch(dev, lib().ssm_tokens_conv, args)
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _tokens_scan_bytes(T, D, N):
+    # sizes only: the sequences do not change what the ranges of rows need
+    args = TokensScanArgs(dtype=SSM_F32, tokens=T, channels=D, state=N, sequences=1, slots=1, seq_start=256,
+                          delta_stride=D, x_stride=D, Bm_stride=N, C_stride=N, y_stride=D, pool_stride=D * N)
+    n = ctypes.c_size_t(0)
+    _check(lib().ssm_workspace_bytes(SSM_OP_TOKENS_SCAN, ctypes.byref(args), ctypes.byref(n)))
+    return n.value
 
 
 def tokens_scan(*, delta, x, A, Bm, C, skip=None, z=None, delta_bias=None, delta_softplus=False, pool,
@@ -913,33 +1010,26 @@ def tokens_scan(*, delta, x, A, Bm, C, skip=None, z=None, delta_bias=None, delta
     ``delta``, ``x``, ``z`` (T, D) and ``Bm``, ``C`` (T, N) may be slices of wider rows; ``pool``
     (slots, D, N) float32 holds the states, in place; ``seq_start``, ``slot`` and ``fresh`` as in
     ``tokens_conv``; ``delta_bias`` and ``delta_softplus`` as in ``scan_fwd``.  Returns a dict with y (T, D)."""
-    if x is None:
-        raise ValueError("x is required")
-    _need(x, "x", view=True)
-    st = x.dtype
-    code = _stream_code(st, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x has shape {tuple(x.shape)}; expected (T, D)")
-    T, D = x.shape
-    dev = x.device
-    _need(A, "A", torch.float32, None, dev)
-    if A is None or A.dim() != 2 or A.shape[0] != D:
+    T, D, st, code, dev = _row_input(x)
+    if not isinstance(A, torch.Tensor) or A.dim() != 2 or A.shape[0] != D:
         raise ValueError(f"A must be (D, N) with D={D}")
     N = A.shape[1]
-    sdelta = _rows(delta, "delta", st, (T, D), dev)
-    sB = _rows(Bm, "Bm", st, (T, N), dev)
-    sC = _rows(C, "C", st, (T, N), dev)
-    sz = _rows(z, "z", st, (T, D), dev) if z is not None else 0
-    _need(skip, "skip", torch.float32, (D,), dev)
-    _need(delta_bias, "delta_bias", torch.float32, (D,), dev)
-    S, slots, spool = _sequences(T, pool, (D, N), torch.float32, dev, seq_start, slot, fresh)
-    out = dict(out or {})
-    y = _out(out, "y", (T, D), st, dev, view=True)
-    args = TokensScanArgs(code, int(bool(delta_softplus)), T, D, N, S, slots, delta.data_ptr(), x.data_ptr(),
-                          A.data_ptr(), Bm.data_ptr(), C.data_ptr(), _ptr(delta_bias), _ptr(skip), _ptr(z),
-                          _ptr(seq_start), _ptr(slot), _ptr(fresh), pool.data_ptr(), y.data_ptr(), sdelta,
-                          x.stride(0), sB, sC, sz, y.stride(0), spool)
-    with _on_device(dev):
-        ws, nws = _workspace(SSM_OP_TOKENS_SCAN, ctypes.byref(args), dev) if seq_start is not None else (None, 0)
-        _check(lib().ssm_tokens_scan(ctypes.byref(args), _ptr(ws), nws, _stream(dev)))
+    xp, sx = _rows(x, "x", st, T, D, dev)
+    dp, sd = _rows(delta, "delta", st, T, D, dev)
+    Bp, sB = _rows(Bm, "Bm", st, T, N, dev)
+    Cp, sC = _rows(C, "C", st, T, N, dev)
+    zp, sz = _rows(z, "z", st, T, D, dev) if z is not None else (0, 0)
+    Ap = _dense(A, "A", _F32, (D, N), dev)
+    kp = _dense(skip, "skip", _F32, (D,), dev)
+    bp = _dense(delta_bias, "delta_bias", _F32, (D,), dev)
+    S, slots, spool, start, sl, fr = _sequences(T, pool, (D, N), _F32, dev, seq_start, slot, fresh)
+    out = dict(out) if out else {}
+    yp, sy = _y_rows(out, st, T, D, dev)
+    args = _TOKENS_SCAN_ARGS.pack(code, 1 if delta_softplus else 0, T, D, N, S, slots, dp, xp, Ap, Bp, Cp, bp, kp, zp,
+                                  start, sl, fr, pool.data_ptr(), yp, sd, sx, sB, sC, sz, sy, spool)
+    if dev.type != "cuda":
+        _on_gpu(dev)
+    nws = _tokens_scan_bytes(T, D, N) if seq_start is not None else 0
+    ws, wp = _scratch(nws, dev)
+    _launch(dev, lib().ssm_tokens_scan, args, wp, nws)
     return out

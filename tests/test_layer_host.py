@@ -234,3 +234,22 @@ def test_reference_scan_is_the_oracles():
                                   np.zeros((T, D)))
     np.testing.assert_allclose(y.T[None], y0, rtol=1e-12, atol=1e-13)   # both in fp64
     np.testing.assert_allclose(pool, h0_last, rtol=1e-12, atol=1e-13)
+
+
+@pytest.mark.parametrize("packed,struct", [("_CONV_ARGS", "ConvArgs"), ("_FOUR_PTRS", "ConvFwdOut"),
+                                           ("_FOUR_PTRS", "ConvGrads"), ("_CKPT8_ARGS", "Ckpt8Args"),
+                                           ("_TOKENS_CONV_ARGS", "TokensConvArgs"),
+                                           ("_TOKENS_SCAN_ARGS", "TokensScanArgs")])
+def test_packed_arguments_are_the_structs(packed, struct):
+    """The bytes the binding passes are the struct's, field by field."""
+    p, c = getattr(B, packed), getattr(B, struct)
+    assert p.size == ctypes.sizeof(c)
+    n = len(p.unpack(bytes(p.size)))
+    fields = [f[0] for f in c._fields_]
+    assert n == len(fields)
+    got = c.from_buffer_copy(p.pack(*range(1, n + 1)))
+    for i, f in enumerate(fields):
+        v = getattr(got, f)
+        if f == "layout":
+            v = ctypes.cast(v, ctypes.c_void_p).value
+        assert v == i + 1, f
