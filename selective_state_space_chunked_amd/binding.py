@@ -721,16 +721,20 @@ def _streams(views):
     return vw.lay if vw is not None and vw.any else None
 
 
+# torch.cuda.current_stream builds a Stream object on every call, which costs more than the rest of a launch here
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _launch(dev, fn, *args):
     """Calls the library on the tensors' device (it launches on the current one) and its current stream."""
     if dev.type != "cuda":
         _on_gpu(dev)
     cur = torch.cuda.current_device()
     if dev.index is None or dev.index == cur:
-        rc = fn(*args, _stream(dev))
+        rc = fn(*args, _raw_stream(cur))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _stream(dev))
+            rc = fn(*args, _raw_stream(dev.index))
     if rc:
         _check(rc)
 

@@ -282,7 +282,7 @@ constexpr int kConvRun = 8;     // consecutive steps of one lane
 constexpr int kCkptBlock = 64;  // steps that share a scale
 // backward: groups of 256 items a workgroup takes at most, and the workgroups there should be before it takes more
 // than one (B=8 D=2048 L=4096 bf16, kernel us with 1, 2, 4, 8 groups: 135, 100, 95, 90)
-constexpr int kConvGroups = 8, kConvWG = 4096;
+constexpr int kConvGroups = 8, kConvWG = 4096, kConvOne = 4;
 struct ConvParams {
     const void* x; const int8_t* x8; const float* x8_scale;
     const float* w; const float* bias; const void* init;
@@ -319,16 +319,21 @@ struct TokScanParams {
     int D, N;
     int vec;                         // steps: 16-byte accesses of the states and of A
     // prompts: ranges of `rows` rows (the last may be shorter); workspace
-    int rows, nrange;
+    int rows, nrange, joined;
     float *h0, *hsum;                // (nrange - 1, N, D) of the sequence that crosses a range's end: its first
                                      // state if it begins there, and its state at the end of the range
     float* dsum;                     // (nrange - 1, D) sum of its step sizes in the range
     int* through;                    // (nrange - 1) whether it runs through the whole range
 };
-// rows a range covers at least, and the waves the ranges are made for: the second pass's registers
-// allow four on each of the 1024 SIMDs.  Measured at 8192 rows x 2048 channels (both passes and the
-// states between, us): 1024 waves 226, 2048 161, 3072 155, 4096 149, 6144 154.
-constexpr int kTokRowsMin = 32;
+// rows a range covers at least
+constexpr int kTokRowsMin = 16;
+// Up to this many ranges a wave of the second pass composes the states before its own by itself; a kernel of
+// its own costs more for so few (333 rows x 200 channels, N = 7, a pass: 19.4 us with it, 16.2 us without; 25 us
+// with ranges of at least 32 rows).
+constexpr int kTokChain = 24;
+// The waves the ranges are made for: the second pass's registers allow four on each of the 1024 SIMDs.
+// Measured at 8192 rows x 2048 channels (both passes and the states between, us): 1024 waves 226, 2048 161,
+// 3072 155, 4096 149, 6144 154.
 constexpr int kTokWaves = 4096;
 hipError_t launch_tok_conv(const TokConvParams& p, int dtype, hipStream_t st);
 hipError_t launch_tok_scan(const TokScanParams& p, int dtype, bool sum, hipStream_t st);

@@ -17,8 +17,8 @@ namespace {
 // state belong to the run its first row lies in (which then reaches past its end
 // where the sequence starts in its last rows), so only that wave reads and
 // writes the slot.
-constexpr int kTokRun = 32;
-constexpr int kTokGrp = 4;   // rows whose loads are issued together
+constexpr int kTokRun = 16;
+constexpr int kTokGrp = 2;   // rows whose loads are issued together
 
 // FULL: every lane has all its channels.
 template <typename T, int W, bool FULL>

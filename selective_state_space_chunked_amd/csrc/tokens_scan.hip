@@ -335,7 +335,17 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_ker
 #pragma unroll
         for (int n = 0; n < N; ++n) l.h[n] = 0.0f;
         if (st < r.r0) {   // from the ranges before: the state that crosses into this one
-            get_range<N>(p.hsum + (int64_t)(c - 1) * N * p.D, p.D, d, l.h);
+            get_range<N>(p.hsum + (int64_t)(p.joined ? c - 1 : st / p.rows) * N * p.D, p.D, d, l.h);
+            if (!p.joined) {
+#pragma unroll 2
+                for (int k = st / p.rows + 1; k < c; ++k) {
+                    float S[N];
+                    get_range<N>(p.hsum + (int64_t)k * N * p.D, p.D, d, S);
+                    const float ds = p.dsum[(int64_t)k * p.D + d];
+#pragma unroll
+                    for (int n = 0; n < N; ++n) l.h[n] = fmaf(__builtin_amdgcn_exp2f(l.a[n] * ds), l.h[n], S[n]);
+                }
+            }
         } else if (en > r.r1) {
             get_range<N>(p.h0 + (int64_t)c * N * p.D, p.D, d, l.h);
         } else if (!(p.q.fresh && p.q.fresh[s])) {
@@ -350,96 +360,112 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_ker
 }
 
 // One row a sequence.  Q lanes a channel, four states each (the last lane's may
-// be fewer); VEC: the states of a lane are one 16-byte access.
-template <typename T, int Q, bool VEC>
+// be fewer), U channels a lane with all their loads under way together.  VEC:
+// the states of a lane are one 16-byte access.
+template <typename T, int Q, bool VEC, int U>
 __global__ __launch_bounds__(256) void tok_step_kernel(TokScanParams p, int cblocks) {
-    const int s = blockIdx.x / cblocks;
-    const int i = (blockIdx.x % cblocks) * 256 + (int)threadIdx.x;
-    const int d0 = i / Q, q = i % Q;
-    const bool act = d0 < p.D;
-    const int d = act ? d0 : 0, n0 = 4 * q, N = p.N;
+    const int s = blockIdx.x / cblocks, q = threadIdx.x % Q;
+    const int c0 = (blockIdx.x % cblocks) * (U * 256 / Q) + (int)threadIdx.x / Q;   // unit u: c0 + u * 256 / Q
+    const int n0 = 4 * q, N = p.N;
     const bool four = n0 + 4 <= N;   // VEC: all of a lane's states or (N = 12) none
     // the state is loaded from the slot that is named; whether the sequence has it comes in meanwhile
     const int slot = uniform(slot_named(p.q, s));
     if (slot < 0) return;
     const int64_t t = s;
-    float* pool = p.pool + slot * p.spool + (int64_t)d * N + n0;
-    const float* A = p.A + (int64_t)d * N + n0;
+    const bool fresh = p.q.fresh && p.q.fresh[s];
+    float* const pool = p.pool + slot * p.spool + n0;
     const T* B = (const T*)p.Bm + t * p.sB + n0;
     const T* C = (const T*)p.C + t * p.sC + n0;
-    const bool fresh = p.q.fresh && p.q.fresh[s];
-    float h[4] = {}, a[4] = {}, b[4], c[4];
-    if (VEC && four) {
-        const float4 av = *reinterpret_cast<const float4*>(A);
-        a[0] = av.x; a[1] = av.y; a[2] = av.z; a[3] = av.w;
-        if (!fresh) {
-            const float4 hv = *reinterpret_cast<const float4*>(pool);
-            h[0] = hv.x; h[1] = hv.y; h[2] = hv.z; h[3] = hv.w;
-        }
-    } else if (!VEC) {
+    float h[U][4], a[U][4], b[4], c[4], dl[U], x[U], bias[U], skip[U], z[U];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (n0 + e < N) {
-                a[e] = A[e];
-                if (!fresh) h[e] = pool[e];
+    for (int u = 0; u < U; ++u) {
+        const int d = min(c0 + u * (256 / Q), p.D - 1);
+        const float* A = p.A + (int64_t)d * N + n0;
+        const float* hp = pool + (int64_t)d * N;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[u][e] = a[u][e] = 0.0f;
+        if (VEC && four) {
+            if (!fresh) {
+                const float4 hv = *reinterpret_cast<const float4*>(hp);
+                h[u][0] = hv.x; h[u][1] = hv.y; h[u][2] = hv.z; h[u][3] = hv.w;
+            }
+            const float4 av = *reinterpret_cast<const float4*>(A);
+            a[u][0] = av.x; a[u][1] = av.y; a[u][2] = av.z; a[u][3] = av.w;
+        } else if (!VEC) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (n0 + e < N) {
+                    a[u][e] = A[e];
+                    if (!fresh) h[u][e] = hp[e];
+                }
             }
         }
+        dl[u] = to_f32(((const T*)p.delta)[t * p.sdelta + d]);
+        x[u] = to_f32(((const T*)p.x)[t * p.sx + d]);
+        bias[u] = p.stepf.bias ? p.stepf.bias[d] : 0.0f;
+        skip[u] = p.skip ? p.skip[d] : 0.0f;
+        z[u] = p.z ? to_f32(((const T*)p.z)[t * p.sz + d]) : 0.0f;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         b[e] = n0 + e < N ? to_f32(B[e]) : 0.0f;
         c[e] = n0 + e < N ? to_f32(C[e]) : 0.0f;
     }
-    float dl = to_f32(((const T*)p.delta)[t * p.sdelta + d]) + (p.stepf.bias ? p.stepf.bias[d] : 0.0f);
-    if (p.stepf.softplus) dl = softplus_t(dl);
-    const float x = to_f32(((const T*)p.x)[t * p.sx + d]);
-    const float u = dl * x;
-    float y = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (n0 + e < N) {
-            h[e] = fmaf(__builtin_amdgcn_exp2f(a[e] * kLog2e * dl), h[e], u * b[e]);
-            y = fmaf(h[e], c[e], y);
-        }
-    }
     if (slot_taken(p.q, s, slot)) return;
-    if (Q > 1) y += dpp<SSM_DPP_QUAD(1, 0, 3, 2)>(0.0f, y);
-    if (Q > 2) y += dpp<SSM_DPP_QUAD(2, 3, 0, 1)>(0.0f, y);
-    if (!act) return;
-    if (VEC) {
-        if (four) *reinterpret_cast<float4*>(pool) = make_float4(h[0], h[1], h[2], h[3]);
-    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (n0 + e < N) pool[e] = h[e];
-    }
-    if (q == 0) {
-        if (p.skip) y = fmaf(p.skip[d], x, y);
-        if (p.z) {
-            const float z = to_f32(((const T*)p.z)[t * p.sz + d]);
-            y *= z * sigmoid_f(z);
+    for (int u = 0; u < U; ++u) {
+        const int d = c0 + u * (256 / Q);
+        float step = dl[u] + bias[u];
+        if (p.stepf.softplus) step = softplus_t(step);
+        const float v = step * x[u];
+        float y = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (n0 + e < N) {
+                h[u][e] = fmaf(__builtin_amdgcn_exp2f(a[u][e] * kLog2e * step), h[u][e], v * b[e]);
+                y = fmaf(h[u][e], c[e], y);
+            }
         }
-        ((T*)p.y)[t * p.sy + d] = to_stream<T>(y);
+        if (Q > 1) y += dpp<SSM_DPP_QUAD(1, 0, 3, 2)>(0.0f, y);
+        if (Q > 2) y += dpp<SSM_DPP_QUAD(2, 3, 0, 1)>(0.0f, y);
+        if (d >= p.D) continue;
+        float* hp = pool + (int64_t)d * N;
+        if (VEC) {
+            if (four) *reinterpret_cast<float4*>(hp) = make_float4(h[u][0], h[u][1], h[u][2], h[u][3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n0 + e < N) hp[e] = h[u][e];
+        }
+        if (q == 0) {
+            if (p.skip) y = fmaf(skip[u], x[u], y);
+            if (p.z) y *= z[u] * sigmoid_f(z[u]);
+            ((T*)p.y)[t * p.sy + d] = to_stream<T>(y);
+        }
     }
 }
 
+template <typename T, int Q, int U>
+hipError_t tok_step_u(const TokScanParams& p, hipStream_t st) {
+    constexpr int per = U * 256 / Q;
+    const int64_t cblocks = ((int64_t)p.D + per - 1) / per, blocks = cblocks * p.q.S;
+    if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
+    // VEC: N a multiple of 4, so a lane has four states or none
+    if (p.vec) tok_step_kernel<T, Q, true, U><<<(unsigned)blocks, 256, 0, st>>>(p, (int)cblocks);
+    else tok_step_kernel<T, Q, false, U><<<(unsigned)blocks, 256, 0, st>>>(p, (int)cblocks);
+    return hipGetLastError();
+}
+template <typename T, int Q>
+hipError_t tok_step_q(const TokScanParams& p, hipStream_t st) {
+    // Several channels a lane once there are workgroups enough for it: 256 sequences x 4096 channels x 16 states
+    // take 39.7 us with one, 31.8 with two, 30.8 with four, 30.0 with eight; one token of one sequence is
+    // fastest spread over all lanes.
+    const int64_t lanes = (int64_t)p.q.S * p.D * Q;
+    return lanes >= 4 * 256 * 1024 ? tok_step_u<T, Q, 4>(p, st) : tok_step_u<T, Q, 1>(p, st);
+}
 template <typename T>
 hipError_t tok_step(const TokScanParams& p, hipStream_t st) {
-    const int q = p.N <= 4 ? 1 : p.N <= 8 ? 2 : 4;
-    const int64_t cblocks = ((int64_t)p.D * q + 255) / 256, blocks = cblocks * p.q.S;
-    if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
-    const unsigned g = (unsigned)blocks;
-    const int cb = (int)cblocks;
-    if (p.vec) {   // N a multiple of 4: a lane has four states or none
-        if (q == 1) tok_step_kernel<T, 1, true><<<g, 256, 0, st>>>(p, cb);
-        else if (q == 2) tok_step_kernel<T, 2, true><<<g, 256, 0, st>>>(p, cb);
-        else tok_step_kernel<T, 4, true><<<g, 256, 0, st>>>(p, cb);
-    } else {
-        if (q == 1) tok_step_kernel<T, 1, false><<<g, 256, 0, st>>>(p, cb);
-        else if (q == 2) tok_step_kernel<T, 2, false><<<g, 256, 0, st>>>(p, cb);
-        else tok_step_kernel<T, 4, false><<<g, 256, 0, st>>>(p, cb);
-    }
-    return hipGetLastError();
+    return p.N <= 4 ? tok_step_q<T, 1>(p, st) : p.N <= 8 ? tok_step_q<T, 2>(p, st) : tok_step_q<T, 4>(p, st);
 }
 
 template <typename T, int N>
