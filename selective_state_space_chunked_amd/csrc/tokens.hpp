@@ -79,6 +79,43 @@ __device__ __forceinline__ int slot_of(const Sequences& q, int s) {
     return v < 0 || slot_taken(q, s, v) ? -1 : v;
 }
 
+// A wave's view of the call's sequences.  Fewer than 64 of them (as a rule) lie in
+// one register a list, so what a wave asks about them costs one trip to memory,
+// under way while its first rows are loaded; otherwise each question reads the
+// lists.  Every member is called by whole waves with scalar arguments.
+struct SeqTable {
+    const Sequences& q;
+    const bool small;
+    int start_, slot_, fresh_;
+    __device__ __forceinline__ explicit SeqTable(const Sequences& q_) : q(q_), small(q_.S < 64) {
+        start_ = slot_ = fresh_ = 0;
+        if (small) {
+            const int l = lane_id();
+            start_ = q.start[min(l, q.S)];
+            slot_ = q.slot ? q.slot[min(l, q.S - 1)] : l;
+            fresh_ = q.fresh ? q.fresh[min(l, q.S - 1)] : 0;
+        }
+    }
+    // the last sequence whose first row is at or before row t, as find_seq
+    __device__ __forceinline__ int find(int t) const {
+        if (!small) return uniform(find_seq(q.start, q.S, t));
+        return __popcll(__ballot(lane_id() <= q.S && start_ <= t)) - 1;
+    }
+    __device__ __forceinline__ int first(int s) const {   // s <= S
+        return small ? __builtin_amdgcn_readlane(start_, s) : uniform(q.start[s]);
+    }
+    __device__ __forceinline__ int end(int s) const { return min(first(s + 1), q.T); }
+    __device__ __forceinline__ int slot(int s) const {   // as slot_of
+        if (!small) return uniform(slot_of(q, s));
+        const int v = __builtin_amdgcn_readlane(slot_, s);
+        if (v < 0 || v >= q.slots) return -1;
+        return __ballot(lane_id() < s && slot_ == v) ? -1 : v;
+    }
+    __device__ __forceinline__ bool fresh(int s) const {
+        return small ? __builtin_amdgcn_readlane(fresh_, s) != 0 : q.fresh && q.fresh[s];
+    }
+};
+
 // Sixteen bytes of consecutive elements at any element's address (global memory
 // takes unaligned accesses), as floats and back.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));

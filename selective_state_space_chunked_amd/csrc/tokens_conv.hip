@@ -69,15 +69,25 @@ struct ConvLane {
         if (FULL) q.store(y + t * sy);
         else q.store(y + t * sy, cnt);
     }
+    __device__ __forceinline__ void window(const Vec<T>* r) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) r[i].get(win[i]);
+    }
     // rows [t0, t1): the next group's loads are under way while a group is computed
     __device__ __forceinline__ void walk(int t0, int t1) {
-        Vec<T> r[kTokGrp], nx[kTokGrp];
+        Vec<T> r[kTokGrp];
+#pragma unroll
+        for (int g = 0; g < kTokGrp; ++g)
+            if (t0 + g < t1) load_row(t0 + g, r[g]);
+        walk(t0, t1, r);
+    }
+    __device__ __forceinline__ void walk(int t0, int t1, Vec<T> (&r)[kTokGrp]) {   // r: the first group
+        Vec<T> nx[kTokGrp];
         auto load = [&](int t, Vec<T>(&v)[kTokGrp]) {
 #pragma unroll
             for (int g = 0; g < kTokGrp; ++g)
                 if (t + g < t1) load_row(t + g, v[g]);
         };
-        load(t0, r);
         for (int t = t0; t < t1; t += kTokGrp) {
             if (t + kTokGrp < t1) load(t + kTokGrp, nx);
 #pragma unroll
@@ -148,25 +158,33 @@ struct ConvLane {
 
 template <typename T, int W, bool FULL>
 __device__ __forceinline__ void rows_of_wave(const TokConvParams& p, int c0, int64_t unit) {
-    ConvLane<T, W, FULL> l(p, c0);
     constexpr int H = W - 1, V = Vec<T>::V;
     const int r0 = (int)min(unit * kTokRun, (int64_t)p.q.T), r1 = min(r0 + kTokRun, p.q.T);
     if (r0 >= r1) return;
-    const int32_t* start = p.q.start;
-    int s = uniform(find_seq(start, p.q.S, r0));
+    const SeqTable q(p.q);
+    ConvLane<T, W, FULL> l(p, c0);
+    // what most waves begin with, whichever sequence the rows belong to: the first rows and those before them
+    Vec<T> before[H], head[kTokGrp];
+#pragma unroll
+    for (int i = 0; i < H; ++i) l.load_row(max(r0 - H + i, 0), before[i]);
+#pragma unroll
+    for (int g = 0; g < kTokGrp; ++g) l.load_row(min(r0 + g, r1 - 1), head[g]);
+    int s = q.find(r0);
     if (s >= p.q.S) return;
     if (s >= 0) {   // the sequence that runs into this range
-        const int st = uniform(start[s]), en = uniform(min(start[s + 1], p.q.T));
+        const int st = q.first(s), en = q.end(s);
         if (st >= 0 && st < r0) {
             const int t0 = max(r0, st + H), t1 = min(en, r1);
-            if (t0 < t1 && slot_of(p.q, s) >= 0) {
+            if (t0 < t1 && q.slot(s) >= 0) {
+                if (t0 == r0) {
+                    l.window(before);
+                    l.walk(t0, t1, head);
+                } else {   // its first H rows are the wave's before
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    Vec<T> r;
-                    l.load_row(t0 - H + i, r);
-                    r.get(l.win[i]);
+                    for (int i = 0; i < H; ++i) l.load_row(t0 - H + i, before[i]);
+                    l.window(before);
+                    l.walk(t0, t1);
                 }
-                l.walk(t0, t1);
             }
         }
         if (st < r0) ++s;
@@ -174,16 +192,16 @@ __device__ __forceinline__ void rows_of_wave(const TokConvParams& p, int c0, int
         s = 0;
     }
     for (; s < p.q.S; ++s) {   // sequences whose first row lies in this range
-        const int st = uniform(start[s]);
+        const int st = q.first(s);
         if (st >= r1) break;
-        const int en = uniform(min(start[s + 1], p.q.T));
+        const int en = q.end(s);
         if (st < r0 || en <= st) continue;
-        const int slot = uniform(slot_of(p.q, s));
+        const int slot = q.slot(s);
         if (slot < 0) continue;
         Vec<T> old[H];
         float nh[V * H];
         l.load_state(slot, old);
-        l.begin(old, p.q.fresh && p.q.fresh[s], st, en - st, nh);
+        l.begin(old, q.fresh(s), st, en - st, nh);
         l.store_state(slot, nh);
         l.walk(st, min(en, max(r1, st + H)));
     }

@@ -235,12 +235,13 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_sum
     const int c = blockIdx.x / gblocks;
     if (cb * 64 >= p.D) return;
     const Range_ r = rows_of(p, c);
-    const int s = uniform(find_seq(p.q.start, p.q.S, r.r1 - 1));
+    const SeqTable q(p.q);
+    const int s = q.find(r.r1 - 1);
     int st = 0, en = 0, slot = -1;
     if (s >= 0 && s < p.q.S) {
-        st = uniform(p.q.start[s]);
-        en = uniform(min(p.q.start[s + 1], p.q.T));
-        if (st >= 0 && en > r.r1) slot = uniform(slot_of(p.q, s));
+        st = q.first(s);
+        en = q.end(s);
+        if (st >= 0 && en > r.r1) slot = q.slot(s);
     }
     if (cb == 0 && lane_id() == 0) p.through[c] = slot >= 0 && st < r.r0;
     if (slot < 0) return;   // none crosses the end
@@ -253,7 +254,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_sum
     for (int n = 0; n < N; ++n) l.h[n] = 0.0f;
     l.dsum = 0.0f;
     if (st >= r.r0) {   // it begins here: its first state, kept for the second pass (which may find it overwritten)
-        if (!(p.q.fresh && p.q.fresh[s])) load_states<N>(p.pool + slot * p.spool + (int64_t)d * N, l.h);
+        if (!q.fresh(s)) load_states<N>(p.pool + slot * p.spool + (int64_t)d * N, l.h);
         put_range<N>(p.h0 + at, p.D, d, l.h);
     }
     l.template walk<false>(max(st, r.r0), r.r1);
@@ -263,52 +264,65 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_sum
 
 // Between the passes: the states at the ranges' ends, from those that each range leaves alone,
 //   h <- exp(A dsum) h + S where the sequence runs through the whole range, S where it begins there.
-// A workgroup takes 64 channels of one state; its 16 waves take the ranges in 16 runs, compose
-// each, then each composes the runs before its own and goes over its ranges again.
+// A workgroup takes 64 channels of one state; its 16 waves take the ranges in runs of PER, compose
+// each, then each composes the runs before its own and goes over its ranges again.  PER ranges stay in
+// registers in between, so the states are read once and written once, which bounds it; more than
+// 16 * PER ranges are taken in turns of that many, with the state carried over.
 constexpr int kRuns = 16;
+template <int PER>
 __global__ __launch_bounds__(64 * kRuns) void tok_scan_join_kernel(TokScanParams p) {
-    __shared__ float sh[kRuns][64], ss[kRuns][64];
+    __shared__ float end_[kRuns][64], decay_[kRuns][64];
     const int n = blockIdx.x % p.N, lane = lane_id(), w = uniform(threadIdx.x >> 6);
     const int d = min((int)(blockIdx.x / p.N) * 64 + lane, p.D - 1);
     const float a = p.A[(int64_t)d * p.N + n] * kLog2e;
-    const int ends = p.nrange - 1, per = (ends + kRuns - 1) / kRuns;
-    const int k0 = min(w * per, ends), k1 = min(k0 + per, ends);
-    float* S = p.hsum + (int64_t)n * p.D + d;
+    const int ends = p.nrange - 1;
+    float* const S = p.hsum + (int64_t)n * p.D + d;
     const int64_t step = (int64_t)p.N * p.D;
-    auto go = [&](float h, bool keep, float* sum) {
-        bool all = true;
-        float ds = 0.0f;
-        for (int k = k0; k < k1; k += 8) {
-            float s[8], e[8];
-            int f[8];
+    float carry = 0.0f;
+    for (int base = 0; base < ends; base += kRuns * PER) {
+        const int k0 = base + w * PER;
+        float s[PER], e[PER];
+        int f[PER];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j = min(k + i, k1 - 1);
-                s[i] = S[j * step];
-                e[i] = p.dsum[(int64_t)j * p.D + d];
-                f[i] = p.through[j];
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (k + i >= k1) break;
-                h = f[i] ? fmaf(__builtin_amdgcn_exp2f(a * e[i]), h, s[i]) : s[i];
-                ds += e[i];
-                all = all && f[i];
-                if (keep) S[(k + i) * step] = h;
-            }
+        for (int i = 0; i < PER; ++i) {
+            const int j = min(k0 + i, ends - 1);
+            s[i] = S[j * step];
+            e[i] = p.dsum[(int64_t)j * p.D + d];
+            f[i] = p.through[j];
         }
-        // the run as a map: through a run with a beginning in it nothing comes
-        if (sum) *sum = all ? __builtin_amdgcn_exp2f(a * ds) : -1.0f;
-        return h;
-    };
-    float decay;
-    const float h = go(0.0f, false, &decay);
-    sh[w][lane] = h;
-    ss[w][lane] = decay;
-    __syncthreads();
-    float in = 0.0f;
-    for (int i = 0; i < w; ++i) in = ss[i][lane] < 0.0f ? sh[i][lane] : fmaf(ss[i][lane], in, sh[i][lane]);
-    go(in, true, nullptr);
+        // the run as a map: through a run with a beginning in it nothing comes (decay -1)
+        float h = 0.0f, decay = 1.0f;
+        bool all = true;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const bool has = k0 + i < ends;
+            e[i] = __builtin_amdgcn_exp2f(a * e[i]);
+            const float g = f[i] ? fmaf(e[i], h, s[i]) : s[i];
+            h = has ? g : h;
+            decay *= has ? e[i] : 1.0f;
+            all = all && (f[i] || !has);
+        }
+        end_[w][lane] = h;
+        decay_[w][lane] = all ? decay : -1.0f;
+        __syncthreads();
+        float in = carry;
+        for (int i = 0; i < w; ++i) {
+            const float q = decay_[i][lane];
+            in = q < 0.0f ? end_[i][lane] : fmaf(q, in, end_[i][lane]);
+        }
+        h = in;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            h = f[i] ? fmaf(e[i], h, s[i]) : s[i];
+            if (k0 + i < ends) S[(int64_t)(k0 + i) * step] = h;
+        }
+        for (int i = w; i < kRuns; ++i) {   // on to what the next turn begins with
+            const float q = decay_[i][lane];
+            in = q < 0.0f ? end_[i][lane] : fmaf(q, in, end_[i][lane]);
+        }
+        carry = in;
+        __syncthreads();
+    }
 }
 
 // Second pass: every row's output and every sequence's last state.
@@ -318,18 +332,19 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_ker
     const int c = blockIdx.x / gblocks;
     if (cb * 64 >= p.D) return;
     const Range_ r = rows_of(p, c);
-    int s = uniform(find_seq(p.q.start, p.q.S, r.r0));
+    const SeqTable q(p.q);
+    int s = q.find(r.r0);
     if (s >= p.q.S) return;
     const int d = min(cb * 64 + lane_id(), p.D - 1);
     __shared__ __align__(16) float lds[kScanWaves * ScanLane<T, N, FULL>::kLds];
     ScanLane<T, N, FULL> l(p, d, lds + (threadIdx.x >> 6) * ScanLane<T, N, FULL>::kLds);
     if (s < 0) s = 0;
     for (; s < p.q.S; ++s) {
-        const int st = uniform(p.q.start[s]);
+        const int st = q.first(s);
         if (st >= r.r1) break;
-        const int en = uniform(min(p.q.start[s + 1], p.q.T));
+        const int en = q.end(s);
         if (st < 0 || en <= max(st, r.r0)) continue;
-        const int slot = uniform(slot_of(p.q, s));
+        const int slot = q.slot(s);
         if (slot < 0) continue;
         float* pool = p.pool + slot * p.spool + (int64_t)d * N;
 #pragma unroll
@@ -337,7 +352,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_ker
         if (st < r.r0) {   // from the ranges before: the state that crosses into this one
             get_range<N>(p.hsum + (int64_t)(p.joined ? c - 1 : st / p.rows) * N * p.D, p.D, d, l.h);
             if (!p.joined) {
-#pragma unroll 2
+#pragma unroll 1
                 for (int k = st / p.rows + 1; k < c; ++k) {
                     float S[N];
                     get_range<N>(p.hsum + (int64_t)k * N * p.D, p.D, d, S);
@@ -348,7 +363,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_ker
             }
         } else if (en > r.r1) {
             get_range<N>(p.h0 + (int64_t)c * N * p.D, p.D, d, l.h);
-        } else if (!(p.q.fresh && p.q.fresh[s])) {
+        } else if (!q.fresh(s)) {
             load_states<N>(pool, l.h);
         }
         l.template walk<true>(max(st, r.r0), min(en, r.r1));
@@ -359,13 +374,21 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_ker
     }
 }
 
-// One row a sequence.  Q lanes a channel, four states each (the last lane's may
-// be fewer), U channels a lane with all their loads under way together.  VEC:
-// the states of a lane are one 16-byte access.
-template <typename T, int Q, bool VEC, int U>
+// One row a sequence.  Q lanes share a channel, four states each (the last lane's may be fewer), and Q channels
+// (units): the loads of all their states are under way together, and what a channel has once (step size, input,
+// gate) lane q of the group reads and forms for unit q; the others take it by a lane move, and the units' sums
+// over the states come back to it by a transpose.  VEC: the states of a lane are one 16-byte access.
+template <int Q, int U>
+__device__ __forceinline__ float of_unit(float v) {   // lane U of the group's value
+    if (Q == 4) return dpp<SSM_DPP_QUAD(U, U, U, U)>(0.0f, v);
+    if (Q == 2) return dpp<SSM_DPP_QUAD(U, U, 2 + U, 2 + U)>(0.0f, v);
+    return v;
+}
+template <typename T, int Q, bool VEC>
 __global__ __launch_bounds__(256) void tok_step_kernel(TokScanParams p, int cblocks) {
+    constexpr int G = 256 / Q;   // groups of a workgroup; unit u's channel is c0 + u * G
     const int s = blockIdx.x / cblocks, q = threadIdx.x % Q;
-    const int c0 = (blockIdx.x % cblocks) * (U * 256 / Q) + (int)threadIdx.x / Q;   // unit u: c0 + u * 256 / Q
+    const int c0 = (blockIdx.x % cblocks) * 256 + (int)threadIdx.x / Q;
     const int n0 = 4 * q, N = p.N;
     const bool four = n0 + 4 <= N;   // VEC: all of a lane's states or (N = 12) none
     // the state is loaded from the slot that is named; whether the sequence has it comes in meanwhile
@@ -376,12 +399,15 @@ __global__ __launch_bounds__(256) void tok_step_kernel(TokScanParams p, int cblo
     float* const pool = p.pool + slot * p.spool + n0;
     const T* B = (const T*)p.Bm + t * p.sB + n0;
     const T* C = (const T*)p.C + t * p.sC + n0;
-    float h[U][4], a[U][4], b[4], c[4], dl[U], x[U], bias[U], skip[U], z[U];
+    // a lane's places in a channel's states and A, from the workgroup's first channel: 32 bits
+    const int last = p.D - 1 - (int)(blockIdx.x % cblocks) * 256;
+    float* const hb = pool + (int64_t)(p.D - 1 - last) * N;
+    const float* const Ab = p.A + (int64_t)(p.D - 1 - last) * N + n0;
+    float h[Q][4], a[Q][4], b[4], c[4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int d = min(c0 + u * (256 / Q), p.D - 1);
-        const float* A = p.A + (int64_t)d * N + n0;
-        const float* hp = pool + (int64_t)d * N;
+    for (int u = 0; u < Q; ++u) {
+        const int at = min((int)threadIdx.x / Q + u * G, last) * N;
+        const float *A = Ab + at, *hp = hb + at;
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[u][e] = a[u][e] = 0.0f;
         if (VEC && four) {
@@ -400,36 +426,34 @@ __global__ __launch_bounds__(256) void tok_step_kernel(TokScanParams p, int cblo
                 }
             }
         }
-        dl[u] = to_f32(((const T*)p.delta)[t * p.sdelta + d]);
-        x[u] = to_f32(((const T*)p.x)[t * p.sx + d]);
-        bias[u] = p.stepf.bias ? p.stepf.bias[d] : 0.0f;
-        skip[u] = p.skip ? p.skip[d] : 0.0f;
-        z[u] = p.z ? to_f32(((const T*)p.z)[t * p.sz + d]) : 0.0f;
     }
+    const int dq = min(c0 + q * G, p.D - 1);   // the lane's own unit
+    float step = to_f32(((const T*)p.delta)[t * p.sdelta + dq]);
+    const float x = to_f32(((const T*)p.x)[t * p.sx + dq]);
+    const float bias = p.stepf.bias ? p.stepf.bias[dq] : 0.0f, skip = p.skip ? p.skip[dq] : 0.0f;
+    const float z = p.z ? to_f32(((const T*)p.z)[t * p.sz + dq]) : 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        b[e] = n0 + e < N ? to_f32(B[e]) : 0.0f;
-        c[e] = n0 + e < N ? to_f32(C[e]) : 0.0f;
+        const bool has = VEC ? four : n0 + e < N;
+        b[e] = has ? to_f32(B[e]) : 0.0f;
+        c[e] = has ? to_f32(C[e]) : 0.0f;
     }
     if (slot_taken(p.q, s, slot)) return;
+    step += bias;
+    if (p.stepf.softplus) step = softplus_t(step);
+    const float in = step * x, step2 = step * kLog2e;
+    float y[Q];
+    auto unit = [&](int u, float dl, float v) {
+        y[u] = 0.0f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int d = c0 + u * (256 / Q);
-        float step = dl[u] + bias[u];
-        if (p.stepf.softplus) step = softplus_t(step);
-        const float v = step * x[u];
-        float y = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (n0 + e < N) {
-                h[u][e] = fmaf(__builtin_amdgcn_exp2f(a[u][e] * kLog2e * step), h[u][e], v * b[e]);
-                y = fmaf(h[u][e], c[e], y);
-            }
+        for (int e = 0; e < 4; ++e) {   // of a place past the states: not used, as v may be infinite
+            h[u][e] = fmaf(__builtin_amdgcn_exp2f(a[u][e] * dl), h[u][e], v * b[e]);
+            if (VEC) y[u] = fmaf(h[u][e], c[e], y[u]);
+            else y[u] = n0 + e < N ? fmaf(h[u][e], c[e], y[u]) : y[u];
         }
-        if (Q > 1) y += dpp<SSM_DPP_QUAD(1, 0, 3, 2)>(0.0f, y);
-        if (Q > 2) y += dpp<SSM_DPP_QUAD(2, 3, 0, 1)>(0.0f, y);
-        if (d >= p.D) continue;
-        float* hp = pool + (int64_t)d * N;
+        if (VEC && Q == 4) y[u] = four ? y[u] : 0.0f;
+        if ((int)threadIdx.x / Q + u * G > last) return;
+        float* hp = hb + ((int)threadIdx.x / Q + u * G) * N;
         if (VEC) {
             if (four) *reinterpret_cast<float4*>(hp) = make_float4(h[u][0], h[u][1], h[u][2], h[u][3]);
         } else {
@@ -437,31 +461,33 @@ __global__ __launch_bounds__(256) void tok_step_kernel(TokScanParams p, int cblo
             for (int e = 0; e < 4; ++e)
                 if (n0 + e < N) hp[e] = h[u][e];
         }
-        if (q == 0) {
-            if (p.skip) y = fmaf(skip[u], x[u], y);
-            if (p.z) y *= z[u] * sigmoid_f(z[u]);
-            ((T*)p.y)[t * p.sy + d] = to_stream<T>(y);
-        }
+    };
+    unit(0, of_unit<Q, 0>(step2), of_unit<Q, 0>(in));
+    if (Q > 1) unit(1 % Q, of_unit<Q, 1 % Q>(step2), of_unit<Q, 1 % Q>(in));
+    if (Q > 2) {
+        unit(2 % Q, of_unit<Q, 2 % Q>(step2), of_unit<Q, 2 % Q>(in));
+        unit(3 % Q, of_unit<Q, 3 % Q>(step2), of_unit<Q, 3 % Q>(in));
     }
+    float o = y[0];   // lane q: unit q's sum over the group's lanes
+    if (Q > 1) o = pair_level<SSM_DPP_QUAD(1, 0, 3, 2)>(y[0], y[1 % Q], (q & 1) != 0);
+    if (Q > 2) {
+        const float r = pair_level<SSM_DPP_QUAD(1, 0, 3, 2)>(y[2 % Q], y[3 % Q], (q & 1) != 0);
+        o = pair_level<SSM_DPP_QUAD(2, 3, 0, 1)>(o, r, (q & 2) != 0);
+    }
+    if (c0 + q * G >= p.D) return;
+    if (p.skip) o = fmaf(skip, x, o);
+    if (p.z) o *= z * sigmoid_f(z);
+    ((T*)p.y)[t * p.sy + dq] = to_stream<T>(o);
 }
 
-template <typename T, int Q, int U>
-hipError_t tok_step_u(const TokScanParams& p, hipStream_t st) {
-    constexpr int per = U * 256 / Q;
-    const int64_t cblocks = ((int64_t)p.D + per - 1) / per, blocks = cblocks * p.q.S;
-    if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
-    // VEC: N a multiple of 4, so a lane has four states or none
-    if (p.vec) tok_step_kernel<T, Q, true, U><<<(unsigned)blocks, 256, 0, st>>>(p, (int)cblocks);
-    else tok_step_kernel<T, Q, false, U><<<(unsigned)blocks, 256, 0, st>>>(p, (int)cblocks);
-    return hipGetLastError();
-}
 template <typename T, int Q>
 hipError_t tok_step_q(const TokScanParams& p, hipStream_t st) {
-    // Several channels a lane once there are workgroups enough for it: 256 sequences x 4096 channels x 16 states
-    // take 39.7 us with one, 31.8 with two, 30.8 with four, 30.0 with eight; one token of one sequence is
-    // fastest spread over all lanes.
-    const int64_t lanes = (int64_t)p.q.S * p.D * Q;
-    return lanes >= 4 * 256 * 1024 ? tok_step_u<T, Q, 4>(p, st) : tok_step_u<T, Q, 1>(p, st);
+    const int64_t cblocks = ((int64_t)p.D + 255) / 256, blocks = cblocks * p.q.S;
+    if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
+    // VEC: N a multiple of 4, so a lane has four states or none
+    if (p.vec) tok_step_kernel<T, Q, true><<<(unsigned)blocks, 256, 0, st>>>(p, (int)cblocks);
+    else tok_step_kernel<T, Q, false><<<(unsigned)blocks, 256, 0, st>>>(p, (int)cblocks);
+    return hipGetLastError();
 }
 template <typename T>
 hipError_t tok_step(const TokScanParams& p, hipStream_t st) {
@@ -501,7 +527,8 @@ hipError_t launch_tok_step(const TokScanParams& p, int dtype, hipStream_t st) {
 }
 hipError_t launch_tok_join(const TokScanParams& p, hipStream_t st) {
     const int64_t blocks = ((int64_t)p.D + 63) / 64 * p.N;
-    tok_scan_join_kernel<<<(unsigned)blocks, 64 * kRuns, 0, st>>>(p);
+    if (p.nrange - 1 <= 8 * kRuns) tok_scan_join_kernel<8><<<(unsigned)blocks, 64 * kRuns, 0, st>>>(p);
+    else tok_scan_join_kernel<16><<<(unsigned)blocks, 64 * kRuns, 0, st>>>(p);
     return hipGetLastError();
 }
 hipError_t launch_tok_scan(const TokScanParams& p, int dtype, bool sum, hipStream_t st) {
