@@ -152,9 +152,10 @@ def lib():
     """Load libssmscan.so; raise if it has not been built."""
     global _lib
     if _lib is None:
-        if not os.path.exists(LIB_PATH):
-            raise RuntimeError(f"HIP library {LIB_PATH} is missing: run __graft_entry__.build() "
-                               "(or python selective_state_space_chunked_amd/build.py)")
+        for path in (LIB_PATH, os.path.join(_HERE, "_pycall.so")):
+            if not os.path.exists(path):
+                raise RuntimeError(f"HIP library {path} is missing: run __graft_entry__.build() "
+                                   "(or python selective_state_space_chunked_amd/build.py)")
         L = ctypes.CDLL(LIB_PATH)
         L.ssm_workspace_bytes.argtypes = [ctypes.c_int, _vp, ctypes.POINTER(ctypes.c_size_t)]
         L.ssm_scan_fwd.argtypes = [ctypes.POINTER(ScanArgs), ctypes.POINTER(ScanFwdOut), _vp, ctypes.c_size_t, _vp]
@@ -179,8 +180,23 @@ def lib():
         L.ssm_status_string.argtypes = [ctypes.c_int]
         L.ssm_last_error_detail.restype = ctypes.c_char_p
         L.ssm_abi_version.restype = ctypes.c_int
-        _lib = L
+        _lib = _with_pycall(L)
     return _lib
+
+
+# The convolution, checkpoint and packed-row functions go through a native module where a call's arguments are plain
+# (csrc/pycall.cpp): single tokens and small layers are bound by what a call costs the host.
+_pycall = None
+
+
+def _with_pycall(L):
+    global _pycall
+    from . import _pycall as native
+    native.bind(*(ctypes.cast(getattr(L, f), _vp).value for f in (
+        "ssm_conv_fwd", "ssm_conv_bwd", "ssm_ckpt8_unpack", "ssm_tokens_conv", "ssm_tokens_scan",
+        "ssm_workspace_bytes")))
+    _pycall = native
+    return L
 
 
 class SSMError(RuntimeError):
@@ -673,9 +689,11 @@ def pd_scan_bwd(*, gy, gh_last=None, ckpt=None, want=("gd", "gb", "gC", "gh0"), 
 # ---------------------------------------------------------------------------
 # short causal convolution, 8-bit activation checkpoints
 #
-# Single tokens and small layers are bound by what a call costs the host, so
-# these functions check a tensor by one short predicate (the checks that name
-# what is wrong run only where it fails) and pass their structs as packed bytes.
+# A call whose tensors are plain goes through the native module; the functions
+# here take the others (views, installed allocators, caller-supplied outputs of
+# the convolution, tensors of another device than the current one) and name what
+# is wrong with a call.  They check a tensor by one short predicate and pass their
+# structs as packed bytes.
 # ---------------------------------------------------------------------------
 _STREAM = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
 _F32 = torch.float32
@@ -739,6 +757,26 @@ def _launch(dev, fn, *args):
         _check(rc)
 
 
+def _native(t):
+    """The native calls and where they launch, (module, device, stream), for a call with tensor t; else None: outputs
+    come from an installed allocator, or t is no GPU tensor."""
+    if _allocator is not None or not (isinstance(t, torch.Tensor) and t.is_cuda):
+        return None
+    if _pycall is None:
+        lib()
+    dev = torch.cuda.current_device()
+    return _pycall, dev, _raw_stream(dev)
+
+
+def _done(r):
+    """Whether a native call was made: raises the library's error, False where the arguments are for the path below."""
+    if r is NotImplemented:
+        return False
+    if r.__class__ is int:
+        _check(r)
+    return True
+
+
 def _need_ckpt8(ckpt8):
     x8, scale = ckpt8
     _need(x8, "x8", torch.int8)
@@ -796,6 +834,11 @@ def conv_fwd(*, x=None, ckpt8=None, w, bias=None, init=None, silu=False, want_y=
     last (the last W-1 inputs, what a following segment takes as ``init``) and x8, x8_scale (the 8-bit
     checkpoint of x), those requested.  ``ckpt8`` = (x8, x8_scale) takes the place of x, with ``dtype`` that
     of y: the convolution's output again from its checkpoint."""
+    if not out and ckpt8 is None and dtype is None and (nat := _native(x)):
+        m, di, stream = nat
+        r = m.conv_fwd(di, stream, x, None, None, w, bias, init, silu, want_y, want_last, want_ckpt8)
+        if _done(r):
+            return {k: v for k, v in zip(("y", "last", "x8", "x8_scale"), r) if v is not None}
     packed, shape, W, st, dev = _conv_args(x, ckpt8, w, bias, init, silu, dtype)
     Bsz, D, L = shape
     out = dict(out) if out else {}
@@ -840,6 +883,12 @@ def _scratch(n, dev):
 def conv_bwd(*, gy, x=None, ckpt8=None, w, bias=None, init=None, silu=False, glast=None, want=_CONV_GRADS, out=None):
     """Gradients of <gy, y> + <glast, last> of ``conv_fwd``, from its input or its input's 8-bit checkpoint
     (then those of the values the checkpoint stands for).  Returns a dict of the gradients named in ``want``."""
+    if not out and (nat := _native(gy)) and (want is _CONV_GRADS or set(want) <= set(_CONV_GRADS)):
+        m, di, stream = nat
+        q, sc = ckpt8 if ckpt8 is not None else (None, None)
+        r = m.conv_bwd(di, stream, gy, glast, x, q, sc, w, bias, init, silu, *[k in want for k in _CONV_GRADS])
+        if _done(r):
+            return {k: v for k, v in zip(_CONV_GRADS, r) if v is not None}
     if not isinstance(gy, torch.Tensor):
         raise ValueError("gy must be a torch.Tensor")
     packed, shape, W, st, dev = _conv_args(x, ckpt8, w, bias, init, silu, gy.dtype)
@@ -895,6 +944,11 @@ def ckpt8_pack(x, *, out=None):
 def ckpt8_unpack(x8, x8_scale, *, dtype=torch.float32, out=None):
     """The stream (B, D, L) of ``dtype`` that an 8-bit checkpoint stands for (what ``scan_bwd`` and other
     readers of whole streams take)."""
+    if out is None and dtype in _STREAM and (nat := _native(x8)):
+        m, di, stream = nat
+        r = m.ckpt8_unpack(di, stream, x8, x8_scale, dtype is torch.bfloat16)
+        if _done(r):
+            return r
     x8, x8_scale = _need_ckpt8((x8, x8_scale))
     code = _stream_code(dtype, "dtype")
     Bsz, D, L = x8.shape
@@ -980,6 +1034,12 @@ def tokens_conv(*, x, w, bias=None, silu=False, pool, seq_start=None, slot=None,
     one row a sequence).  ``pool`` (slots, D, W-1) holds each sequence's last W-1 inputs; sequence s begins
     with slot[s] (zeros where ``fresh``) and leaves its own there, in place.  A slot of -1 marks an empty
     place of the batch, which leaves its row as it was.  Returns a dict with y (T, D)."""
+    if nat := _native(x):
+        m, di, stream = nat
+        y = out.get("y") if out else None
+        r = m.tokens_conv(di, stream, x, w, bias, silu, seq_start, slot, fresh, pool, y)
+        if _done(r):
+            return dict(out) if y is not None else {**(out or {}), "y": r}
     T, D, st, code, dev = _row_input(x)
     xp, sx = _rows(x, "x", st, T, D, dev)
     if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[0] != D:
@@ -1014,6 +1074,13 @@ def tokens_scan(*, delta, x, A, Bm, C, skip=None, z=None, delta_bias=None, delta
     ``delta``, ``x``, ``z`` (T, D) and ``Bm``, ``C`` (T, N) may be slices of wider rows; ``pool``
     (slots, D, N) float32 holds the states, in place; ``seq_start``, ``slot`` and ``fresh`` as in
     ``tokens_conv``; ``delta_bias`` and ``delta_softplus`` as in ``scan_fwd``.  Returns a dict with y (T, D)."""
+    if nat := _native(x):
+        m, di, stream = nat
+        y = out.get("y") if out else None
+        r = m.tokens_scan(di, stream, x, A, delta, Bm, C, z, skip, delta_bias, delta_softplus, seq_start, slot, fresh,
+                          pool, y)
+        if _done(r):
+            return dict(out) if y is not None else {**(out or {}), "y": r}
     T, D, st, code, dev = _row_input(x)
     if not isinstance(A, torch.Tensor) or A.dim() != 2 or A.shape[0] != D:
         raise ValueError(f"A must be (D, N) with D={D}")

@@ -1,7 +1,9 @@
 """Build the gfx950 shared library libssmscan.so in-tree with hipcc.
 
 Every HIP source under csrc/ and the host library csrc/api.cpp are compiled
-for gfx950 and linked into ``selective_state_space_chunked_amd/libssmscan.so``.
+for gfx950 and linked into ``selective_state_space_chunked_amd/libssmscan.so``;
+the binding's native calls (csrc/pycall.cpp, host code) become ``_pycall.so``
+beside it.
 Packed FP32 instructions are disabled for the device code; no fast-math.
 """
 from __future__ import annotations
@@ -17,6 +19,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libssmscan.so")
+PYCALL = os.path.join(PKG, "_pycall.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
@@ -43,11 +46,34 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_pycall() -> None:
+    """csrc/pycall.cpp against the installed torch and Python headers (host compiler, no GPU code)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+
+    libs = ext.library_paths()[0]
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include")]
+    for p in [*ext.include_paths(), sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", p]
+    tmp = PYCALL + ".tmp"
+    cmd += [os.path.join(CSRC, "pycall.cpp"), "-o", tmp, "-L", libs, f"-Wl,-rpath,{libs}", "-ltorch_python",
+            "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling pycall.cpp failed:\n{r.stderr}")
+    os.replace(tmp, PYCALL)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        native = ex.submit(_compile_pycall)
         objs = list(ex.map(_compile, srcs))
+        native.result()
     tmp = OUT + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -545,3 +545,95 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         for k in eager:
             assert torch.equal(eager[k], got[k]), (i, k)
+
+
+# ---------------------------------------------------------------------------
+# the binding's two ways into the library
+# ---------------------------------------------------------------------------
+def layer_calls(seed):
+    """Every function of this file once, with plain tensors; {name: outputs}."""
+    r = gen(seed)
+    D, N, W = 72, 16, 4
+    t, gy, glast = conv_inputs(2, 9, 1100, W, "bf16", True, seed)
+    par = dict(w=t["w"], bias=t["bias"], init=t["init"], silu=True)
+    o = {}
+
+    def keep(name, d):
+        o.update({f"{name} {k}": v for k, v in (d.items() if isinstance(d, dict) else [("y", d)])})
+        return d
+
+    f = keep("fwd", ssm.conv_fwd(x=t["x"], want_last=True, want_ckpt8=True, **par))
+    keep("fwd only last", ssm.conv_fwd(x=t["x"], want_y=False, want_last=True, **par))
+    keep("bwd", ssm.conv_bwd(gy=gy, glast=glast, x=t["x"], **par))
+    keep("bwd8", ssm.conv_bwd(gy=gy, ckpt8=(f["x8"], f["x8_scale"]), want=("gw", "gx"), **par))
+    keep("unpack", ssm.ckpt8_unpack(f["x8"], f["x8_scale"], dtype=torch.bfloat16))
+    keep("unpack32", ssm.ckpt8_unpack(f["x8"], f["x8_scale"]))
+    start, slot, fresh, slots = sequences([3, 0, 41, 1, 9], seed, empty=False)
+    T = int(start[-1])
+    at = dict(seq_start=torch.from_numpy(start).to(DEV), slot=torch.from_numpy(slot).to(DEV),
+              fresh=torch.from_numpy(fresh).to(DEV))
+    cpool, spool = dev(r.normal(size=(slots, D, W - 1)), "bf16"), dev(r.normal(size=(slots, D, N)))
+    x = tok_rows(T, D, "bf16", r, True, [])
+    s = scan_inputs(T, D, N, "bf16", r, view=True)
+    w, b = dev(r.normal(size=(D, W))), dev(r.normal(size=D))
+    y = torch.zeros(T, D + 8, dtype=torch.bfloat16, device=DEV)[:, :D]
+    keep("tconv", ssm.tokens_conv(x=x, w=w, bias=b, silu=True, pool=cpool, **at))
+    got = ssm.tokens_conv(x=x, w=w, pool=cpool, out={"y": y}, **at)
+    assert got["y"] is y
+    keep("tconv2", got)
+    keep("tscan", ssm.tokens_scan(**s, delta_softplus=True, pool=spool, **at))
+    step = {k: v[:5] if k in ("delta", "x", "z", "Bm", "C") else v for k, v in s.items()}
+    keep("tstep", ssm.tokens_scan(**{**step, "z": None, "skip": None}, pool=spool, slot=at["slot"]))
+    keep("pools", {"c": cpool, "s": spool})
+    torch.cuda.synchronize()
+    return o
+
+
+def test_native_calls_are_the_bindings():
+    """Without an installed allocator plain calls go through the native module: the same keys and the same bits."""
+    a = layer_calls(3)
+    ssm.set_allocator(None)
+    from selective_state_space_chunked_amd import binding
+    made = []
+    orig = binding._done
+
+    def count(r):
+        made.append(r is not NotImplemented)
+        return orig(r)
+
+    binding._done = count
+    try:
+        b = layer_calls(3)
+    finally:
+        binding._done = orig
+    assert made and all(made)
+    assert a.keys() == b.keys()
+    for k in a:
+        assert a[k].dtype == b[k].dtype and a[k].shape == b[k].shape and torch.equal(a[k], b[k]), k
+
+
+def test_native_calls_refuse_as_the_binding():
+    """Arguments the native module leaves alone raise the binding's errors; those the library refuses, the library's."""
+    ssm.set_allocator(None)
+    x, w = torch.zeros(2, 3, 10, device=DEV), torch.zeros(3, 4, device=DEV)
+    rows, pool = torch.zeros(6, 3, device=DEV), torch.zeros(4, 3, 3, device=DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    for f, kw, exc in ((ssm.conv_fwd, dict(x=x, w=torch.zeros(3, 5, device=DEV)), ssm.binding.SSMError),
+                       (ssm.conv_fwd, dict(x=x, w=torch.zeros(2, 4, device=DEV)), ValueError),
+                       (ssm.conv_fwd, dict(x=x.double(), w=w), TypeError),
+                       (ssm.conv_fwd, dict(x=x, w=w.cpu()), ValueError),
+                       (ssm.conv_bwd, dict(gy=x[..., :9], x=x, w=w), ValueError),
+                       (ssm.conv_bwd, dict(gy=x, x=x, w=w, want=("gz",)), ValueError),
+                       (ssm.tokens_conv, dict(x=rows, w=w, pool=pool), ssm.binding.SSMError),      # 6 rows, 4 slots
+                       (ssm.tokens_conv, dict(x=rows, w=w, pool=pool.bfloat16(), slot=torch.zeros(6, **i32)), TypeError),
+                       (ssm.tokens_conv, dict(x=rows, w=w, pool=pool, slot=torch.zeros(5, **i32)), ValueError),
+                       (ssm.tokens_scan, dict(delta=rows, x=rows, A=torch.zeros(3, 17, device=DEV),
+                                              Bm=torch.zeros(6, 17, device=DEV), C=torch.zeros(6, 17, device=DEV),
+                                              pool=torch.zeros(6, 3, 17, device=DEV)), ssm.binding.SSMError),
+                       (ssm.tokens_scan, dict(delta=rows, x=rows, A=torch.zeros(3, 4, device=DEV),
+                                              Bm=torch.zeros(6, 5, device=DEV), C=torch.zeros(6, 4, device=DEV),
+                                              pool=torch.zeros(6, 3, 4, device=DEV)), ValueError),
+                       (ssm.tokens_conv, dict(x=rows, w=w, pool=pool, slot=torch.zeros(6, **i32),
+                                              out={"y": rows}), ssm.binding.SSMError)):            # y over x
+        with pytest.raises(exc):
+            f(**kw)
