@@ -193,7 +193,7 @@ def _with_pycall(L):
     global _pycall
     from . import _pycall as native
     native.bind(*(ctypes.cast(getattr(L, f), _vp).value for f in (
-        "ssm_conv_fwd", "ssm_conv_bwd", "ssm_ckpt8_unpack", "ssm_tokens_conv", "ssm_tokens_scan",
+        "ssm_conv_fwd", "ssm_conv_bwd", "ssm_ckpt8_pack", "ssm_ckpt8_unpack", "ssm_tokens_conv", "ssm_tokens_scan",
         "ssm_workspace_bytes")))
     _pycall = native
     return L
@@ -926,6 +926,13 @@ def conv_bwd(*, gy, x=None, ckpt8=None, w, bias=None, init=None, silu=False, gla
 def ckpt8_pack(x, *, out=None):
     """The 8-bit checkpoint of a stream x (B, D, L): a dict with x8 (B, D, L) int8 and x8_scale
     (B, D, ceil(L / 64)) float32, one scale for every 64 steps of a row."""
+    if not out and (nat := _native(x)):
+        m, di, stream = nat
+        r = m.ckpt8_pack(di, stream, x)
+        if _done(r):
+            return {"x8": r[0], "x8_scale": r[1]}
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("x must be a torch.Tensor")
     _need(x, "x", view=True)
     code = _stream_code(x.dtype, "x")
     if x.dim() != 3:

@@ -18,11 +18,13 @@ namespace {
 struct Calls {
     decltype(&ssm_conv_fwd) conv_fwd;
     decltype(&ssm_conv_bwd) conv_bwd;
+    decltype(&ssm_ckpt8_pack) pack;
     decltype(&ssm_ckpt8_unpack) unpack;
     decltype(&ssm_tokens_conv) tokens_conv;
     decltype(&ssm_tokens_scan) tokens_scan;
     decltype(&ssm_workspace_bytes) bytes;
 } g{};
+constexpr int kCalls = 7;
 
 // The arguments of one call, checked one by one; `ok` turns false at the first that is not as expected.
 struct Args {
@@ -337,6 +339,25 @@ PyObject* conv_bwd(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
     });
 }
 
+// x -> (x8, x8_scale)
+PyObject* ckpt8_pack(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+    return guarded([&]() -> PyObject* {
+        Args in{argv, argc};
+        in.dev = (int)in.whole();
+        void* stream = (void*)(intptr_t)in.whole();
+        const at::Tensor* x = in.tensor(true);
+        if (!x || x->dim() != 3 || !stream_type(x->scalar_type()) || !x->is_contiguous()) return none_of_these();
+        ssm_ckpt8_args a{};
+        a.dtype = code(x->scalar_type());
+        a.batch = x->size(0); a.channels = x->size(1); a.length = x->size(2);
+        at::Tensor x8 = fresh(x->sizes(), at::kChar, in.dev);
+        at::Tensor sc = fresh({a.batch, a.channels, (a.length + SSM_CKPT8_BLOCK - 1) / SSM_CKPT8_BLOCK}, at::kFloat, in.dev);
+        if (int rc = g.pack(&a, x->data_ptr(), (int8_t*)x8.data_ptr(), (float*)sc.data_ptr(), stream))
+            return PyLong_FromLong(rc);
+        return Py_BuildValue("(NN)", wrapped(x8), wrapped(sc));
+    });
+}
+
 // x8, x8_scale, 1 for bf16 -> y
 PyObject* ckpt8_unpack(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
     return guarded([&]() -> PyObject* {
@@ -360,20 +381,21 @@ PyObject* ckpt8_unpack(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
 
 // addresses of the library's functions, in the order of Calls
 PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
-    if (argc != 6) {
-        PyErr_SetString(PyExc_TypeError, "bind takes six addresses");
+    if (argc != kCalls) {
+        PyErr_SetString(PyExc_TypeError, "bind takes the addresses of Calls");
         return nullptr;
     }
-    void* p[6];
-    for (int i = 0; i < 6; ++i) {
+    void* p[kCalls];
+    for (int i = 0; i < kCalls; ++i) {
         p[i] = PyLong_AsVoidPtr(argv[i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "address 0");
             return nullptr;
         }
     }
-    g = Calls{(decltype(g.conv_fwd))p[0],    (decltype(g.conv_bwd))p[1],    (decltype(g.unpack))p[2],
-              (decltype(g.tokens_conv))p[3], (decltype(g.tokens_scan))p[4], (decltype(g.bytes))p[5]};
+    g = Calls{(decltype(g.conv_fwd))p[0], (decltype(g.conv_bwd))p[1],    (decltype(g.pack))p[2],
+              (decltype(g.unpack))p[3],   (decltype(g.tokens_conv))p[4], (decltype(g.tokens_scan))p[5],
+              (decltype(g.bytes))p[6]};
     Py_RETURN_NONE;
 }
 
@@ -396,6 +418,7 @@ PyMethodDef methods[] = {
     {"tokens_scan", (PyCFunction)(void (*)(void))counted<tokens_scan, 16>, METH_FASTCALL, nullptr},
     {"conv_fwd", (PyCFunction)(void (*)(void))counted<conv_fwd, 12>, METH_FASTCALL, nullptr},
     {"conv_bwd", (PyCFunction)(void (*)(void))counted<conv_bwd, 15>, METH_FASTCALL, nullptr},
+    {"ckpt8_pack", (PyCFunction)(void (*)(void))counted<ckpt8_pack, 3>, METH_FASTCALL, nullptr},
     {"ckpt8_unpack", (PyCFunction)(void (*)(void))counted<ckpt8_unpack, 5>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pycall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -566,6 +566,7 @@ def layer_calls(seed):
     keep("fwd only last", ssm.conv_fwd(x=t["x"], want_y=False, want_last=True, **par))
     keep("bwd", ssm.conv_bwd(gy=gy, glast=glast, x=t["x"], **par))
     keep("bwd8", ssm.conv_bwd(gy=gy, ckpt8=(f["x8"], f["x8_scale"]), want=("gw", "gx"), **par))
+    keep("pack", ssm.ckpt8_pack(t["x"]))
     keep("unpack", ssm.ckpt8_unpack(f["x8"], f["x8_scale"], dtype=torch.bfloat16))
     keep("unpack32", ssm.ckpt8_unpack(f["x8"], f["x8_scale"]))
     start, slot, fresh, slots = sequences([3, 0, 41, 1, 9], seed, empty=False)
