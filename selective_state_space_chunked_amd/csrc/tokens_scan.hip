@@ -183,14 +183,20 @@ struct ScanLane {
 #pragma unroll
                 for (int g = 0; g < kGrp; ++g) {
                     dl[g] = to_f32(rd[g]) + bias;
-                    xv[g] = i + g < n ? to_f32(rx[g]) : 0.0f;
+                    xv[g] = to_f32(rx[g]);
                     zv[g] = OUT ? to_f32(rz[g]) : 0.0f;
                 }
                 load();
 #pragma unroll
                 for (int g = 0; g < kGrp; ++g) {
                     if (FULL || softplus) dl[g] = softplus_t(dl[g]);
-                    dl[g] = i + g < n ? dl[g] : 0.0f;
+                }
+                if (i + kGrp > n) {
+#pragma unroll
+                    for (int g = 0; g < kGrp; ++g) {
+                        dl[g] = i + g < n ? dl[g] : 0.0f;
+                        xv[g] = i + g < n ? xv[g] : 0.0f;
+                    }
                 }
                 const buffer_t yg = buffer_of(py, (uint32_t)(min(kGrp, n - i) - 1) * by + row_bytes);
 #pragma unroll
