@@ -247,7 +247,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_sum
     if (s >= 0 && s < p.q.S) {
         st = q.first(s);
         en = q.end(s);
-        if (st >= 0 && en > r.r1) slot = q.slot(s);
+        if (st >= 0 && st < r.r1 && en > r.r1) slot = q.slot(s);   // st beyond: the list does not ascend
     }
     if (cb == 0 && lane_id() == 0) p.through[c] = slot >= 0 && st < r.r0;
     if (slot < 0) return;   // none crosses the end

@@ -378,7 +378,7 @@ def test_tokens_scan_without_gate_or_transform(gate, softplus, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("S,D,N,W", [(1, 1, 1, 2), (1, 64, 16, 4), (7, 37, 5, 3), (70, 72, 16, 4), (33, 264, 8, 2),
-                                     (130, 40, 16, 4)])
+                                     (130, 40, 16, 4), (9, 40, 12, 4), (5, 300, 4, 3), (3, 513, 8, 2)])
 def test_steps(S, D, N, W, dtype):
     """The step forms: one row a sequence, with empty places and a slot named twice."""
     r = gen(S + D)
@@ -404,6 +404,109 @@ def test_steps(S, D, N, W, dtype):
     ssm.tokens_scan(**t, delta_softplus=True, pool=pool, slot=ti(slot), fresh=ti(fresh), out={"y": y})
     R.check("scan y", y, ref, err, dtype)
     R.check("scan pool", pool, pref, np.nan_to_num(perr), "f32")
+
+
+def test_thousands_of_sequences():
+    """More sequences than one round of the search through seq_start tells apart."""
+    r = gen(61)
+    D, N, W, S = 24, 5, 3, 5003
+    start = np.concatenate([[0], np.cumsum(r.integers(0, 3, S))]).astype(np.int32)
+    T = int(start[-1])
+    slot = r.permutation(S).astype(np.int32)
+    slot[17::100] = -1
+    slot[4000] = slot[3]        # an earlier sequence has it
+    fresh = r.random(S) < 0.5
+    at = dict(seq_start=torch.from_numpy(start).to(DEV), slot=torch.from_numpy(slot).to(DEV),
+              fresh=torch.from_numpy(fresh).to(DEV))
+    x, w = tok_rows(T, D, "f32", r, False, []), dev(r.normal(size=(D, W)))
+    pool, y = dev(r.normal(size=(S, D, W - 1))), dev(r.normal(size=(T, D)))
+    ref, err, pref = R.tokens_conv(f64(x), f64(w), None, False, f64(pool), start, slot, fresh, f64(y))
+    ssm.tokens_conv(x=x, w=w, pool=pool, out={"y": y}, **at)
+    R.check("conv y", y, ref, err, "f32")
+    R.check("conv pool", pool, pref, 0 * pref, "f32")
+    t = scan_inputs(T, D, N, "f32", r)
+    pool, y = dev(r.normal(size=(S, D, N))), dev(r.normal(size=(T, D)))
+    ref, err, pref, perr = scan_ref(t, True, pool, start, slot, fresh, y)
+    ssm.tokens_scan(**t, delta_softplus=True, pool=pool, out={"y": y}, **at)
+    R.check("scan y", y, ref, err, "f32")
+    R.check("scan pool", pool, pref, perr, "f32")
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_lists_that_do_not_ascend_stay_inside_the_buffers(many):
+    """seq_start, slot and fresh are not checked on the host: whatever they hold, nothing outside the rows of y and the
+    slots of the pool is written (what the rows then hold is unspecified)."""
+    r = gen(62)
+    D, N, W, T, S = 40, 16, 4, 300, 90 if many else 6
+    big = np.iinfo(np.int32)
+    starts = [[250, 0, 10, 290, 20, 300, 0], [500, 600, -7, 40, big.max, big.min, 299], [big.max] * 7,
+              [-3, 200, 100, 299, 298, 10, 1000], [299, 300, 301, 302, 303, 304, 305], [300, 250, 200, 150, 100, 50, 0]]
+    if many:
+        starts = [r.integers(-50, 400, S + 1) for _ in range(4)] + [np.arange(S, -1, -1) * 4]
+    rows = torch.full((T + 2, D + 9), 7.0, device=DEV)
+    pools = [torch.full((S + 2, D, k), 7.0, device=DEV) for k in (W - 1, N)]
+    w, x = dev(r.normal(size=(D, W))), tok_rows(T, D, "f32", r, True, [])
+    t = scan_inputs(T, D, N, "f32", r, view=True)
+    for i, st in enumerate(starts):
+        slot = r.integers(0, S, S)
+        slot[i % S] = (big.max, big.min, S, -1)[i % 4]
+        at = dict(seq_start=torch.tensor(np.asarray(st), dtype=torch.int32, device=DEV),
+                  slot=torch.tensor(slot, dtype=torch.int32, device=DEV),
+                  fresh=torch.tensor(r.integers(0, 256, S), dtype=torch.uint8, device=DEV))
+        y = rows[1:T + 1, 4:4 + D]
+        ssm.tokens_conv(x=x, w=w, pool=pools[0][1:-1], out={"y": y}, **at)
+        ssm.tokens_scan(**t, delta_softplus=True, pool=pools[1][1:-1], out={"y": y}, **at)
+        torch.cuda.synchronize()
+        assert (rows[0] == 7).all() and (rows[-1] == 7).all() and (rows[:, :4] == 7).all() and (rows[:, 4 + D:] == 7).all()
+        assert all((p[0] == 7).all() and (p[-1] == 7).all() for p in pools)
+
+
+def test_offsets_past_32_bits():
+    """Rows and slots of the widest strides, and batch rows 2^32 elements apart: as the same tensors laid out densely."""
+    r = gen(63)
+    D, N, W, T, S = 24, 16, 4, 70, 3
+    wide, wide_out = (torch.empty(T * 2**26, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+
+    def spread(v, at):
+        o = wide.as_strided(v.shape, (2**26 - 1, 1), at)
+        o.copy_(v)
+        return o
+
+    t = scan_inputs(T, D, N, "bf16", r)
+    far = {k: spread(t[k], 100 * i) for i, k in enumerate(("delta", "x", "z", "Bm", "C"))}
+    w = dev(r.normal(size=(D, W)))
+    at = dict(seq_start=torch.tensor([0, 33, 34, T], dtype=torch.int32, device=DEV),
+              slot=torch.tensor([2, 0, 1], dtype=torch.int32, device=DEV))
+    for k, inner, dt in (("c", W - 1, torch.bfloat16), ("s", N, torch.float32)):
+        first = torch.randn(S, D, inner, device=DEV).to(dt)
+        base = torch.empty(2 * (2**30 + 4) + D * inner, dtype=dt, device=DEV)
+        res = []
+        for f in (False, True):
+            for step in (False, True):
+                pool = base.as_strided(first.shape, (2**30 + 4, inner, 1)) if f else torch.empty_like(first)
+                pool.copy_(first)
+                a = {**t, **far} if f else t
+                a = {n: v[:S] if step and n in far else v for n, v in a.items()}
+                on = dict(slot=at["slot"]) if step else at
+                out = {"y": wide_out.as_strided((S if step else T, D), (2**26 - 1, 1), 900)} if f else {}
+                y = (ssm.tokens_conv(x=a["x"], w=w, pool=pool, out=out, **on) if k == "c" else
+                     ssm.tokens_scan(**a, delta_softplus=True, pool=pool, out=out, **on))["y"]
+                res += [y.clone(), pool.clone()]
+        for p, q in zip(res[:4], res[4:]):
+            assert torch.equal(p, q), k
+        del base, pool
+    x = dev(r.normal(size=(2, 3, 700)), "bf16")
+    gy = dev(r.normal(size=(2, 3, 700)), "bf16")
+    fx, fg, fo = (v.as_strided(x.shape, (2**32, 2**20, 1), i) for v, i in ((wide, 0), (wide, 5000), (wide_out, 3)))
+    fx.copy_(x)
+    fg.copy_(gy)
+    par = dict(w=w[:3], silu=True)
+    assert torch.equal(ssm.conv_fwd(x=fx, out={"y": fo}, **par)["y"], ssm.conv_fwd(x=x, **par)["y"])
+    p, q = ssm.conv_bwd(x=x, gy=gy, **par), ssm.conv_bwd(x=fx, gy=fg, out={"gx": fo}, **par)
+    assert all(torch.equal(p[k], q[k]) for k in p)
+    p, q = ssm.ckpt8_pack(x), ssm.ckpt8_pack(fx)
+    assert all(torch.equal(p[k], q[k]) for k in p)
+    assert torch.equal(ssm.ckpt8_unpack(**p, dtype=torch.bfloat16, out=fo), ssm.ckpt8_unpack(**p, dtype=torch.bfloat16))
 
 
 def test_pool_of_a_layer_among_others():
@@ -611,6 +714,13 @@ def test_native_calls_are_the_bindings():
     assert a.keys() == b.keys()
     for k in a:
         assert a[k].dtype == b[k].dtype and a[k].shape == b[k].shape and torch.equal(a[k], b[k]), k
+
+
+def test_wanted_gradients_from_an_iterator():
+    t, gy, glast = conv_inputs(1, 4, 40, 4, "f32", True, 64)
+    par = dict(gy=gy, glast=glast, x=t["x"], w=t["w"], bias=t["bias"], init=t["init"])
+    every, some = ssm.conv_bwd(**par), ssm.conv_bwd(want=(k for k in ("gw", "ginit")), **par)
+    assert set(some) == {"gw", "ginit"} and all(torch.equal(some[k], every[k]) for k in some)
 
 
 def test_native_calls_refuse_as_the_binding():
