@@ -883,6 +883,8 @@ def _scratch(n, dev):
 def conv_bwd(*, gy, x=None, ckpt8=None, w, bias=None, init=None, silu=False, glast=None, want=_CONV_GRADS, out=None):
     """Gradients of <gy, y> + <glast, last> of ``conv_fwd``, from its input or its input's 8-bit checkpoint
     (then those of the values the checkpoint stands for).  Returns a dict of the gradients named in ``want``."""
+    if want is not _CONV_GRADS:
+        want = tuple(want)
     if not out and (nat := _native(gy)) and (want is _CONV_GRADS or set(want) <= set(_CONV_GRADS)):
         m, di, stream = nat
         q, sc = ckpt8 if ckpt8 is not None else (None, None)
