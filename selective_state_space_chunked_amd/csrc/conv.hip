@@ -6,7 +6,18 @@
 //
 // W is 2 to 4, so a step takes a handful of operations on the 4 (bf16) to 8
 // bytes it moves: the kernels are bound by HBM.  A lane takes 8 consecutive
-// steps of a row.
+// steps of a row: one 16-byte access of bf16, and the W-1 steps it needs beside
+// its own are a lane's away.
+//
+// Measured, kernel time and bytes moved (a copy of 256 MiB runs at 4.9 TB/s,
+// read + written):
+//   B=8 D=2048 L=4096 W=4 bf16   forward                65 us   4.1 TB/s
+//                                forward + checkpoint   83 us   4.1 TB/s
+//                                backward               92 us   4.4 TB/s
+//                                backward from 8 bits   99 us   3.4 TB/s
+//                                checkpoint to bf16     34 us   6.0 TB/s
+//   B=1 D=1024 L=128000 f32      checkpoint            144 us   4.6 TB/s
+//                                checkpoint to f32     126 us   5.3 TB/s
 #include <algorithm>
 
 #include "common.hpp"
@@ -187,7 +198,9 @@ struct Run8 {
 
 // Forward: a workgroup takes TX lanes' runs of TY rows (TX * TY = 256), UNITS neighbouring groups of rows, with all
 // loads issued before the first is used; the grid runs along the steps first, so the workgroups under way sweep
-// the streams in order.  With P8 the eight lanes of a 64-step block agree on its scale (TX >= 8).
+// the streams in order (along the channels first it takes longer).  A lane's inputs before its own come from its left
+// neighbour by a lane move, at a wave's first lane from memory (lanes 0 .. W-2 load them with the rest).  With P8 the
+// eight lanes of a 64-step block agree on its scale (TX >= 8).
 template <typename T, int W, bool X8, bool P8, int UNITS>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int dblocks) {
     constexpr int H = W - 1, R = kConvRun;
@@ -374,7 +387,9 @@ __device__ __forceinline__ void lds_barrier() { __asm__ volatile("s_waitcnt lgkm
 // gradients after it come from the lanes beside it, between waves through LDS.
 // The items are taken 256 at a time from the last to the first, so the gradients
 // after a group are those of the group before; the next group's loads are under
-// way while one is computed.
+// way while one is computed.  Bound by HBM, with about 60 % of the time in its 42
+// vector instructions a step (a silu and its slope, W products three times over).
+// B=8 D=2048 L=4096 bf16: one group a workgroup 135 us, eight 92.
 template <typename T, int W, bool X8>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
     constexpr int H = W - 1, R = kConvRun;
@@ -517,7 +532,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
         else if (p.gbias) p.gbias[d] = a;
     }
 }
-// the parts of gw and gbias, added in order
+// the parts of gw and gbias, added in order (10240 sums of 2 parts: 5 us, of which a launch is 3)
 __global__ __launch_bounds__(256) void conv_reduce_kernel(ConvParams p) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = (int64_t)p.D * (p.W + 1);
     if (i >= n) return;
@@ -529,7 +544,7 @@ __global__ __launch_bounds__(256) void conv_reduce_kernel(ConvParams p) {
     else if (p.gbias) p.gbias[d] = a;
 }
 
-// the stream that a checkpoint stands for; workgroups as in the forward
+// the stream that a checkpoint stands for; workgroups as in the forward.  Bound by its writes.
 template <typename T, int UNITS>
 __global__ __launch_bounds__(256) void ckpt8_unpack_kernel(ConvParams p, int dblocks) {
     constexpr int R = kConvRun;
