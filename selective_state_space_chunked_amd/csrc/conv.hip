@@ -13,13 +13,14 @@
 // read + written):
 //   B=8 D=2048 L=4096 W=4 bf16   forward                65 us   4.1 TB/s
 //                                forward + checkpoint   83 us   4.1 TB/s
-//                                backward               92 us   4.4 TB/s
-//                                backward from 8 bits   99 us   3.4 TB/s
+//                                backward               77 us   5.2 TB/s
+//                                backward from 8 bits   82 us   4.1 TB/s
 //                                checkpoint to bf16     34 us   6.0 TB/s
 //   B=1 D=1024 L=128000 f32      checkpoint            144 us   4.6 TB/s
 //                                checkpoint to f32     126 us   5.3 TB/s
 #include <algorithm>
 
+#include "buffer.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -121,15 +122,14 @@ __device__ __forceinline__ uint32_t four_bytes(const uint32_t* k) {
     return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
 }
 
-// gy act'(p) of the step whose window is e[0..W-1]
+// gy silu'(p) of the step whose window is e[0..W-1]
 template <int W>
-__device__ __forceinline__ float grad_pre(const float* e, const float (&w)[W], float bias, float gy, int silu) {
+__device__ __forceinline__ float grad_pre(const float* e, const float (&w)[W], float bias, float gy) {
     float a = bias;
 #pragma unroll
     for (int k = 0; k < W; ++k) a = fmaf(w[k], e[k], a);
-    if (!silu) return gy;
-    const float s = sigmoid_f(a);
-    return gy * s * fmaf(a, 1.0f - s, 1.0f);
+    const float s = sigmoid_f(a), gs = gy * s;   // gy s (1 + a (1 - s))
+    return fmaf(gs, fmaf(-a, s, a), gs);
 }
 
 // A run of eight steps as loaded, turned into floats where it is used (so loads stay under way meanwhile).
@@ -381,15 +381,36 @@ struct BwdAt {
 // workgroup barrier that waits for LDS accesses only: loads and stores of global memory stay under way
 __device__ __forceinline__ void lds_barrier() { __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// a workgroup's sums of gw and gbias, of its lanes' acc
+template <int W>
+__device__ __forceinline__ void bwd_sums(const ConvParams& p, int d, int part, const float (&acc)[W + 1]) {
+    const int lane = lane_id();
+    if (!p.gw && !p.gbias) return;
+    __shared__ float sum[4][W + 1];
+#pragma unroll
+    for (int k = 0; k <= W; ++k) {
+        float a = acc[k];
+        for (int m = 32; m; m >>= 1) a += __shfl_xor(a, m);
+        if (lane == 0) sum[threadIdx.x >> 6][k] = a;
+    }
+    __syncthreads();
+    if (threadIdx.x <= W) {
+        const int k = threadIdx.x;
+        const float a = (sum[0][k] + sum[1][k]) + (sum[2][k] + sum[3][k]);
+        if (p.parts > 1) p.part[((int64_t)part * p.D + d) * (W + 1) + k] = a;
+        else if (k < W) { if (p.gw) p.gw[(int64_t)d * W + k] = a; }
+        else if (p.gbias) p.gbias[d] = a;
+    }
+}
 // Backward: a workgroup takes the items (batch row, run) [part * per_part, ..)
 // of one channel and leaves its sums of gw and gbias: no atomics, one order.
 // Neighbouring lanes hold neighbouring items, so the inputs before a run and the
 // gradients after it come from the lanes beside it, between waves through LDS.
 // The items are taken 256 at a time from the last to the first, so the gradients
 // after a group are those of the group before; the next group's loads are under
-// way while one is computed.  Bound by HBM, with about 60 % of the time in its 42
-// vector instructions a step (a silu and its slope, W products three times over).
-// B=8 D=2048 L=4096 bf16: one group a workgroup 135 us, eight 92.
+// way while one is computed.  For short rows (no whole tile of 512 steps, or a fifth
+// of the lanes idle in the kernel below): B=2 D=195 L=517 f32 5.4 us, of which a
+// launch is 3.
 template <typename T, int W, bool X8>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
     constexpr int H = W - 1, R = kConvRun;
@@ -431,7 +452,11 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
 #pragma unroll
         for (int j = 0; j < R; ++j) e[H + j] = v[j];
 #pragma unroll
-        for (int j = 0; j < R; ++j) gp[j] = grad_pre<W>(e + j, w, bias, g[j], p.silu);
+        for (int j = 0; j < R; ++j) gp[j] = g[j];
+        if (p.silu) {   // one branch for the run: its steps' exp2 and reciprocals overlap
+#pragma unroll
+            for (int j = 0; j < R; ++j) gp[j] = grad_pre<W>(e + j, w, bias, g[j]);
+        }
         if (!c.full) {
 #pragma unroll
             for (int j = 0; j < R; ++j) gp[j] = j < n ? gp[j] : 0.0f;
@@ -460,7 +485,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
                 gr[i] = t < p.L ? to_f32(gy[t]) : 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < H; ++i) gp[R + i] = grad_pre<W>(f + i, w, bias, gr[i], p.silu);
+            for (int i = 0; i < H; ++i) gp[R + i] = p.silu ? grad_pre<W>(f + i, w, bias, gr[i]) : gr[i];
         }
         if (n < R + H) {   // none after the row's last step
 #pragma unroll
@@ -515,22 +540,183 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
         }
         c = nx;
     }
-    if (!p.gw && !p.gbias) return;
-    __shared__ float sum[4][W + 1];
+    bwd_sums<W>(p, d, part, acc);
+}
+
+// Backward of rows of some length.  As above, but a wave takes tiles of 64 runs of one row each and forms the gradients
+// after a tile again (one lane a step, from the inputs and gradients there), so waves wait for nothing of each other;
+// a tile's row and place are scalar, and a lane's addresses are its fixed offset from them.  Whole tiles and rows'
+// ends are taken apart: the loop over whole tiles issues the same loads and stores in every turn, so the wait for a
+// tile's loads is one for these alone, with the next tile's loads and the last one's stores under way (with a branch
+// around either the compiler has to wait for everything).  Bound by HBM, with half of the time in its 34 vector
+// instructions a step.  B=8 D=2048 L=4096 bf16: 77 us, from 8 bits 82 us; the kernel above takes 92 and 99.
+template <typename T, int W, bool X8>
+struct RowTile {
+    static constexpr int H = W - 1, R = kConvRun, N = 64 * R;   // steps of a tile
+    Run<T> g, x;
+    Run8 q;
+    T ex;         // lane i < H: the input H - i steps before the tile; lane 32 + i, i < 2 H: i - H steps from its end
+    int8_t exq;   // the same of a checkpoint
+    float exs;
+    T eg;         // lane 32 + i, i < H: gy i steps from the tile's end
+    // a whole tile
+    __device__ __forceinline__ void load(const ConvParams& p, int b, int d, int seg) {
+        const int lane = lane_id(), first = seg * N, at = lane * R;
+        const T* gy = (const T*)p.gy + b * p.sgy[0] + d * p.sgy[1] + first;
+        const Row<T, X8> in = row_of<T, X8>(p, b, d);
+        g.load(gy + at);
+        if (X8) q.load(in.q + first + at, in.s + first / kCkptBlock + at / kCkptBlock);
+        else x.load(in.x + first + at);
+        edges(p, in, gy, first);
+    }
+    // the first `left` steps of a row's last one
+    __device__ __forceinline__ void load(const ConvParams& p, int b, int d, int seg, int left) {
+        const int lane = lane_id(), first = seg * N, at = lane * R;
+        const T* gy = (const T*)p.gy + b * p.sgy[0] + d * p.sgy[1] + first;
+        const Row<T, X8> in = row_of<T, X8>(p, b, d);
+        g.load(gy + at, left - at);
+        if (X8) q.load(in.q + first + at, in.s + first / kCkptBlock + at / kCkptBlock, left - at);
+        else x.load(in.x + first + at, left - at);
+        edges(p, in, gy, first);
+    }
+    __device__ __forceinline__ void edges(const ConvParams& p, const Row<T, X8>& in, const T* gy, int first) {
+        const int lane = lane_id(), i = lane & 31, t = (lane < 32 ? 0 : N) - H + i;   // from the tile's first step
+        const bool has = i < (lane < 32 ? H : 2 * H);
+        const int lo = max(first - H, 0), some = min(p.L - lo, N + 2 * H);   // the first step in reach, and their number
+        const uint32_t at = has ? (uint32_t)(first + t - lo) : 0x3fffffffu;     // before the row: past every end
+        if (X8) {
+            const int s0 = max(first / kCkptBlock - 1, 0);
+            exq = buffer_load<int8_t>(buffer_of(in.q + lo, (uint32_t)some), at);
+            exs = buffer_load<float>(buffer_of(in.s + s0, (uint32_t)min(p.nblk - s0, 16) * 4),
+                                     has ? (uint32_t)(first / kCkptBlock + (t >> 6) - s0) * 4 : 0x7fffffffu);
+        } else {
+            ex = buffer_load<T>(buffer_of(in.x + lo, (uint32_t)some * sizeof(T)), at * sizeof(T));
+        }
+        const int after = min(max(p.L - first - N, 0), H);
+        eg = buffer_load<T>(buffer_of(gy + N, (uint32_t)after * sizeof(T)),
+                            lane >= 32 ? (uint32_t)i * sizeof(T) : 0x7fffffffu);
+    }
+    __device__ __forceinline__ float edge() const { return X8 ? (float)exq * exs : to_f32(ex); }
+};
+template <typename T, int W, bool X8, bool GX, bool FULL>
+__device__ __forceinline__ void bwd_tile(const ConvParams& p, const RowTile<T, W, X8>& c, int b, int d, int seg,
+                                         const float (&w)[W], float bias, float (&acc)[W + 1]) {
+    constexpr int H = W - 1, R = kConvRun, N = 64 * R;
+    const int lane = lane_id(), left = p.L - seg * N, n = left - lane * R;   // steps from the tile's, the lane's first one on
+    float v[R], e[R + H], gp[R + H], gr[R], ex = c.edge();
+    if (X8) c.q.get(v);
+    else c.x.get(v);
+    c.g.get(gr);
+    if (p.init && seg == 0) {
+        if (lane < H) ex = to_f32(((const T*)p.init)[((int64_t)b * p.D + d) * H + lane]);
+        __asm__ volatile("" : "+v"(ex));   // waited for here, not where every tile passes
+    }
 #pragma unroll
-    for (int k = 0; k <= W; ++k) {
-        float a = acc[k];
-        for (int m = 32; m; m >>= 1) a += __shfl_xor(a, m);
-        if (lane == 0) sum[threadIdx.x >> 6][k] = a;
+    for (int i = 0; i < H; ++i)
+        e[i] = from_left(v[R - H + i], __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ex), i)));
+    float f[W], ga = to_f32(c.eg);   // lane 32 + i: the window of the step i after the tile, and its gradient
+    f[0] = ex;
+#pragma unroll
+    for (int k = 1; k < W; ++k) f[k] = from_right(f[k - 1], 0.0f);
+#pragma unroll
+    for (int j = 0; j < R; ++j) e[H + j] = v[j];
+#pragma unroll
+    for (int j = 0; j < R; ++j) gp[j] = gr[j];
+    if (p.silu) {   // one branch for the run: its steps' exp2 and reciprocals overlap
+#pragma unroll
+        for (int j = 0; j < R; ++j) gp[j] = grad_pre<W>(e + j, w, bias, gr[j]);
+        ga = grad_pre<W>(f, w, bias, ga);
     }
-    __syncthreads();
-    if (threadIdx.x <= W) {
-        const int k = threadIdx.x;
-        const float a = (sum[0][k] + sum[1][k]) + (sum[2][k] + sum[3][k]);
-        if (p.parts > 1) p.part[((int64_t)part * p.D + d) * (W + 1) + k] = a;
-        else if (k < W) { if (p.gw) p.gw[(int64_t)d * W + k] = a; }
-        else if (p.gbias) p.gbias[d] = a;
+    if (!FULL) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) gp[j] = j < n ? gp[j] : 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+        const float edge = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ga), 32 + i));
+        gp[R + i] = from_right(gp[i], left > N + i ? edge : 0.0f);   // none after the row's last step
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        if (FULL || j < n) {   // steps past the end add nothing, whatever lies there
+#pragma unroll
+            for (int q = 0; q < W; ++q) acc[q] = fmaf(gp[j], e[j + q], acc[q]);
+            acc[W] += gp[j];
+        }
+    }
+    const T* gl = p.glast ? (const T*)p.glast + ((int64_t)b * p.D + d) * H : nullptr;
+    if (GX) {
+        float o[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            float a = 0.0f;
+#pragma unroll
+            for (int q = 0; q < W; ++q) a = fmaf(w[q], gp[j + H - q], a);
+            o[j] = a;
+        }
+        if (gl && left < N + H && n > 0 && n < R + H) {   // the last W-1 steps
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                if (j < n && j + H >= n) o[j] += to_f32(gl[j + H - n]);
+        }
+        T* gx = (T*)p.gx + b * p.sgx[0] + d * p.sgx[1] + seg * N;
+        store_stream(gx + lane * R, o, FULL ? R : n);
+    }
+    if (p.ginit && seg == 0 && lane == 0) {
+        T* gi = (T*)p.ginit + ((int64_t)b * p.D + d) * H;
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            float a = 0.0f;
+#pragma unroll
+            for (int q = 0; q <= j; ++q) a = fmaf(w[q], gp[j - q], a);
+            if (gl && j >= n) a += to_f32(gl[j - n]);
+            gi[j] = from_f32<T>(a);
+        }
+    }
+}
+template <typename T, int W, bool X8, bool GX>
+__global__ __launch_bounds__(256) void conv_bwd_rows_kernel(ConvParams p) {
+    constexpr int N = 64 * kConvRun;
+    const int d = blockIdx.x % p.D, part = blockIdx.x / p.D, wave = uniform((int)threadIdx.x >> 6);
+    float w[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = p.w[(int64_t)d * W + k];
+    const float bias = p.bias ? p.bias[d] : 0.0f;
+    float acc[W + 1] = {};
+    const int t0 = part * p.per_part + wave, t1 = min((part + 1) * p.per_part, p.B * p.tiles);   // whole tiles t0, t0 + 4, ..
+    if (t0 < t1) {
+        RowTile<T, W, X8> c, nx;
+        int t = t0, b = t0 / p.tiles, seg = t0 - b * p.tiles, nb = b, ns = seg;
+        auto next = [&] {   // the place of the wave's next tile; after the last one, that one's again
+            if (t + 4 >= t1) return;
+            ns += 4;
+            while (ns >= p.tiles) {
+                ns -= p.tiles;
+                ++nb;
+            }
+        };
+        c.load(p, b, d, seg);
+        for (;;) {
+            next();
+            nx.load(p, nb, d, ns);
+            bwd_tile<T, W, X8, GX, true>(p, c, b, d, seg, w, bias, acc);
+            b = nb; seg = ns; t += 4;
+            if (t >= t1) break;
+            next();
+            c.load(p, nb, d, ns);
+            bwd_tile<T, W, X8, GX, true>(p, nx, b, d, seg, w, bias, acc);
+            b = nb; seg = ns; t += 4;
+            if (t >= t1) break;
+        }
+    }
+    if (p.L > p.tiles * N) {   // the rows' ends
+        for (int b = part + p.parts * wave; b < p.B; b += p.parts * 4) {
+            RowTile<T, W, X8> c;
+            c.load(p, b, d, p.tiles, p.L - p.tiles * N);
+            bwd_tile<T, W, X8, GX, false>(p, c, b, d, p.tiles, w, bias, acc);
+        }
+    }
+    bwd_sums<W>(p, d, part, acc);
 }
 // the parts of gw and gbias, added in order (10240 sums of 2 parts: 5 us, of which a launch is 3)
 __global__ __launch_bounds__(256) void conv_reduce_kernel(ConvParams p) {
@@ -615,7 +801,14 @@ template <typename T, int W>
 hipError_t conv_bwd_w(const ConvParams& p, hipStream_t st) {
     const int64_t blocks = (int64_t)p.D * p.parts;
     if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
-    if (p.x8) conv_bwd_kernel<T, W, true><<<(unsigned)blocks, 256, 0, st>>>(p);
+    if (p.tiles && p.x8) {
+        if (p.gx) conv_bwd_rows_kernel<T, W, true, true><<<(unsigned)blocks, 256, 0, st>>>(p);
+        else conv_bwd_rows_kernel<T, W, true, false><<<(unsigned)blocks, 256, 0, st>>>(p);
+    } else if (p.tiles) {
+        if (p.gx) conv_bwd_rows_kernel<T, W, false, true><<<(unsigned)blocks, 256, 0, st>>>(p);
+        else conv_bwd_rows_kernel<T, W, false, false><<<(unsigned)blocks, 256, 0, st>>>(p);
+    }
+    else if (p.x8) conv_bwd_kernel<T, W, true><<<(unsigned)blocks, 256, 0, st>>>(p);
     else conv_bwd_kernel<T, W, false><<<(unsigned)blocks, 256, 0, st>>>(p);
     return hipGetLastError();
 }

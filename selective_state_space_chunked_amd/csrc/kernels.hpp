@@ -281,7 +281,7 @@ double roof_instrs_per_lane(int kind, int chains, int iters);
 constexpr int kConvRun = 8;     // consecutive steps of one lane
 constexpr int kCkptBlock = 64;  // steps that share a scale
 // backward: groups of 256 items a workgroup takes at most, and the workgroups there should be before it takes more
-// than one (B=8 D=2048 L=4096 bf16, kernel us with 1, 2, 4, 8 groups: 135, 100, 95, 90)
+// than one (B=8 D=2048 L=4096 bf16 with the sums over parts, us: 4 groups 98, 8 groups 93, 16 groups, one part, 97)
 constexpr int kConvGroups = 8, kConvWG = 4096, kConvOne = 4;
 struct ConvParams {
     const void* x; const int8_t* x8; const float* x8_scale;
@@ -292,7 +292,8 @@ struct ConvParams {
     float* part;                     // (parts, D, W + 1) partial sums of gw and gbias, parts > 1
     int64_t sx[2], sy[2], sgy[2], sgx[2];   // batch, channel strides (steps contiguous)
     int B, D, L, W, silu, nrun, nblk;
-    int parts, per_part;             // backward: items (batch row, run) of a channel per workgroup
+    int tiles;                       // backward: whole tiles of 64 runs a row, or 0: runs are taken on over rows' ends
+    int parts, per_part;             // of a channel: workgroups, and tiles or items (batch row, run) of each
 };
 hipError_t launch_conv_fwd(const ConvParams& p, int dtype, hipStream_t st);
 hipError_t launch_conv_bwd(const ConvParams& p, int dtype, hipStream_t st);

@@ -100,6 +100,26 @@ def test_conv_parts_and_determinism():
         assert all(torch.equal(g[k], h[k]) for k in g)
 
 
+@pytest.mark.parametrize("dtype,x8", [("f32", False), ("bf16", False), ("f32", True)])
+@pytest.mark.parametrize("B,D,L,W", [(2, 3, 1999, 2), (3, 4, 4095, 3), (2, 3, 10241, 4), (1, 2, 10243, 4), (4, 2, 8193, 2),
+                                     (7, 2, 510, 4), (3, 5, 2561, 4), (2, 3, 2562, 3)])
+def test_conv_backward_of_long_rows(B, D, L, W, dtype, x8):
+    """Rows of tiles of 512 steps: the last one whole, short by a little, or with one step or two."""
+    t, gy, glast = conv_inputs(B, D, L, W, dtype, True, L)
+    src, kept = {}, None
+    if x8:
+        k = ssm.ckpt8_pack(t["x"])
+        src = dict(ckpt8=(k["x8"], k["x8_scale"]))
+        kept = R.unpack(k["x8"].cpu().numpy(), k["x8_scale"].cpu().numpy()).astype(np.float64)
+    conv_check(t, gy, glast, L % 4 != 1, dtype, x64=kept, fwd=False, **src)
+
+
+def test_conv_parts_of_several_groups():
+    """Channels and steps enough that a workgroup takes two groups of several parts, across rows."""
+    t, gy, glast = conv_inputs(4, 1100, 4091, 4, "bf16", True, 11)
+    conv_check(t, gy, glast, True, "bf16", fwd=False)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_conv_segments(dtype):
     """A sequence in two segments is the whole one: last becomes init, ginit becomes glast, bit for bit in the streams."""
