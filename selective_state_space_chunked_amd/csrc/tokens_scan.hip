@@ -16,11 +16,11 @@
 // and the second pass walks every range from the state that enters it.
 //
 // The passes are bound by the issue of these instructions (an exp2 takes 8
-// cycles, the others 2 to 3): the main loops hold 273 (first pass) and 374 vector
+// cycles, the others 2 to 3): the main loops hold 265 (first pass) and 362 vector
 // instructions for four rows, 256 and 320 of them the state's own; loads by
 // scalar addresses and B, C by way of LDS leave the rest that small.  8192 rows x
-// 2048 channels x 16 states in bf16, 13 sequences: 57 us, 10 us between and 75 us
-// (17000 x 1024, one sequence: 58, 10 and 75), where the streams alone are 28 us of
+// 2048 channels x 16 states in bf16, 13 sequences: 53 us, 10 us between and 72 us
+// (17000 x 1024, one sequence: 55, 10 and 73), where the streams alone are 28 us of
 // memory traffic.  Of each pass about 10 us do not shrink with the rows.
 //
 // Single tokens.  Bound by the states' traffic: four states a lane, so a wave
@@ -28,31 +28,14 @@
 // 5.2 TB/s; one sequence of 2048 channels: 3.7 us, the latency of its loads.
 #include <algorithm>
 
+#include "buffer.hpp"
 #include "tokens.hpp"
 
 namespace ssm {
 namespace {
 
-// Buffer accesses: the row's address is scalar, a lane adds its byte offset in 32 bits, and offsets
-// from `bytes` on read as zero.  (Kept as flat pointers the compiler spends two vector registers and a
-// 64-bit vector addition on every access.)
-typedef __amdgpu_buffer_rsrc_t buffer_t;
-__device__ __forceinline__ buffer_t buffer_of(const void* row, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(row), 0, bytes, 0x00027000);
-}
-template <typename T> __device__ __forceinline__ T buffer_load(buffer_t r, uint32_t off, uint32_t row = 0);
-template <> __device__ __forceinline__ bf16_t buffer_load<bf16_t>(buffer_t r, uint32_t off, uint32_t row) {
-    return __builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
-}
-template <> __device__ __forceinline__ float buffer_load<float>(buffer_t r, uint32_t off, uint32_t row) {
-    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0));
-}
-__device__ __forceinline__ void buffer_store(buffer_t r, uint32_t off, bf16_t v) {
-    __builtin_amdgcn_raw_buffer_store_b16(v, r, off, 0, 0);
-}
-__device__ __forceinline__ void buffer_store(buffer_t r, uint32_t off, float v) {
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, off, 0, 0);
-}
+// The streams are read through buffers (kept as flat pointers the compiler spends two vector registers and a 64-bit
+// vector addition on every access).
 constexpr uint32_t kAll = 0xffffffffu;   // rows of a group: in bounds by their index, no limit wanted
 
 constexpr int kScanWaves = 4;   // of a workgroup: the same rows, neighbouring channels
@@ -136,21 +119,12 @@ struct ScanLane {
         int tl = t0;   // the row of pd, px, pz
         auto load = [&] {   // rows tl .. tl+3 (past the last row of all, the last one again)
             const buffer_t d_ = buffer_of(pd, kAll), x_ = buffer_of(px, kAll), z_ = buffer_of(pz, kAll);
-            if (tl + kGrp <= rows) {
 #pragma unroll
-                for (int g = 0; g < kGrp; ++g) {
-                    rd[g] = buffer_load<T>(d_, db, g * bd);
-                    rx[g] = buffer_load<T>(x_, db, g * bx);
-                    if (OUT) rz[g] = buffer_load<T>(z_, db, g * bz);
-                }
-            } else {
-#pragma unroll
-                for (int g = 0; g < kGrp; ++g) {
-                    const uint32_t r = max(min(g, rows - 1 - tl), 0);
-                    rd[g] = buffer_load<T>(d_, db, r * bd);
-                    rx[g] = buffer_load<T>(x_, db, r * bx);
-                    if (OUT) rz[g] = buffer_load<T>(z_, db, r * bz);
-                }
+            for (int g = 0; g < kGrp; ++g) {
+                const uint32_t r = max(min(g, rows - 1 - tl), 0);
+                rd[g] = buffer_load<T>(d_, db, r * bd);
+                rx[g] = buffer_load<T>(x_, db, r * bx);
+                if (OUT) rz[g] = buffer_load<T>(z_, db, r * bz);
             }
             const int64_t on = tl + kGrp < rows ? kGrp : 0;
             tl += (int)on;
@@ -178,14 +152,23 @@ struct ScanLane {
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
             __builtin_amdgcn_wave_barrier();
         };
+        // Waits are for the loads of a group or tile before, with the next one's under way: for that the compiler has
+        // to see the same loads on every way through the loops, and none pending from before them (57 + 75 us where it
+        // does not, 53 + 72 us where it does).
         load_bc(t0);
         load();
+#pragma unroll
+        for (int g = 0; g < kGrp; ++g) {
+            __asm__ volatile("" : "+v"(rd[g]), "+v"(rx[g]));
+            if (OUT) __asm__ volatile("" : "+v"(rz[g]));
+        }
         for (int tt = t0; tt < t1; tt += kTile) {
             stage();
-            if (tt + kTile < t1) load_bc(tt + kTile);
+            load_bc(min(tt + kTile, t1 - 1));   // (after the last tile: of no use)
             const int n = min(kTile, t1 - tt);
+            int i = 0;
 #pragma unroll 1
-            for (int i = 0; i < n; i += kGrp) {
+            do {
                 // rows from t1 on are identity steps: step size and input 0, B and C read as 0, y past the
                 // end of its buffer
                 float dl[kGrp], xv[kGrp], zv[kGrp];
@@ -211,7 +194,8 @@ struct ScanLane {
 #pragma unroll
                 for (int g = 0; g < kGrp; ++g) row<OUT>(i + g, yg, db + g * by, dl[g], xv[g], zv[g]);
                 py += kGrp * sy;
-            }
+                i += kGrp;
+            } while (i < n);
         }
     }
 };
