@@ -126,6 +126,7 @@ template <typename T> struct Vec;
 template <> struct Vec<float> {
     static constexpr int V = 4;
     f32x4 r;
+    __device__ __forceinline__ void arrived() { __asm__ volatile("" : "+v"(r)); }   // its load is waited for here
     __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const f32x4*>(p); }
     __device__ __forceinline__ void load(const float* p, int n) {   // the first n, the others 0
 #pragma unroll
@@ -149,6 +150,7 @@ template <> struct Vec<float> {
 template <> struct Vec<bf16_t> {
     static constexpr int V = 4;
     u32x2 r;
+    __device__ __forceinline__ void arrived() { __asm__ volatile("" : "+v"(r)); }
     __device__ __forceinline__ void load(const bf16_t* p) { r = *reinterpret_cast<const u32x2*>(p); }
     __device__ __forceinline__ void load(const bf16_t* p, int n) {
         r = u32x2(0);

@@ -5,7 +5,7 @@
 // A lane takes four neighbouring channels, so a wave reads and writes whole lines
 // of a row, and keeps the W-1 inputs before its rows in registers while it walks
 // down a run of them, four rows' loads under way at a time.  A few operations an
-// element: bound by HBM (8192 rows x 4096 channels in bf16: 134 MB in 33.6 us),
+// element: bound by HBM (8192 rows x 4096 channels in bf16: 134 MB in 32 us),
 // single tokens by the latency of their loads (64 x 2048: 3.1 us).
 #include <algorithm>
 
@@ -89,24 +89,25 @@ struct ConvLane {
     // rows [t0, t1): the next group's loads are under way while a group is computed
     __device__ __forceinline__ void walk(int t0, int t1) {
         Vec<T> r[kTokGrp];
+        if (t0 >= t1) return;
 #pragma unroll
-        for (int g = 0; g < kTokGrp; ++g)
-            if (t0 + g < t1) load_row(t0 + g, r[g]);
+        for (int g = 0; g < kTokGrp; ++g) load_row(min(t0 + g, t1 - 1), r[g]);
         walk(t0, t1, r);
     }
+    // (whole groups apart: with the same loads and stores in every turn a wait is for a group's loads alone)
     __device__ __forceinline__ void walk(int t0, int t1, Vec<T> (&r)[kTokGrp]) {   // r: the first group
-        Vec<T> nx[kTokGrp];
-        auto load = [&](int t, Vec<T>(&v)[kTokGrp]) {
 #pragma unroll
-            for (int g = 0; g < kTokGrp; ++g)
-                if (t + g < t1) load_row(t + g, v[g]);
-        };
-        for (int t = t0; t < t1; t += kTokGrp) {
-            if (t + kTokGrp < t1) load(t + kTokGrp, nx);
-            rows<kTokGrp>(t, r, t1 - t);
+        for (int g = 0; g < kTokGrp; ++g) r[g].arrived();
+        int t = t0;
+        for (; t + kTokGrp <= t1; t += kTokGrp) {
+            Vec<T> nx[kTokGrp];
+#pragma unroll
+            for (int g = 0; g < kTokGrp; ++g) load_row(min(t + kTokGrp + g, t1 - 1), nx[g]);
+            rows<kTokGrp>(t, r, kTokGrp);
 #pragma unroll
             for (int g = 0; g < kTokGrp; ++g) r[g] = nx[g];
         }
+        if (t < t1) rows<kTokGrp>(t, r, t1 - t);
     }
     // the slot's inputs, [channel][oldest first]
     __device__ __forceinline__ void load_state(int slot, Vec<T> (&h)[H]) const {
