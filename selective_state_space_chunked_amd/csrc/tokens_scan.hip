@@ -38,6 +38,7 @@ namespace {
 // vector addition on every access).
 constexpr uint32_t kAll = 0xffffffffu;   // rows of a group: in bounds by their index, no limit wanted
 
+typedef float f4 __attribute__((ext_vector_type(4)));
 constexpr int kScanWaves = 4;   // of a workgroup: the same rows, neighbouring channels
 constexpr int kTile = 16;   // rows of B and C in LDS
 constexpr int kGrp = 4;   // rows loaded together
@@ -46,6 +47,7 @@ constexpr int kGrp = 4;   // rows loaded together
 template <typename T, int N, bool FULL>
 struct ScanLane {
     static constexpr int NQ = N <= 4 ? 4 : N <= 8 ? 8 : 16;   // places of B, then of C, in a row of LDS
+    static constexpr int NV = (N + 3) / 4;
     static constexpr int kLds = kTile * 2 * NQ;               // floats of LDS a wave
     static constexpr int kStage = kTile * NQ / 64;            // loads of a lane for a tile of B, and of C
     const T *delta, *x, *z, *B, *C;
@@ -55,8 +57,9 @@ struct ScanLane {
     uint32_t row_bytes, db;   // of a row's channels; byte offset of the lane's
     int rows;
     uint32_t ob, oc;          // byte offset of the lane's element of B and of C in a tile
-    float *put, *lds;
-    float a[N], h[N], bias, skip, dsum;
+    float *put, *putc, *lds, *lds_b;
+    float a[N], bias, skip, dsum;
+    f4 h[NV];                 // the channel's states; those past N stay what they are and go nowhere
     int softplus;
     bool skips, gates;
 
@@ -74,7 +77,9 @@ struct ScanLane {
         ob = n < N ? (uint32_t)(r * (int)sB + n) * sizeof(T) : 0x7fffffffu;   // places past the states read as 0
         oc = n < N ? (uint32_t)(r * (int)sC + n) * sizeof(T) : 0x7fffffffu;
         lds = lds_;
-        put = lds_ + r * 2 * NQ + n;
+        put = lds_ + r * 2 * NQ + (n % 4) * (NQ / 4) + n / 4;
+        putc = lds_ + r * 2 * NQ + NQ + n;
+        lds_b = lds_ + (lane % 4) * (NQ / 4);
 #pragma unroll
         for (int n = 0; n < N; ++n) a[n] = p.A[(int64_t)d * N + n] * kLog2e;
         bias = p.stepf.bias ? p.stepf.bias[d] : 0.0f;
@@ -82,26 +87,39 @@ struct ScanLane {
         skips = p.skip != nullptr;
         softplus = p.stepf.softplus;
     }
+    __device__ __forceinline__ void set(const float (&v)[N]) {
+#pragma unroll
+        for (int n = 0; n < 4 * NV; ++n) h[n / 4][n % 4] = n < N ? v[n] : 0.0f;
+    }
+    __device__ __forceinline__ void get(float (&v)[N]) const {
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = h[n / 4][n % 4];
+    }
     template <bool OUT>
     __device__ __forceinline__ void row(int i, buffer_t yg, uint32_t yo, float dl, float xv, float zv) {
-        float b[NQ], c[NQ];
-        const float4* r = reinterpret_cast<const float4*>(lds + i * 2 * NQ);
-#pragma unroll
-        for (int q = 0; q < (N + 3) / 4; ++q) {
-            const float4 v = r[q];
-            b[4 * q] = v.x; b[4 * q + 1] = v.y; b[4 * q + 2] = v.z; b[4 * q + 3] = v.w;
-            if (OUT) {
-                const float4 w = r[NQ / 4 + q];
-                c[4 * q] = w.x; c[4 * q + 1] = w.y; c[4 * q + 2] = w.z; c[4 * q + 3] = w.w;
-            }
-        }
+        // Four states of the wave's 64 channels a matrix instruction: sixteen blocks of 4 x 4, h += b u with b the
+        // rows (lane l: state l % 4 of the four) and u the columns (lane l: its channel), four states a lane.
+        float b[NQ / 4];
+        __builtin_memcpy(b, __builtin_assume_aligned(lds_b + i * 2 * NQ, NQ >= 16 ? 16 : NQ), sizeof(b));
+        const f4* c = reinterpret_cast<const f4*>(lds + i * 2 * NQ + NQ);
         const float u = dl * xv;
         float o = 0.0f;
         if (!OUT) dsum += dl;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            h[n] = fmaf(__builtin_amdgcn_exp2f(a[n] * dl), h[n], u * b[n]);
-            if (OUT) o = fmaf(h[n], c[n], o);
+        for (int q = 0; q < NV; ++q) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (4 * q + e < N) h[q][e] *= __builtin_amdgcn_exp2f(a[4 * q + e] * dl);
+            h[q] = __builtin_amdgcn_mfma_f32_4x4x1f32(b[q], u, h[q], 0, 0, 0);
+        }
+        if (OUT) {
+#pragma unroll
+            for (int q = 0; q < NV; ++q) {
+                const f4 w = c[q];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * q + e < N) o = fmaf(h[q][e], w[e], o);
+            }
         }
         if (OUT) {
             if (FULL || skips) o = fmaf(skip, xv, o);
@@ -147,7 +165,7 @@ struct ScanLane {
 #pragma unroll
             for (int q = 0; q < kStage; ++q) {
                 put[q * (64 / NQ) * 2 * NQ] = to_f32(rb[q]);
-                if (OUT) put[q * (64 / NQ) * 2 * NQ + NQ] = to_f32(rc[q]);
+                if (OUT) putc[q * (64 / NQ) * 2 * NQ] = to_f32(rc[q]);
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
             __builtin_amdgcn_wave_barrier();
@@ -250,15 +268,16 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_sum
     __shared__ __align__(16) float lds[kScanWaves * ScanLane<T, N, FULL>::kLds];
     ScanLane<T, N, FULL> l(p, d, lds + (threadIdx.x >> 6) * ScanLane<T, N, FULL>::kLds);
     const int64_t at = (int64_t)c * N * p.D;
-#pragma unroll
-    for (int n = 0; n < N; ++n) l.h[n] = 0.0f;
+    float h[N] = {};
     l.dsum = 0.0f;
     if (st >= r.r0) {   // it begins here: its first state, kept for the second pass (which may find it overwritten)
-        if (!q.fresh(s)) load_states<N>(p.pool + slot * p.spool + (int64_t)d * N, l.h);
-        put_range<N>(p.h0 + at, p.D, d, l.h);
+        if (!q.fresh(s)) load_states<N>(p.pool + slot * p.spool + (int64_t)d * N, h);
+        put_range<N>(p.h0 + at, p.D, d, h);
     }
+    l.set(h);
     l.template walk<false>(max(st, r.r0), r.r1);
-    put_range<N>(p.hsum + at, p.D, d, l.h);
+    l.get(h);
+    put_range<N>(p.hsum + at, p.D, d, h);
     p.dsum[(int64_t)c * p.D + d] = l.dsum;
 }
 
@@ -348,10 +367,9 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_ker
         const int slot = q.slot(s);
         if (slot < 0) continue;
         float* pool = p.pool + slot * p.spool + (int64_t)d * N;
-#pragma unroll
-        for (int n = 0; n < N; ++n) l.h[n] = 0.0f;
+        float h[N] = {};
         if (st < r.r0) {   // from the ranges before: the state that crosses into this one
-            get_range<N>(p.hsum + (int64_t)(p.joined ? c - 1 : st / p.rows) * N * p.D, p.D, d, l.h);
+            get_range<N>(p.hsum + (int64_t)(p.joined ? c - 1 : st / p.rows) * N * p.D, p.D, d, h);
             if (!p.joined) {
 #pragma unroll 1
                 for (int k = st / p.rows + 1; k < c; ++k) {
@@ -359,18 +377,20 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_ker
                     get_range<N>(p.hsum + (int64_t)k * N * p.D, p.D, d, S);
                     const float ds = p.dsum[(int64_t)k * p.D + d];
 #pragma unroll
-                    for (int n = 0; n < N; ++n) l.h[n] = fmaf(__builtin_amdgcn_exp2f(l.a[n] * ds), l.h[n], S[n]);
+                    for (int n = 0; n < N; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(l.a[n] * ds), h[n], S[n]);
                 }
             }
         } else if (en > r.r1) {
-            get_range<N>(p.h0 + (int64_t)c * N * p.D, p.D, d, l.h);
+            get_range<N>(p.h0 + (int64_t)c * N * p.D, p.D, d, h);
         } else if (!q.fresh(s)) {
-            load_states<N>(pool, l.h);
+            load_states<N>(pool, h);
         }
+        l.set(h);
         l.template walk<true>(max(st, r.r0), min(en, r.r1));
         if (en <= r.r1) {
+            l.get(h);
 #pragma unroll
-            for (int n = 0; n < N; ++n) pool[n] = l.h[n];
+            for (int n = 0; n < N; ++n) pool[n] = h[n];
         }
     }
 }
