@@ -7,8 +7,8 @@
 // the projections write them.  B_t, C_t are the same for the whole wave: 16 rows
 // of them at a time go to LDS as fp32 and come back as broadcast 16-byte reads.
 // Per state and row that leaves a multiply and an exp2 for the transition, a
-// multiply and a multiply-add for the state and one multiply-add for y.  Few
-// long sequences do not fill the GPU, so the rows are cut into ranges whatever
+// multiply for the state, a quarter of a matrix instruction for the input term
+// and one multiply-add for y.  Few long sequences do not fill the GPU, so the rows are cut into ranges whatever
 // the sequences' lengths: a first pass leaves, for the sequence that crosses the
 // end of each range, its state there (from zero where it runs through the whole
 // range) and the sum of its step sizes; a small kernel composes them,
@@ -16,11 +16,11 @@
 // and the second pass walks every range from the state that enters it.
 //
 // The passes are bound by the issue of these instructions (an exp2 takes 8
-// cycles, the others 2 to 3): the main loops hold 265 (first pass) and 362 vector
-// instructions for four rows, 256 and 320 of them the state's own; loads by
+// cycles, the others 2 to 3): the main loops hold 217 (first pass) and 314 vector
+// instructions for four rows, 208 and 272 of them the state's own; loads by
 // scalar addresses and B, C by way of LDS leave the rest that small.  8192 rows x
-// 2048 channels x 16 states in bf16, 13 sequences: 53 us, 10 us between and 72 us
-// (17000 x 1024, one sequence: 55, 10 and 73), where the streams alone are 28 us of
+// 2048 channels x 16 states in bf16, 13 sequences: 50 us, 10 us between and 65 us
+// (17000 x 1024, one sequence: 52, 10 and 64), where the streams alone are 28 us of
 // memory traffic.  Of each pass about 10 us do not shrink with the rows.
 //
 // Single tokens.  Bound by the states' traffic: four states a lane, so a wave
@@ -55,7 +55,7 @@ struct ScanLane {
     int64_t sdelta, sx, sz, sy, sB, sC;
     uint32_t bd, bx, bz, by;  // bytes from one row to the next
     uint32_t row_bytes, db;   // of a row's channels; byte offset of the lane's
-    int rows;
+    int rows, r0, span;
     uint32_t ob, oc;          // byte offset of the lane's element of B and of C in a tile
     float *put, *putc, *lds, *lds_b;
     float a[N], bias, skip, dsum;
@@ -63,7 +63,10 @@ struct ScanLane {
     int softplus;
     bool skips, gates;
 
-    __device__ __forceinline__ ScanLane(const TokScanParams& p, int d, float* lds_) {
+    // lane of channel d, in the range of rows [r0_, r1_)
+    __device__ __forceinline__ ScanLane(const TokScanParams& p, int d, int r0_, int r1_, float* lds_) {
+        r0 = r0_;
+        span = r1_ - r0_;
         delta = (const T*)p.delta; x = (const T*)p.x; y = (T*)p.y; B = (const T*)p.Bm; C = (const T*)p.C;
         gates = p.z != nullptr;
         z = gates ? (const T*)p.z : x;   // without a gate: read and not used
@@ -127,6 +130,16 @@ struct ScanLane {
             buffer_store(yg, yo, to_stream<T>(o));
         }
     }
+    // A SIMD issues from its oldest wave first, so of four waves with the same work one would be done when another has
+    // half of it left, alone and too few to fill the SIMD.  A wave behind the others goes first (8192 x 2048: 54 + 70 us
+    // without, 50 + 65 us with it).
+    __device__ __forceinline__ void yield(int t) const {
+        const int64_t done = 4 * (int64_t)(t - r0);
+        if (done < span) __builtin_amdgcn_s_setprio(3);
+        else if (done < 2 * (int64_t)span) __builtin_amdgcn_s_setprio(2);
+        else if (done < 3 * (int64_t)span) __builtin_amdgcn_s_setprio(1);
+        else __builtin_amdgcn_s_setprio(0);
+    }
     // rows [t0, t1), t0 < t1: the next group's streams and the next tile's B and C are under way
     // while a group is computed
     template <bool OUT>
@@ -172,7 +185,7 @@ struct ScanLane {
         };
         // Waits are for the loads of a group or tile before, with the next one's under way: for that the compiler has
         // to see the same loads on every way through the loops, and none pending from before them (57 + 75 us where it
-        // does not, 53 + 72 us where it does).
+        // did not, 53 + 72 us where it did).
         load_bc(t0);
         load();
 #pragma unroll
@@ -181,6 +194,7 @@ struct ScanLane {
             if (OUT) __asm__ volatile("" : "+v"(rz[g]));
         }
         for (int tt = t0; tt < t1; tt += kTile) {
+            yield(tt);
             stage();
             load_bc(min(tt + kTile, t1 - 1));   // (after the last tile: of no use)
             const int n = min(kTile, t1 - tt);
@@ -266,7 +280,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_sum
     // lanes past the last channel repeat it: the same values to the same places, without a branch a row
     const int d = min(cb * 64 + lane_id(), p.D - 1);
     __shared__ __align__(16) float lds[kScanWaves * ScanLane<T, N, FULL>::kLds];
-    ScanLane<T, N, FULL> l(p, d, lds + (threadIdx.x >> 6) * ScanLane<T, N, FULL>::kLds);
+    ScanLane<T, N, FULL> l(p, d, r.r0, r.r1, lds + (threadIdx.x >> 6) * ScanLane<T, N, FULL>::kLds);
     const int64_t at = (int64_t)c * N * p.D;
     float h[N] = {};
     l.dsum = 0.0f;
@@ -357,7 +371,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 16 / kScanWaves) void tok_scan_ker
     if (s >= p.q.S) return;
     const int d = min(cb * 64 + lane_id(), p.D - 1);
     __shared__ __align__(16) float lds[kScanWaves * ScanLane<T, N, FULL>::kLds];
-    ScanLane<T, N, FULL> l(p, d, lds + (threadIdx.x >> 6) * ScanLane<T, N, FULL>::kLds);
+    ScanLane<T, N, FULL> l(p, d, r.r0, r.r1, lds + (threadIdx.x >> 6) * ScanLane<T, N, FULL>::kLds);
     if (s < 0) s = 0;
     for (; s < p.q.S; ++s) {
         const int st = q.first(s);
