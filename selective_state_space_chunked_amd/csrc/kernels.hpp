@@ -333,8 +333,8 @@ constexpr int kTokRowsMin = 16;
 // with ranges of at least 32 rows).
 constexpr int kTokChain = 24;
 // The waves the ranges are made for: the second pass's registers allow four on each of the 1024 SIMDs, so one
-// round of 4096.  Measured when this was set, at 8192 rows x 2048 channels (both passes and the states between,
-// us): 1024 waves 226, 2048 161, 4096 149, 6144 154.
+// round of 4096.  Measured at 8192 rows x 2048 channels (both passes and the states between): 4096 waves 124 us,
+// 8192 waves 141 us, 5120 waves with registers for five on a SIMD 138 us.
 constexpr int kTokWaves = 4096;
 hipError_t launch_tok_conv(const TokConvParams& p, int dtype, hipStream_t st);
 hipError_t launch_tok_scan(const TokScanParams& p, int dtype, bool sum, hipStream_t st);
