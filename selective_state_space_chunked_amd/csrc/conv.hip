@@ -47,7 +47,7 @@ __device__ __forceinline__ void store_stream(float* p, const float (&v)[kConvRun
     if (n >= kConvRun) {
         *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
         *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
+    } else if (n > 0) {
 #pragma unroll
         for (int j = 0; j < kConvRun; ++j)
             if (j < n) p[j] = v[j];
@@ -61,7 +61,7 @@ __device__ __forceinline__ void store_stream(bf16_t* p, const float (&v)[kConvRu
                ((uint32_t)__builtin_bit_cast(bf16_t, (__bf16)v[2 * j + 1]) << 16);
     if (n >= kConvRun) {
         *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
-    } else {
+    } else if (n > 0) {
 #pragma unroll
         for (int j = 0; j < kConvRun; ++j)
             if (j < n) p[j] = (bf16_t)(w[j / 2] >> (16 * (j & 1)));
@@ -138,11 +138,16 @@ template <> struct Run<bf16_t> {
     u32x4 r;
     __device__ __forceinline__ void load(const bf16_t* p) { r = *reinterpret_cast<const u32x4*>(p); }
     __device__ __forceinline__ void load(const bf16_t* p, int n) {   // the first n
-        uint32_t w[4] = {};
+        r = u32x4(0);
+        if (n >= kConvRun) {
+            load(p);
+        } else if (n > 0) {
+            uint32_t w[4] = {};
 #pragma unroll
-        for (int j = 0; j < kConvRun; ++j)
-            if (j < n) w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
-        r = u32x4{w[0], w[1], w[2], w[3]};
+            for (int j = 0; j < kConvRun; ++j)
+                if (j < n) w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+            r = u32x4{w[0], w[1], w[2], w[3]};
+        }
     }
     __device__ __forceinline__ void get(float (&v)[kConvRun]) const {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -160,11 +165,16 @@ template <> struct Run<float> {
         r[1] = *reinterpret_cast<const f32x4*>(p + 4);
     }
     __device__ __forceinline__ void load(const float* p, int n) {
-        float v[kConvRun];
+        r[0] = r[1] = f32x4(0.0f);
+        if (n >= kConvRun) {
+            load(p);
+        } else if (n > 0) {
+            float v[kConvRun];
 #pragma unroll
-        for (int j = 0; j < kConvRun; ++j) v[j] = j < n ? p[j] : 0.0f;
-        r[0] = f32x4{v[0], v[1], v[2], v[3]};
-        r[1] = f32x4{v[4], v[5], v[6], v[7]};
+            for (int j = 0; j < kConvRun; ++j) v[j] = j < n ? p[j] : 0.0f;
+            r[0] = f32x4{v[0], v[1], v[2], v[3]};
+            r[1] = f32x4{v[4], v[5], v[6], v[7]};
+        }
     }
     __device__ __forceinline__ void get(float (&v)[kConvRun]) const {
         v[0] = r[0].x; v[1] = r[0].y; v[2] = r[0].z; v[3] = r[0].w;
@@ -179,12 +189,18 @@ struct Run8 {
         s = *sc;
     }
     __device__ __forceinline__ void load(const int8_t* p, const float* sc, int n) {
-        uint32_t w[2] = {};
-        s = n > 0 ? *sc : 0.0f;
+        r = u32x2(0);
+        s = 0.0f;
+        if (n >= kConvRun) {
+            load(p, sc);
+        } else if (n > 0) {
+            uint32_t w[2] = {};
+            s = *sc;
 #pragma unroll
-        for (int j = 0; j < kConvRun; ++j)
-            if (j < n) w[j / 4] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
-        r = u32x2{w[0], w[1]};
+            for (int j = 0; j < kConvRun; ++j)
+                if (j < n) w[j / 4] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
+            r = u32x2{w[0], w[1]};
+        }
     }
     // q s as (q + 128) s - 128 s: the sum of unsigned bytes is one conversion, and the multiply-add rounds the
     // exact q s once
@@ -378,6 +394,33 @@ struct BwdAt {
     }
 };
 
+// gw and gbias of a run's steps
+template <int W>
+__device__ __forceinline__ void add_steps(float (&acc)[W + 1], const float* gp, const float* e) {
+#pragma unroll
+    for (int j = 0; j < kConvRun; ++j) {
+#pragma unroll
+        for (int q = 0; q < W; ++q) acc[q] = fmaf(gp[j], e[j + q], acc[q]);
+        acc[W] += gp[j];
+    }
+}
+// of the steps from `from` on and before `to`
+template <int W>
+__device__ __forceinline__ void add_steps(float (&acc)[W + 1], const float* gp, const float* e, int from, int to) {
+    if (from <= 0 && to >= kConvRun) {
+        add_steps<W>(acc, gp, e);
+    } else if (from < kConvRun && to > 0) {
+#pragma unroll
+        for (int j = 0; j < kConvRun; ++j) {
+            if (j >= from && j < to) {
+#pragma unroll
+                for (int q = 0; q < W; ++q) acc[q] = fmaf(gp[j], e[j + q], acc[q]);
+                acc[W] += gp[j];
+            }
+        }
+    }
+}
+
 // workgroup barrier that waits for LDS accesses only: loads and stores of global memory stay under way
 __device__ __forceinline__ void lds_barrier() { __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
@@ -408,9 +451,9 @@ __device__ __forceinline__ void bwd_sums(const ConvParams& p, int d, int part, c
 // gradients after it come from the lanes beside it, between waves through LDS.
 // The items are taken 256 at a time from the last to the first, so the gradients
 // after a group are those of the group before; the next group's loads are under
-// way while one is computed.  For short rows (no whole tile of 512 steps, or a fifth
-// of the lanes idle in the kernel below): B=2 D=195 L=517 f32 5.4 us, of which a
-// launch is 3.
+// way while one is computed.  For short rows (no whole tile of 512 steps, or over a
+// third of the lanes idle in the kernel below): B=2 D=195 L=517 f32 5.4 us, of
+// which a launch is 3.
 template <typename T, int W, bool X8>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
     constexpr int H = W - 1, R = kConvRun;
@@ -492,21 +535,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
             for (int i = 0; i < H; ++i) gp[R + i] = R + i < n ? gp[R + i] : 0.0f;
         }
         if (c.full) {
-#pragma unroll
-            for (int j = 0; j < R; ++j) {
-#pragma unroll
-                for (int q = 0; q < W; ++q) acc[q] = fmaf(gp[j], e[j + q], acc[q]);
-                acc[W] += gp[j];
-            }
+            add_steps<W>(acc, gp, e);
         } else {
-#pragma unroll
-            for (int j = 0; j < R; ++j) {
-                if (j < n) {   // steps past the end add nothing, whatever lies there
-#pragma unroll
-                    for (int q = 0; q < W; ++q) acc[q] = fmaf(gp[j], e[j + q], acc[q]);
-                    acc[W] += gp[j];
-                }
-            }
+            add_steps<W>(acc, gp, e, 0, n);   // steps past the end add nothing, whatever lies there
         }
         const int64_t row = (int64_t)c.b * p.D + d;
         const T* gl = p.glast ? (const T*)p.glast + row * H : nullptr;
@@ -545,10 +576,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
 
 // Backward of rows of some length.  As above, but a wave takes tiles of 64 runs of one row each and forms the gradients
 // after a tile again (one lane a step, from the inputs and gradients there), so waves wait for nothing of each other;
-// a tile's row and place are scalar, and a lane's addresses are its fixed offset from them.  Whole tiles and rows'
-// ends are taken apart: the loop over whole tiles issues the same loads and stores in every turn, so the wait for a
-// tile's loads is one for these alone, with the next tile's loads and the last one's stores under way (with a branch
-// around either the compiler has to wait for everything).  Bound by HBM, with half of the time in its 32 vector
+// a tile's row and place are scalar, and a lane's addresses are its fixed offset from them.  The loop issues the same
+// loads and stores in every turn, so the wait for a tile's loads is one for these alone, with the next tile's loads
+// and the last one's stores under way (with a branch around either the compiler has to wait for everything).  Bound by HBM, with half of the time in its 32 vector
 // instructions a step.  B=8 D=2048 L=4096 bf16: 77 us, from 8 bits 82 us; the kernel above takes 92 and 99.
 template <typename T, int W, bool X8>
 struct RowTile {
@@ -559,23 +589,23 @@ struct RowTile {
     int8_t exq;   // the same of a checkpoint
     float exs;
     T eg;         // lane 32 + i, i < H: gy i steps from the tile's end
-    // a whole tile
-    __device__ __forceinline__ void load(const ConvParams& p, int b, int d, int seg) {
-        const int lane = lane_id(), first = seg * N, at = lane * R;
+    // a whole tile from step `first` on
+    __device__ __forceinline__ void load(const ConvParams& p, int b, int d, int first) {
+        const int at = lane_id() * R;
         const T* gy = (const T*)p.gy + b * p.sgy[0] + d * p.sgy[1] + first;
         const Row<T, X8> in = row_of<T, X8>(p, b, d);
         g.load(gy + at);
-        if (X8) q.load(in.q + first + at, in.s + first / kCkptBlock + at / kCkptBlock);
+        if (X8) q.load(in.q + first + at, in.s + (first + at) / kCkptBlock);
         else x.load(in.x + first + at);
         edges(p, in, gy, first);
     }
-    // the first `left` steps of a row's last one
-    __device__ __forceinline__ void load(const ConvParams& p, int b, int d, int seg, int left) {
-        const int lane = lane_id(), first = seg * N, at = lane * R;
+    // a tile of the row's last `left` steps
+    __device__ __forceinline__ void load(const ConvParams& p, int b, int d, int first, int left) {
+        const int at = lane_id() * R;
         const T* gy = (const T*)p.gy + b * p.sgy[0] + d * p.sgy[1] + first;
         const Row<T, X8> in = row_of<T, X8>(p, b, d);
         g.load(gy + at, left - at);
-        if (X8) q.load(in.q + first + at, in.s + first / kCkptBlock + at / kCkptBlock, left - at);
+        if (X8) q.load(in.q + first + at, in.s + (first + at) / kCkptBlock, left - at);
         else x.load(in.x + first + at, left - at);
         edges(p, in, gy, first);
     }
@@ -588,7 +618,7 @@ struct RowTile {
             const int s0 = max(first / kCkptBlock - 1, 0);
             exq = buffer_load<int8_t>(buffer_of(in.q + lo, (uint32_t)some), at);
             exs = buffer_load<float>(buffer_of(in.s + s0, (uint32_t)min(p.nblk - s0, 16) * 4),
-                                     has ? (uint32_t)(first / kCkptBlock + (t >> 6) - s0) * 4 : 0x7fffffffu);
+                                     has ? (uint32_t)(((first + t) >> 6) - s0) * 4 : 0x7fffffffu);
         } else {
             ex = buffer_load<T>(buffer_of(in.x + lo, (uint32_t)some * sizeof(T)), at * sizeof(T));
         }
@@ -599,16 +629,16 @@ struct RowTile {
     __device__ __forceinline__ float edge() const { return X8 ? (float)exq * exs : to_f32(ex); }
 };
 template <typename T, int W, bool X8, bool GX, bool FULL>
-__device__ __forceinline__ void bwd_tile(const ConvParams& p, const RowTile<T, W, X8>& c, int b, int d, int seg,
+__device__ __forceinline__ void bwd_tile(const ConvParams& p, const RowTile<T, W, X8>& c, int b, int d, int first, int cut,
                                          const float (&w)[W], float bias, float (&acc)[W + 1]) {
     constexpr int H = W - 1, R = kConvRun, N = 64 * R;
-    const int lane = lane_id(), left = p.L - seg * N, n = left - lane * R;   // steps from the tile's, the lane's first one on
+    const int lane = lane_id(), left = p.L - first, n = left - lane * R;   // steps from the tile's, the lane's first one on
     float v[R], e[R + H], gp[R + H], gr[R], ex = c.edge();
     if (X8) c.q.get(v);
     else c.x.get(v);
     c.g.get(gr);
-    if (p.init && seg == 0) {
-        if (lane < H) ex = to_f32(((const T*)p.init)[((int64_t)b * p.D + d) * H + lane]);
+    if (p.init && first < H) {
+        if (lane < H - first) ex = to_f32(((const T*)p.init)[((int64_t)b * p.D + d) * H + first + lane]);
         __asm__ volatile("" : "+v"(ex));   // waited for here, not where every tile passes
     }
 #pragma unroll
@@ -636,14 +666,8 @@ __device__ __forceinline__ void bwd_tile(const ConvParams& p, const RowTile<T, W
         const float edge = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ga), 32 + i));
         gp[R + i] = from_right(gp[i], left > N + i ? edge : 0.0f);   // none after the row's last step
     }
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-        if (FULL || j < n) {   // steps past the end add nothing, whatever lies there
-#pragma unroll
-            for (int q = 0; q < W; ++q) acc[q] = fmaf(gp[j], e[j + q], acc[q]);
-            acc[W] += gp[j];
-        }
-    }
+    if (FULL && cut == first) add_steps<W>(acc, gp, e);
+    else add_steps<W>(acc, gp, e, cut - first - lane * R, n);   // each step once, and none past the end
     const T* gl = p.glast ? (const T*)p.glast + ((int64_t)b * p.D + d) * H : nullptr;
     if (GX) {
         float o[R];
@@ -659,10 +683,10 @@ __device__ __forceinline__ void bwd_tile(const ConvParams& p, const RowTile<T, W
             for (int j = 0; j < R; ++j)
                 if (j < n && j + H >= n) o[j] += to_f32(gl[j + H - n]);
         }
-        T* gx = (T*)p.gx + b * p.sgx[0] + d * p.sgx[1] + seg * N;
+        T* gx = (T*)p.gx + b * p.sgx[0] + d * p.sgx[1] + first;
         store_stream(gx + lane * R, o, FULL ? R : n);
     }
-    if (p.ginit && seg == 0 && lane == 0) {
+    if (p.ginit && first == 0 && lane == 0) {
         T* gi = (T*)p.ginit + ((int64_t)b * p.D + d) * H;
 #pragma unroll
         for (int j = 0; j < H; ++j) {
@@ -683,37 +707,43 @@ __global__ __launch_bounds__(256) void conv_bwd_rows_kernel(ConvParams p) {
     for (int k = 0; k < W; ++k) w[k] = p.w[(int64_t)d * W + k];
     const float bias = p.bias ? p.bias[d] : 0.0f;
     float acc[W + 1] = {};
-    const int t0 = part * p.per_part + wave, t1 = min((part + 1) * p.per_part, p.B * p.tiles);   // whole tiles t0, t0 + 4, ..
+    // A row's end is a whole tile too, of its last N steps: those that the tile before has are formed again, to the same
+    // values, and not added again.  (The runs of a checkpoint keep to its blocks.)
+    const int rest = p.L - p.tiles * N;
+    const bool whole = rest > 0 && (!X8 || p.L % kConvRun == 0);
+    const int each = p.tiles + (whole ? 1 : 0);
+    const int t0 = part * p.per_part + wave, t1 = min((part + 1) * p.per_part, p.B * each);   // tiles t0, t0 + 4, ..
     if (t0 < t1) {
         RowTile<T, W, X8> c, nx;
-        int t = t0, b = t0 / p.tiles, seg = t0 - b * p.tiles, nb = b, ns = seg;
+        int t = t0, b = t0 / each, seg = t0 - b * each, nb = b, ns = seg;
         auto next = [&] {   // the place of the wave's next tile; after the last one, that one's again
             if (t + 4 >= t1) return;
             ns += 4;
-            while (ns >= p.tiles) {
-                ns -= p.tiles;
+            while (ns >= each) {
+                ns -= each;
                 ++nb;
             }
         };
-        c.load(p, b, d, seg);
+        auto first = [&](int s) { return s < p.tiles ? s * N : p.L - N; };
+        c.load(p, b, d, first(seg));
         for (;;) {
             next();
-            nx.load(p, nb, d, ns);
-            bwd_tile<T, W, X8, GX, true>(p, c, b, d, seg, w, bias, acc);
+            nx.load(p, nb, d, first(ns));
+            bwd_tile<T, W, X8, GX, true>(p, c, b, d, first(seg), seg * N, w, bias, acc);
             b = nb; seg = ns; t += 4;
             if (t >= t1) break;
             next();
-            c.load(p, nb, d, ns);
-            bwd_tile<T, W, X8, GX, true>(p, nx, b, d, seg, w, bias, acc);
+            c.load(p, nb, d, first(ns));
+            bwd_tile<T, W, X8, GX, true>(p, nx, b, d, first(seg), seg * N, w, bias, acc);
             b = nb; seg = ns; t += 4;
             if (t >= t1) break;
         }
     }
-    if (p.L > p.tiles * N) {   // the rows' ends
+    if (rest > 0 && !whole) {
         for (int b = part + p.parts * wave; b < p.B; b += p.parts * 4) {
             RowTile<T, W, X8> c;
-            c.load(p, b, d, p.tiles, p.L - p.tiles * N);
-            bwd_tile<T, W, X8, GX, false>(p, c, b, d, p.tiles, w, bias, acc);
+            c.load(p, b, d, p.tiles * N, rest);
+            bwd_tile<T, W, X8, GX, false>(p, c, b, d, p.tiles * N, p.tiles * N, w, bias, acc);
         }
     }
     bwd_sums<W>(p, d, part, acc);

@@ -332,8 +332,8 @@ constexpr int kTokRowsMin = 16;
 // its own costs more for so few (333 rows x 200 channels, N = 7, a pass: 19.4 us with it, 16.2 us without; 25 us
 // with ranges of at least 32 rows).
 constexpr int kTokChain = 24;
-// The waves the ranges are made for: the second pass's registers allow four on each of the 1024 SIMDs, so one
-// round of 4096.  Measured at 8192 rows x 2048 channels (both passes and the states between): 4096 waves 124 us,
+// The waves the ranges are made for: the second pass's registers allow four on each of the 1024 SIMDs, 4096 at
+// once.  Measured at 8192 rows x 2048 channels (both passes and the states between): 4096 waves 124 us,
 // 8192 waves 141 us, 5120 waves with registers for five on a SIMD 138 us.
 constexpr int kTokWaves = 4096;
 hipError_t launch_tok_conv(const TokConvParams& p, int dtype, hipStream_t st);

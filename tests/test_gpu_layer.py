@@ -102,7 +102,8 @@ def test_conv_parts_and_determinism():
 
 @pytest.mark.parametrize("dtype,x8", [("f32", False), ("bf16", False), ("f32", True)])
 @pytest.mark.parametrize("B,D,L,W", [(2, 3, 1999, 2), (3, 4, 4095, 3), (2, 3, 10241, 4), (1, 2, 10243, 4), (4, 2, 8193, 2),
-                                     (7, 2, 510, 4), (3, 5, 2561, 4), (2, 3, 2562, 3)])
+                                     (7, 2, 510, 4), (3, 5, 2561, 4), (2, 3, 2562, 3),
+                                     (3, 2, 513, 4), (2, 2, 514, 3), (2, 3, 2600, 4), (1, 4, 1000, 3)])
 def test_conv_backward_of_long_rows(B, D, L, W, dtype, x8):
     """Rows of tiles of 512 steps: the last one whole, short by a little, or with one step or two."""
     t, gy, glast = conv_inputs(B, D, L, W, dtype, True, L)
