@@ -13,8 +13,8 @@
 // read + written):
 //   B=8 D=2048 L=4096 W=4 bf16   forward                65 us   4.1 TB/s
 //                                forward + checkpoint   83 us   4.1 TB/s
-//                                backward               77 us   5.2 TB/s
-//                                backward from 8 bits   82 us   4.1 TB/s
+//                                backward               79 us   5.1 TB/s
+//                                backward from 8 bits   85 us   4.0 TB/s
 //                                checkpoint to bf16     34 us   6.0 TB/s
 //   B=1 D=1024 L=128000 f32      checkpoint            144 us   4.6 TB/s
 //                                checkpoint to f32     126 us   5.3 TB/s
@@ -579,7 +579,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
 // a tile's row and place are scalar, and a lane's addresses are its fixed offset from them.  The loop issues the same
 // loads and stores in every turn, so the wait for a tile's loads is one for these alone, with the next tile's loads
 // and the last one's stores under way (with a branch around either the compiler has to wait for everything).  Bound by HBM, with half of the time in its 32 vector
-// instructions a step.  B=8 D=2048 L=4096 bf16: 77 us, from 8 bits 82 us; the kernel above takes 92 and 99.
+// instructions a step.  B=8 D=2048 L=4096 bf16: 79 us, from 8 bits 85 us; the kernel above takes 92 and 99.
 template <typename T, int W, bool X8>
 struct RowTile {
     static constexpr int H = W - 1, R = kConvRun, N = 64 * R;   // steps of a tile
