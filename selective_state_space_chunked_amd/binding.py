@@ -1021,6 +1021,8 @@ def _sequences(T, pool, inner, pool_dtype, dev, seq_start, slot, fresh):
     sl = _dense(slot, "slot", torch.int32, (S,), dev)
     fr = 0
     if fresh is not None:
+        if not isinstance(fresh, torch.Tensor):
+            raise ValueError("fresh must be a torch.Tensor")
         if fresh.dtype not in (torch.bool, torch.uint8):
             raise TypeError(f"fresh has dtype {fresh.dtype}, expected torch.bool or torch.uint8")
         fr = _dense(fresh, "fresh", fresh.dtype, (S,), dev)

@@ -181,7 +181,8 @@ def test_binding_refuses():
     good = dict(x=r, w=w, pool=pool, seq_start=_t(3, **i32), slot=_t(2, **i32))
     for over, exc in ((dict(pool=_t(4, 3, 2)), ValueError), (dict(pool=pool.bfloat16()), TypeError),
                       (dict(seq_start=_t(3)), TypeError), (dict(slot=_t(3, **i32)), ValueError),
-                      (dict(fresh=_t(2)), TypeError), (dict(x=_t(2, 6, 3)), ValueError),
+                      (dict(fresh=_t(2)), TypeError), (dict(fresh=[True, False]), ValueError),
+                      (dict(x=_t(2, 6, 3)), ValueError),
                       (dict(pool=_t(4, 3, 6)[..., ::2]), ValueError), (dict(seq_start=_t(0, **i32)), ValueError),
                       (dict(), ValueError)):       # the last: host tensors
         with pytest.raises(exc):
