@@ -202,13 +202,15 @@ struct Run8 {
             r = u32x2{w[0], w[1]};
         }
     }
-    // q s as (q + 128) s - 128 s: the sum of unsigned bytes is one conversion, and the multiply-add rounds the
-    // exact q s once
+    // q s as 2 ((q + 128) h - 128 h) with h = s / 2: the sum of unsigned bytes is one conversion, and the multiply-add
+    // rounds the exact q h once.  128 s would overflow for blocks that reach to within 1/128 of the largest
+    // float, 128 h does not; halving and doubling are exact.  B=8 D=2048 L=4096, backward to bf16:
+    // 86.6 us, by signed bytes and one product (more instructions) 92.1.
     __device__ __forceinline__ void get(float (&v)[kConvRun]) const {
         const uint32_t w[2] = {r.x ^ 0x80808080u, r.y ^ 0x80808080u};
-        const float off = -128.0f * s;
+        const float h = 0.5f * s, off = -128.0f * h;
 #pragma unroll
-        for (int j = 0; j < kConvRun; ++j) v[j] = fmaf((float)((w[j / 4] >> (8 * (j & 3))) & 255u), s, off);
+        for (int j = 0; j < kConvRun; ++j) v[j] = 2.0f * fmaf((float)((w[j / 4] >> (8 * (j & 3))) & 255u), h, off);
     }
 };
 

@@ -769,3 +769,36 @@ def test_native_calls_refuse_as_the_binding():
                                               out={"y": rows}), ssm.binding.SSMError)):            # y over x
         with pytest.raises(exc):
             f(**kw)
+
+
+# ---------------------------------------------------------------------------
+# ends of the ranges
+# ---------------------------------------------------------------------------
+def largest_inputs(B, D, L, dtype, top, seed):
+    """A stream of every size up to `top`, some elements +-top and some 0; weights and gradients that keep sums finite."""
+    r = gen(seed)
+    x = r.uniform(-1, 1, (B, D, L)) * top
+    x[..., ::9] = top
+    x[..., 5::9] = -top
+    x[..., 3::7] = 0.0
+    w = r.uniform(0.5, 1, (D, 4)) * r.choice([-1, 1], (D, 4)) * 2.0 ** -124     # four taps: |p| below 70
+    t = dict(x=dev(x, dtype), w=dev(w), bias=dev(r.normal(size=D)), init=None)
+    return t, dev(r.normal(size=(B, D, L)) * 2.0 ** -12, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,D,L", [(2, 3, 131), (1, 5, 1099), (2, 5, 1104), (1, 3, 513)])
+def test_ckpt8_of_the_largest_values(B, D, L, dtype):
+    """Blocks up to the largest value whose 127 scales are finite: the bytes times their scale, rounded once, in every
+    reader of a checkpoint (runs, rows' ends, whole tiles and what lies beside them)."""
+    top = float(torch.finfo(torch.bfloat16).max) if dtype == "bf16" else (2 - 2.0 ** -22) * 2.0 ** 127
+    t, gy = largest_inputs(B, D, L, dtype, top, L)
+    f = ssm.conv_fwd(x=t["x"], w=t["w"], bias=t["bias"], silu=True, want_ckpt8=True)
+    q, s = R.pack(t["x"].float().cpu().numpy())
+    assert np.array_equal(f["x8"].cpu().numpy(), q) and np.array_equal(f["x8_scale"].cpu().numpy(), s)
+    kept = R.unpack(q, s)
+    assert np.isfinite(kept).all()
+    c8 = (f["x8"], f["x8_scale"])
+    assert np.array_equal(ssm.ckpt8_unpack(*c8).cpu().numpy(), kept)
+    assert torch.equal(ssm.ckpt8_unpack(*c8, dtype=torch.bfloat16).cpu(), torch.from_numpy(kept).bfloat16())
+    conv_check(t, gy, None, True, dtype, x64=kept.astype(np.float64), ckpt8=c8)
