@@ -512,7 +512,9 @@ int ssm_conv_bwd(const ssm_conv_args* args, const void* gy, const void* glast, c
  * steps of a row, in place of its 2 or 4 bytes an element.  Per block, in
  * float32 (each operation rounded to nearest even):
  *   amax = max |x|,  scale = amax / 127,  q = rint(x * (127 / amax)),
- * and the block stands for q * scale: off by at most (1/2 + 2^-16) scale.  A
+ * with a scale of at most 0x1.020406p+121, the largest whose product with 127 is
+ * finite (only the largest float itself exceeds it), and the block stands for
+ * q * scale: off by at most (1/2 + 2^-16) scale.  A
  * block whose amax is below 2^-100 is all zeros (scale 0); a block that holds a
  * NaN or an infinity stands for NaN throughout.  ssm_conv_fwd writes it in the
  * pass that reads x; ssm_conv_fwd and ssm_conv_bwd take it in place of x;

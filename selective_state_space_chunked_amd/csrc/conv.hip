@@ -29,6 +29,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTiny8 = 7.888609052210118e-31f;   // 2^-100: blocks below it are held as zeros
+constexpr float kTop8 = 0x1.020406p+121f;          // the largest scale whose product with 127 is finite
 
 __device__ __forceinline__ float sigmoid_f(float v) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
@@ -271,7 +272,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int dblocks
                 m = block_max(m);
                 const float amax = __int_as_float(m);
                 const bool bad = m >= 0x7f800000, zero = amax < kTiny8;
-                const float scale = bad ? __int_as_float(0x7fc00000) : zero ? 0.0f : amax / 127.0f;
+                const float scale = bad ? __int_as_float(0x7fc00000) : zero ? 0.0f : fminf(amax / 127.0f, kTop8);
                 const float inv = bad || zero ? 0.0f : 127.0f / amax;
                 if (n[u] > 0) {
                     int8_t* o = p.o8 + row * p.L + t0;

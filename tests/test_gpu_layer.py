@@ -802,3 +802,18 @@ def test_ckpt8_of_the_largest_values(B, D, L, dtype):
     assert np.array_equal(ssm.ckpt8_unpack(*c8).cpu().numpy(), kept)
     assert torch.equal(ssm.ckpt8_unpack(*c8, dtype=torch.bfloat16).cpu(), torch.from_numpy(kept).bfloat16())
     conv_check(t, gy, None, True, dtype, x64=kept.astype(np.float64), ckpt8=c8)
+
+
+def test_ckpt8_of_the_largest_float():
+    """127 times the scale rounded from it would be infinite: the scale is one step less, and every element finite."""
+    top = np.finfo(np.float32).max
+    t, gy = largest_inputs(2, 3, 1099, "f32", float(top), 5)
+    f = ssm.conv_fwd(x=t["x"], w=t["w"], bias=t["bias"], silu=True, want_ckpt8=True)
+    q, s = R.pack(t["x"].cpu().numpy())
+    s = np.minimum(s, np.nextafter(top / np.float32(127), np.float32(0)))
+    assert np.array_equal(f["x8"].cpu().numpy(), q) and np.array_equal(f["x8_scale"].cpu().numpy(), s)
+    kept = R.unpack(q, s)
+    assert np.isfinite(kept).all() and np.abs(kept).max() == np.nextafter(top, np.float32(0))
+    c8 = (f["x8"], f["x8_scale"])
+    assert np.array_equal(ssm.ckpt8_unpack(*c8).cpu().numpy(), kept)
+    conv_check(t, gy, None, True, "f32", x64=kept.astype(np.float64), ckpt8=c8)
