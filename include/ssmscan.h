@@ -513,12 +513,13 @@ int ssm_conv_bwd(const ssm_conv_args* args, const void* gy, const void* glast, c
  * float32 (each operation rounded to nearest even):
  *   amax = max |x|,  scale = amax / 127,  q = rint(x * (127 / amax)),
  * with a scale of at most 0x1.020406p+121, the largest whose product with 127 is
- * finite (only the largest float itself exceeds it), and the block stands for
- * q * scale: off by at most (1/2 + 2^-16) scale.  A
- * block whose amax is below 2^-100 is all zeros (scale 0); a block that holds a
- * NaN or an infinity stands for NaN throughout.  ssm_conv_fwd writes it in the
- * pass that reads x; ssm_conv_fwd and ssm_conv_bwd take it in place of x;
- * ssm_ckpt8_unpack rounds it to a stream that ssm_scan_bwd takes.
+ * finite (only the largest float's exceeds it).  The block stands for q * scale:
+ * off by at most (1/2 + 2^-15) scale, as the reciprocal step, the product, the
+ * scale and the value are each off by up to 2^-24 of at most 127 scales.  A block
+ * whose amax is below 2^-100 is all zeros (scale 0); a block that holds a NaN or
+ * an infinity stands for NaN throughout.  ssm_conv_fwd writes it in the pass that
+ * reads x; ssm_conv_fwd and ssm_conv_bwd take it in place of x; ssm_ckpt8_unpack
+ * rounds it to a stream that ssm_scan_bwd takes.
  */
 #define SSM_CKPT8_BLOCK 64
 typedef struct {

@@ -254,3 +254,19 @@ def test_packed_arguments_are_the_structs(packed, struct):
         if f == "layout":
             v = ctypes.cast(v, ctypes.c_void_p).value
         assert v == i + 1, f
+
+
+def test_checkpoint_error_bound():
+    """Blocks whose element lies next to a half of a step: the rounding to a byte is off by 1/2, and the reciprocal step,
+    the product, the scale and the value by 2^-24 of up to 127 scales each, 127 * 2^-22 < 2^-15 in all."""
+    rng = np.random.default_rng(0)
+    amax = np.append(rng.uniform(1, 2, 200000), 1.0524639).astype(np.float32)
+    x = ((rng.integers(100, 127, amax.size) + 0.5) * amax.astype(np.float64) / 127).astype(np.float32)
+    x = x.view(np.int32) + rng.integers(-4, 5, amax.size, dtype=np.int32)
+    x = x.view(np.float32)
+    x[-1] = 1.0317461      # off by (1/2 + 1.24 * 2^-16) scale
+    block = np.stack([amax, x], -1)[None]
+    q, s = R.pack(block)
+    off = np.abs(R.unpack(q, s).astype(np.float64) - block) / s.astype(np.float64)
+    assert off.max() <= 0.5 + 2.0 ** -15
+    assert off[0, -1, 1] > 0.5 + 2.0 ** -16
