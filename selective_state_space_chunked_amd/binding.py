@@ -14,6 +14,7 @@ import ctypes
 import functools
 import os
 import struct
+import warnings
 
 import torch
 
@@ -152,10 +153,9 @@ def lib():
     """Load libssmscan.so; raise if it has not been built."""
     global _lib
     if _lib is None:
-        for path in (LIB_PATH, os.path.join(_HERE, "_pycall.so")):
-            if not os.path.exists(path):
-                raise RuntimeError(f"HIP library {path} is missing: run __graft_entry__.build() "
-                                   "(or python selective_state_space_chunked_amd/build.py)")
+        if not os.path.exists(LIB_PATH):
+            raise RuntimeError(f"HIP library {LIB_PATH} is missing: run __graft_entry__.build() "
+                               "(or python selective_state_space_chunked_amd/build.py)")
         L = ctypes.CDLL(LIB_PATH)
         L.ssm_workspace_bytes.argtypes = [ctypes.c_int, _vp, ctypes.POINTER(ctypes.c_size_t)]
         L.ssm_scan_fwd.argtypes = [ctypes.POINTER(ScanArgs), ctypes.POINTER(ScanFwdOut), _vp, ctypes.c_size_t, _vp]
@@ -180,23 +180,31 @@ def lib():
         L.ssm_status_string.argtypes = [ctypes.c_int]
         L.ssm_last_error_detail.restype = ctypes.c_char_p
         L.ssm_abi_version.restype = ctypes.c_int
-        _lib = _with_pycall(L)
+        _lib = L
     return _lib
 
 
 # The convolution, checkpoint and packed-row functions go through a native module where a call's arguments are plain
-# (csrc/pycall.cpp): single tokens and small layers are bound by what a call costs the host.
-_pycall = None
+# (csrc/pycall.cpp): single tokens and small layers are bound by what a call costs the host.  The module is built for one
+# Python and torch; where it does not load, the path below takes every call, at more host time.
+_pycall = None   # not loaded yet; False: not there
 
 
-def _with_pycall(L):
+def _load_pycall():
     global _pycall
-    from . import _pycall as native
+    L = lib()
+    try:
+        from . import _pycall as native
+    except ImportError as e:
+        warnings.warn(f"native calls not available ({e}): calls of the convolution, checkpoint and packed-row functions "
+                      "take more host time", RuntimeWarning, stacklevel=4)
+        _pycall = False
+        return False
     native.bind(*(ctypes.cast(getattr(L, f), _vp).value for f in (
         "ssm_conv_fwd", "ssm_conv_bwd", "ssm_ckpt8_pack", "ssm_ckpt8_unpack", "ssm_tokens_conv", "ssm_tokens_scan",
         "ssm_workspace_bytes")))
     _pycall = native
-    return L
+    return native
 
 
 class SSMError(RuntimeError):
@@ -759,13 +767,14 @@ def _launch(dev, fn, *args):
 
 def _native(t):
     """The native calls and where they launch, (module, device, stream), for a call with tensor t; else None: outputs
-    come from an installed allocator, or t is no GPU tensor."""
+    come from an installed allocator, t is no GPU tensor, or the native module does not load."""
     if _allocator is not None or not (isinstance(t, torch.Tensor) and t.is_cuda):
         return None
-    if _pycall is None:
-        lib()
+    m = _load_pycall() if _pycall is None else _pycall
+    if not m:
+        return None
     dev = torch.cuda.current_device()
-    return _pycall, dev, _raw_stream(dev)
+    return m, dev, _raw_stream(dev)
 
 
 def _done(r):

@@ -1,6 +1,10 @@
 """The short convolution, 8-bit checkpoints and packed-row forms without a GPU: their refusals, before anything is
 enqueued, and the float64 references against differences and against the fp64 scan oracle."""
 import ctypes
+import os
+import shutil
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -270,3 +274,47 @@ def test_checkpoint_error_bound():
     off = np.abs(R.unpack(q, s).astype(np.float64) - block) / s.astype(np.float64)
     assert off.max() <= 0.5 + 2.0 ** -15
     assert off[0, -1, 1] > 0.5 + 2.0 ** -16
+
+
+@pytest.mark.parametrize("module", [None, b"no shared object"])
+def test_library_without_the_native_calls(module, tmp_path):
+    """The package with the HIP library alone, the native module missing or built for another interpreter: every entry
+    point is there, and what wants the module warns once and goes on without it."""
+    pkg = tmp_path / "selective_state_space_chunked_amd"
+    pkg.mkdir()
+    here = os.path.dirname(B.__file__)
+    for f in os.listdir(here):
+        if f.endswith(".py"):
+            shutil.copy(os.path.join(here, f), pkg)
+    os.symlink(B.LIB_PATH, pkg / "libssmscan.so")
+    if module is not None:
+        (pkg / "_pycall.so").write_bytes(module)
+    code = """
+import warnings
+import torch
+import selective_state_space_chunked_amd as ssm
+from selective_state_space_chunked_amd import binding as B
+
+with warnings.catch_warnings():
+    warnings.simplefilter("error")
+    assert ssm.lib().ssm_abi_version() == 8          # what the scans need
+with warnings.catch_warnings(record=True) as w:
+    warnings.simplefilter("always")
+
+    class OnGpu(torch.Tensor):
+        is_cuda = True
+
+    x = torch.zeros(1, 2, 3).as_subclass(OnGpu)
+    assert B._native(x) is None and B._native(x) is None
+    assert [i.category for i in w] == [RuntimeWarning] and "native calls" in str(w[0].message)
+    try:
+        ssm.conv_fwd(x=torch.zeros(1, 2, 3), w=torch.zeros(2, 4))
+    except ValueError as e:
+        assert "GPU" in str(e)
+    else:
+        raise AssertionError
+print("went on")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": str(tmp_path)})
+    assert r.returncode == 0 and r.stdout == "went on\n", r.stderr
