@@ -3,7 +3,7 @@
 Every HIP source under csrc/ and the host library csrc/api.cpp are compiled
 for gfx950 and linked into ``selective_state_space_chunked_amd/libssmscan.so``;
 the binding's native calls (csrc/pycall.cpp, host code) become ``_pycall.so``
-beside it.
+beside it, where torch and the Python headers are installed.
 Packed FP32 instructions are disabled for the device code; no fast-math.
 """
 from __future__ import annotations
@@ -68,18 +68,25 @@ def _compile_pycall() -> None:
 
 
 def build(verbose: bool = False) -> str:
+    """Compiles and links the library, and the native calls where torch and the Python headers are there: the library
+    does not need them, nor do its users in C."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         native = ex.submit(_compile_pycall)
         objs = list(ex.map(_compile, srcs))
-        native.result()
     tmp = OUT + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, OUT)
+    try:
+        native.result()
+    except Exception as e:
+        if os.path.exists(PYCALL):   # of an earlier source: its structs may be others by now
+            os.remove(PYCALL)
+        print(f"{OUT} is built without the native calls: {e}", file=sys.stderr)
     if verbose:
         print(f"built {OUT}")
     return OUT

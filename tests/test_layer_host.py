@@ -318,3 +318,27 @@ print("went on")
     r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300,
                        env={**os.environ, "PYTHONPATH": str(tmp_path)})
     assert r.returncode == 0 and r.stdout == "went on\n", r.stderr
+
+
+@pytest.mark.parametrize("lacks", ["torch", "compiler"])
+def test_library_builds_without_the_native_calls(lacks, tmp_path, monkeypatch, capsys):
+    """What only the native calls need -- torch, a host compiler with the Python headers -- the library is built without;
+    native calls of an earlier build do not stay beside it."""
+    from selective_state_space_chunked_amd import build
+
+    def run(cmd, **_):
+        good = not any("pycall" in c for c in cmd)
+        if good:
+            open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0 if good else 1, "", "" if good else "no Python.h")
+
+    out, native = tmp_path / "libssmscan.so", tmp_path / "_pycall.so"
+    native.write_bytes(b"earlier")
+    for name, value in (("OUT", str(out)), ("PYCALL", str(native)), ("BUILD_DIR", str(tmp_path / "b"))):
+        monkeypatch.setattr(build, name, value)
+    monkeypatch.setattr(build.subprocess, "run", run)
+    if lacks == "torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    assert build.build() == str(out)
+    assert out.exists() and not native.exists()
+    assert "without the native calls" in capsys.readouterr().err
