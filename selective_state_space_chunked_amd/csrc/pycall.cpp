@@ -6,6 +6,7 @@
 // binding's own path, which names what is wrong: it then returns NotImplemented
 // and has done nothing.
 #include <ATen/ATen.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -110,13 +111,10 @@ struct Scratch {
     }
 };
 template <typename F>
-PyObject* guarded(F f) {   // nothing C++ throws reaches the interpreter
-    try {
-        return f();
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
-    }
+PyObject* guarded(F f) {   // what C++ throws reaches the interpreter as torch's exceptions: no memory as OutOfMemoryError
+    HANDLE_TH_ERRORS
+    return f();
+    END_HANDLE_TH_ERRORS
 }
 
 // sequences of a packed-row call: seq_start, slot, fresh, pool; pool (slots, D, inner)

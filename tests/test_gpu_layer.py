@@ -817,3 +817,23 @@ def test_ckpt8_of_the_largest_float():
     c8 = (f["x8"], f["x8_scale"])
     assert np.array_equal(ssm.ckpt8_unpack(*c8).cpu().numpy(), kept)
     conv_check(t, gy, None, True, "f32", x64=kept.astype(np.float64), ckpt8=c8)
+
+
+def test_native_calls_without_memory():
+    """No memory for an output: torch's OutOfMemoryError, as from the binding's own path, and the next call is fine."""
+    ssm.set_allocator(None)
+    x8, scale = torch.ones(1, 64, 1 << 20, dtype=torch.int8, device=DEV), torch.ones(1, 64, 1 << 14, device=DEV)
+    w, gy = torch.ones(64, 4, device=DEV), torch.ones(1, 64, 1 << 20, device=DEV)
+    ref = ssm.ckpt8_unpack(x8[:, :1].contiguous(), scale[:, :1].contiguous())
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(
+        (torch.cuda.memory_reserved() + (64 << 20)) / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        for call in (lambda: ssm.ckpt8_unpack(x8, scale), lambda: ssm.conv_fwd(x=gy, w=w),
+                     lambda: ssm.conv_bwd(gy=gy, ckpt8=(x8, scale), w=w)):
+            with pytest.raises(torch.OutOfMemoryError):
+                call()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert torch.equal(ssm.ckpt8_unpack(x8, scale)[:, :1], ref)
