@@ -548,8 +548,9 @@ int ssm_ckpt8_unpack(const ssm_ckpt8_args* args, const int8_t* x8, const float* 
  *    host: values out of range are never followed out of the buffers, but rows
  *    of sequences that overlap or descend have unspecified results.
  *  - Rows: row strides in elements; the row itself is contiguous.  Inputs may be
- *    slices of wider rows (any stride from 0 to 2^26 - 1), y's stride is at
- *    least its row.
+ *    slices of wider rows (any stride from 0 to 2^40 - 1; to 2^26 - 1 in
+ *    ssm_tokens_scan with seq_start), y's stride is at least its row.  The
+ *    stride of a single row is not used.
  *  - pool_stride: elements from one slot to the next, at least a slot's own.
  *  - pool is read and written; it must not overlap any other buffer.
  */

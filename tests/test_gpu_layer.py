@@ -837,3 +837,34 @@ def test_native_calls_without_memory():
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert torch.equal(ssm.ckpt8_unpack(x8, scale)[:, :1], ref)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_last_tokens_of_long_rows(dtype):
+    """The last token of each of two long sequences, a slice whose rows are 2^26 elements apart, through the step forms
+    and as prompts of one row: as the same rows laid out densely."""
+    r = gen(71)
+    D, N, W, S = 2048, 16, 4, 2
+    hidden = torch.zeros(S, 2 ** 15, D, dtype=DT[dtype], device=DEV)
+    t = scan_inputs(S, D, N, dtype, r)
+    hidden[:, -1] = t["x"]
+    far = hidden[:, -1]
+    assert far.stride() == (2 ** 26, 1)
+    w, one = dev(r.normal(size=(D, W))), torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    cpool, spool = dev(r.normal(size=(S, D, W - 1)), dtype), dev(r.normal(size=(S, D, N)))
+    rows = ("delta", "x", "z", "Bm", "C")
+    for n, at in ((S, {}), (1, dict(seq_start=one)), (1, {})):
+        cut = {k: v[:n] if k in rows else v for k, v in t.items()}
+        res = []
+        for x in (far[:n], t["x"][:n]):
+            c, s = cpool[:n].clone(), spool[:n].clone()
+            a = {k: x if k in ("delta", "x", "z") else v for k, v in cut.items()}
+            res.append([ssm.tokens_conv(x=x, w=w, silu=True, pool=c, **at)["y"],
+                        ssm.tokens_scan(**a, delta_softplus=True, pool=s, **at)["y"], c, s])
+        assert all(torch.equal(p, q) for p, q in zip(*res))
+    c1, c2 = cpool.clone(), cpool.clone()
+    start = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    p, q = (ssm.tokens_conv(x=x, w=w, pool=c, seq_start=start)["y"] for x, c in ((far, c1), (t["x"], c2)))
+    assert torch.equal(p, q) and torch.equal(c1, c2)
+    with pytest.raises(ssm.binding.SSMError):      # the scan of prompts ends at 2^26
+        ssm.tokens_scan(**{**t, "x": far}, pool=spool.clone(), seq_start=start)

@@ -342,3 +342,31 @@ def test_library_builds_without_the_native_calls(lacks, tmp_path, monkeypatch, c
     assert build.build() == str(out)
     assert out.exists() and not native.exists()
     assert "without the native calls" in capsys.readouterr().err
+
+
+def test_row_strides():
+    """A single row's stride is not used; the step forms and the convolution take any stride below 2^40, the scan of
+    prompts any below 2^26."""
+    L, n = B.lib(), ctypes.c_size_t(0)
+
+    def conv(**over):
+        return L.ssm_workspace_bytes(B.SSM_OP_TOKENS_CONV, ctypes.byref(tconv_args(**over)), ctypes.byref(n))
+
+    def scan(**over):
+        return L.ssm_workspace_bytes(B.SSM_OP_TOKENS_SCAN, ctypes.byref(tscan_args(**over)), ctypes.byref(n))
+
+    step = dict(seq_start=None, sequences=10, slots=10)
+    one = dict(tokens=1, sequences=1)
+    for name in ("x_stride", "y_stride", "delta_stride", "Bm_stride", "C_stride", "z_stride"):
+        calls = [scan] if name not in ("x_stride", "y_stride") else [conv, scan]
+        z = dict(z=10 * FAKE, z_stride=8) if name == "z_stride" else {}
+        for call in calls:
+            def stride(v, **over):
+                return call(**{**(z if call is scan else {}), **over, name: v})
+
+            assert stride(1 << 50, **one) == 0 and stride(0, **one) == 0 and stride(1 << 50, **one, seq_start=None) == 0
+            assert stride(1 << 26, **step) == 0 and stride(1 << 39, **step) == 0
+            assert stride(1 << 40, **step) == code("LAYOUT") and stride(-1, **step) == code("LAYOUT")
+            assert stride(1 << 26) == (0 if call is conv else code("LAYOUT")) and stride((1 << 26) - 1) == 0
+            far = {"tokens": (1 << 24) - 1, "sequences": (1 << 24) - 1, "slots": 1 << 24, "seq_start": None}
+            assert stride(1 << 30, **far) == code("LAYOUT")     # ends past any memory
