@@ -868,3 +868,32 @@ def test_last_tokens_of_long_rows(dtype):
     assert torch.equal(p, q) and torch.equal(c1, c2)
     with pytest.raises(ssm.binding.SSMError):      # the scan of prompts ends at 2^26
         ssm.tokens_scan(**{**t, "x": far}, pool=spool.clone(), seq_start=start)
+
+
+@pytest.mark.parametrize("layer", [True, False])
+@pytest.mark.parametrize("N", range(1, 17))
+def test_tokens_scan_of_every_state_size(N, layer):
+    """Each state size has a kernel and a layout of its own: prompts over more ranges than a wave composes by itself, with
+    skip, gate and softplus and without, and the same states in steps."""
+    r = gen(100 + N)
+    D, lengths = 70, [5, 1, 0, 17, 390, 64, 2]
+    start, slot, fresh, slots = sequences(lengths, N, empty=False)
+    T = int(start[-1])
+    t = scan_inputs(T, D, N, "bf16" if N % 2 else "f32", r, view=True, gate=layer)
+    dtype = "bf16" if N % 2 else "f32"
+    if not layer:
+        t["delta"], t["delta_bias"] = dev(r.uniform(0.001, 0.2, (T, D)), dtype), None
+    owned = R.owners(T, len(slot), slots, start, slot)
+    pool, y = dev(dirty(r.normal(size=(slots, D, N)), owned, fresh)), torch.zeros(T, D, dtype=DT[dtype], device=DEV)
+    ref, err, pref, perr = scan_ref(t, layer, pool, start, slot, fresh, y)
+    got = ssm.tokens_scan(**t, delta_softplus=layer, pool=pool, seq_start=torch.from_numpy(start).to(DEV),
+                          slot=torch.from_numpy(slot).to(DEV), fresh=torch.from_numpy(fresh).to(DEV), out={"y": y})
+    R.check("y", got["y"], ref, err, dtype)
+    R.check("pool", pool, pref, np.nan_to_num(perr), "f32")
+    S = 5
+    step = {k: v[:S] if k in ("delta", "x", "z", "Bm", "C") and v is not None else v for k, v in t.items()}
+    pool = dev(r.normal(size=(S, D, N)))
+    ref, err, pref, perr = scan_ref(step, layer, pool, None, None, None, y[:S])
+    got = ssm.tokens_scan(**step, delta_softplus=layer, pool=pool)
+    R.check("step y", got["y"], ref, err, dtype)
+    R.check("step pool", pool, pref, perr, "f32")
