@@ -897,3 +897,46 @@ def test_tokens_scan_of_every_state_size(N, layer):
     got = ssm.tokens_scan(**step, delta_softplus=layer, pool=pool)
     R.check("step y", got["y"], ref, err, dtype)
     R.check("step pool", pool, pref, perr, "f32")
+
+
+def test_native_calls_in_a_graph():
+    """The native calls allocate outputs and workspaces in a captured graph's own memory: replays with other inputs, eager
+    calls and waits between them, equal the eager calls bit for bit."""
+    ssm.set_allocator(None)
+    r = gen(81)
+    D, N, W, T = 72, 16, 4, 600
+    t, gy, glast = conv_inputs(3, D, 1100, W, "bf16", True, 82)
+    s = scan_inputs(T, D, N, "bf16", r, view=True)
+    at = dict(seq_start=torch.tensor([0, 31, 31, 590, T], dtype=torch.int32, device=DEV),
+              slot=torch.tensor([3, 0, 2, 1], dtype=torch.int32, device=DEV))
+    pools = [dev(r.normal(size=(4, D, W - 1)), "bf16"), dev(r.normal(size=(4, D, N)))]
+    keep = [p.clone() for p in pools]
+
+    def run():
+        for p, k in zip(pools, keep):
+            p.copy_(k)
+        o = dict(ssm.conv_fwd(x=t["x"], w=t["w"], bias=t["bias"], init=t["init"], silu=True, want_ckpt8=True))
+        o.update(ssm.conv_bwd(gy=gy, glast=glast, ckpt8=(o["x8"], o["x8_scale"]), w=t["w"], bias=t["bias"],
+                              init=t["init"], silu=True))
+        o["back"] = ssm.ckpt8_unpack(o["x8"], o["x8_scale"], dtype=torch.bfloat16)
+        o["c"] = ssm.tokens_conv(x=s["x"], w=t["w"], bias=t["bias"], silu=True, pool=pools[0], **at)["y"]
+        o["s"] = ssm.tokens_scan(**{**s, "x": o["c"]}, delta_softplus=True, pool=pools[1], **at)["y"]
+        o["pools"] = torch.cat([p.float().flatten() for p in pools])
+        return o
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap = run()
+    for i in range(4):
+        t["x"].copy_(dev(r.normal(size=t["x"].shape), "bf16"))
+        s["x"].copy_(dev(r.normal(size=s["x"].shape), "bf16"))
+        keep[1].copy_(dev(r.normal(size=keep[1].shape)))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {k: v.clone() for k, v in cap.items()}
+        eager = run()
+        torch.cuda.synchronize()
+        for k in eager:
+            assert torch.equal(eager[k], got[k]), (i, k)
