@@ -596,9 +596,9 @@ typedef struct {
  *   h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t,
  *   y_t = (C_t . h_t + skip x_t) * z_t sigmoid(z_t)     (skip, z: where given).
  * The states are float32.  The workspace (SSM_OP_TOKENS_SCAN) holds the states that cross from one
- * range of rows to the next; the step form needs none.  Ranges are joined by exp(A sum delta), which
- * has to be a finite float32: a sequence that grows by more than e^88 over a range of rows (A delta > 0)
- * is out of reach of the packed form, though not of single steps. */
+ * range of rows to the next; the step form needs none.  Ranges are joined by exp(A sum delta), several
+ * of them at once, which has to be a finite float32: a sequence that grows by more than e^88 over a
+ * call (A delta > 0) is out of reach of the packed form, though not of single steps. */
 int ssm_tokens_scan(const ssm_tokens_scan_args* args, void* ws, size_t ws_bytes, void* stream);
 
 /* Diagnostics: per-kernel timing with HIP events.  After ssm_profile_begin(n)

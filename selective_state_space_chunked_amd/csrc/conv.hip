@@ -11,13 +11,13 @@
 //
 // Measured, kernel time and bytes moved (a copy of 256 MiB runs at 4.9 TB/s,
 // read + written):
-//   B=8 D=2048 L=4096 W=4 bf16   forward                65 us   4.1 TB/s
-//                                forward + checkpoint   83 us   4.1 TB/s
-//                                backward               79 us   5.1 TB/s
-//                                backward from 8 bits   85 us   4.0 TB/s
-//                                checkpoint to bf16     34 us   6.0 TB/s
-//   B=1 D=1024 L=128000 f32      checkpoint            144 us   4.6 TB/s
-//                                checkpoint to f32     126 us   5.3 TB/s
+//   B=8 D=2048 L=4096 W=4 bf16   forward                63 us   4.4 TB/s
+//                                forward + checkpoint   77 us   4.5 TB/s
+//                                backward               77 us   5.3 TB/s
+//                                backward from 8 bits   77 us   4.5 TB/s
+//                                checkpoint to bf16     32 us   6.4 TB/s
+//   B=1 D=1024 L=128000 f32      checkpoint            145 us   4.6 TB/s
+//                                checkpoint to f32     124 us   5.4 TB/s
 #include <algorithm>
 
 #include "buffer.hpp"
@@ -205,8 +205,8 @@ struct Run8 {
     }
     // q s as 2 ((q + 128) h - 128 h) with h = s / 2: the sum of unsigned bytes is one conversion, and the multiply-add
     // rounds the exact q h once.  128 s would overflow for blocks that reach to within 1/128 of the largest
-    // float, 128 h does not; halving and doubling are exact.  B=8 D=2048 L=4096, backward to bf16:
-    // 86.6 us, by signed bytes and one product (more instructions) 92.1.
+    // float, 128 h does not; halving and doubling are exact.  B=8 D=2048 L=4096, backward to bf16 with the
+    // sums over the parts: 86.6 us, by signed bytes and one product (more instructions) 92.1.
     __device__ __forceinline__ void get(float (&v)[kConvRun]) const {
         const uint32_t w[2] = {r.x ^ 0x80808080u, r.y ^ 0x80808080u};
         const float h = 0.5f * s, off = -128.0f * h;
@@ -581,8 +581,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
 // after a tile again (one lane a step, from the inputs and gradients there), so waves wait for nothing of each other;
 // a tile's row and place are scalar, and a lane's addresses are its fixed offset from them.  The loop issues the same
 // loads and stores in every turn, so the wait for a tile's loads is one for these alone, with the next tile's loads
-// and the last one's stores under way (with a branch around either the compiler has to wait for everything).  Bound by HBM, with half of the time in its 32 vector
-// instructions a step.  B=8 D=2048 L=4096 bf16: 79 us, from 8 bits 85 us; the kernel above takes 92 and 99.
+// and the last one's stores under way (with a branch around either the compiler has to wait for everything).  Bound by
+// HBM, with half of the time in its 33 vector instructions a step (38 from 8 bits).  B=8 D=2048 L=4096 bf16, with the
+// sums over the parts: 82 us, from 8 bits 81; the kernel above takes 94 and 92.
 template <typename T, int W, bool X8>
 struct RowTile {
     static constexpr int H = W - 1, R = kConvRun, N = 64 * R;   // steps of a tile

@@ -281,7 +281,8 @@ double roof_instrs_per_lane(int kind, int chains, int iters);
 constexpr int kConvRun = 8;     // consecutive steps of one lane
 constexpr int kCkptBlock = 64;  // steps that share a scale
 // backward: groups of 256 items a workgroup takes at most, and the workgroups there should be before it takes more
-// than one (B=8 D=2048 L=4096 bf16 with the sums over parts, us: 4 groups 98, 8 groups 93, 16 groups, one part, 97)
+// than one (L=4096 bf16 with the sums over parts, us with 4, 8 and 16 groups: B=8 D=2048 87, 84, 86; B=16 D=1024 81, 80,
+// 88; B=8 D=512 L=16384 82, 82, 85)
 constexpr int kConvGroups = 8, kConvWG = 4096, kConvOne = 4;
 struct ConvParams {
     const void* x; const int8_t* x8; const float* x8_scale;
@@ -329,12 +330,12 @@ struct TokScanParams {
 // rows a range covers at least
 constexpr int kTokRowsMin = 16;
 // Up to this many ranges a wave of the second pass composes the states before its own by itself; a kernel of
-// its own costs more for so few (333 rows x 200 channels, N = 7, a pass: 19.4 us with it, 16.2 us without; 25 us
+// its own costs more for so few (333 rows x 200 channels, N = 7, a pass: 17.7 us with it, 15.6 us without; 19.8 us
 // with ranges of at least 32 rows).
 constexpr int kTokChain = 24;
 // The waves the ranges are made for: the second pass's registers allow four on each of the 1024 SIMDs, 4096 at
-// once.  Measured at 8192 rows x 2048 channels (both passes and the states between): 4096 waves 124 us,
-// 8192 waves 141 us, 5120 waves with registers for five on a SIMD 138 us.
+// once.  Measured at 8192 rows x 2048 channels and 17000 x 1024 (both passes and the states between): 4096 waves 114
+// and 116 us, 8192 waves 128 and 132 us, 5120 waves with registers for five on a SIMD 126 and 130 us.
 constexpr int kTokWaves = 4096;
 hipError_t launch_tok_conv(const TokConvParams& p, int dtype, hipStream_t st);
 hipError_t launch_tok_scan(const TokScanParams& p, int dtype, bool sum, hipStream_t st);

@@ -119,7 +119,7 @@ struct SeqTable {
 // Four consecutive elements at any element's address (global memory takes
 // unaligned accesses), as floats and back.  Eight bf16 elements a lane would be
 // whole 16-byte accesses, but twice the registers: the packed convolution of 8192
-// rows x 4096 channels takes 33.6 us with four and 37.6 us with eight.
+// rows x 4096 channels took 33.6 us with four and 37.6 us with eight.
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
 template <typename T> struct Vec;

@@ -19,13 +19,16 @@
 // cycles, the others 2 to 3): the main loops hold 217 (first pass) and 314 vector
 // instructions for four rows, 208 and 272 of them the state's own; loads by
 // scalar addresses and B, C by way of LDS leave the rest that small.  8192 rows x
-// 2048 channels x 16 states in bf16, 13 sequences: 50 us, 10 us between and 65 us
-// (17000 x 1024, one sequence: 52, 10 and 64), where the streams alone are 28 us of
-// memory traffic.  Of each pass about 10 us do not shrink with the rows.
+// 2048 channels x 16 states in bf16, 13 sequences: 46 us, 10 us between and 59 us
+// (17000 x 1024, one sequence: 48, 10 and 58), where the streams alone are 28 us of
+// memory traffic.  Of each pass about 10 us do not shrink with the rows: a wave's first loads follow one
+// another (lists of sequences, A, states, rows).  Each sequence in a range is walked from its own first loads on, so
+// many short ones among long ones cost more: 8 sequences of 1024 rows and 256 of one row take 338 us (in 9 sequences
+// 117 us), 1024 of 8 rows 128 us, all at 2048 channels.
 //
 // Single tokens.  Bound by the states' traffic: four states a lane, so a wave
-// reads and writes the pool in whole lines.  256 x 4096 x 16: 134 MB in 26 us,
-// 5.2 TB/s; one sequence of 2048 channels: 3.7 us, the latency of its loads.
+// reads and writes the pool in whole lines.  256 x 4096 x 16 with 32 places empty: 125 MB in 25 us,
+// 5.0 TB/s; one sequence of 2048 channels: 3.5 us, the latency of its loads.
 #include <algorithm>
 
 #include "buffer.hpp"
@@ -77,7 +80,7 @@ struct ScanLane {
         row_bytes = (uint32_t)p.D * sizeof(T);
         bz = (uint32_t)sz * sizeof(T); by = max((uint32_t)sy * (uint32_t)sizeof(T), row_bytes);
         const int lane = lane_id(), n = lane % NQ, r = lane / NQ;
-        ob = n < N ? (uint32_t)(r * (int)sB + n) * sizeof(T) : 0x7fffffffu;   // places past the states read as 0
+        ob = n < N ? (uint32_t)(r * (int)sB + n) * sizeof(T) : 0x7fffffffu;   // places past the states: 0, or any element of rows far apart (they meet nothing)
         oc = n < N ? (uint32_t)(r * (int)sC + n) * sizeof(T) : 0x7fffffffu;
         lds = lds_;
         put = lds_ + r * 2 * NQ + (n % 4) * (NQ / 4) + n / 4;
