@@ -226,7 +226,7 @@ def _gated(s):
     before[..., 1:] = h[..., :-1]
     if s["h0"] is not None:
         before[..., 0] = s["h0"]
-    mu = s["gy"].float()
+    mu = s["gy"].float().clone()
     if s["gh_last"] is not None:
         mu[..., -1] += s["gh_last"]
     after = torch.zeros_like(a)
