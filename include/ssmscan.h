@@ -75,7 +75,10 @@
 extern "C" {
 #endif
 
-/* 8: adds the short causal convolution (ssm_conv_*), 8-bit activation
+/* Entry points added since with structs of their own leave the version as it is:
+ * the gated recurrence (ssm_gated_*, ssm_tokens_gated), the group norm
+ * (ssm_group_norm_*) and products in 8-bit integers (ssm_tokens_pack8, _mm8).
+ * 8: adds the short causal convolution (ssm_conv_*), 8-bit activation
  * checkpoints (ssm_ckpt8_*) and the serving forms over packed rows
  * (ssm_tokens_*); structs of 7 unchanged.  7 added SSM_HEAD_SCALAR
  * (head_dim field); 6 added strided views (ssm_layout, the layout fields of ssm_scan_args and
@@ -118,6 +121,10 @@ extern "C" {
 #define SSM_OP_CONV_BWD     9   /* ssm_conv_args                           */
 #define SSM_OP_TOKENS_CONV 10   /* ssm_tokens_conv_args: no workspace      */
 #define SSM_OP_TOKENS_SCAN 11   /* ssm_tokens_scan_args                    */
+#define SSM_OP_GATED_FWD   12   /* ssm_gated_args: no workspace            */
+#define SSM_OP_GATED_BWD   13   /* ssm_gated_args                          */
+#define SSM_OP_TOKENS_GATED 14  /* ssm_tokens_gated_args                   */
+#define SSM_OP_GROUP_NORM_BWD 15 /* ssm_group_norm_args                    */
 
 /* discretisations of SSM_REAL_SELECTIVE (S3M page, section 1.1) */
 #define SSM_EULER 0   /* b_t = delta_t x_t B_t (the default)                               */
@@ -600,6 +607,147 @@ typedef struct {
  * of them at once, which has to be a finite float32: a sequence that grows by more than e^88 over a
  * call (A delta > 0) is out of reach of the packed form, though not of single steps. */
 int ssm_tokens_scan(const ssm_tokens_scan_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gated linear recurrence.  A state for each channel whose decay and input are
+ * opened by gates of their own (the scan without a state expansion):
+ *   rho = sigmoid(r + r_bias),  iota = sigmoid(i + i_bias),
+ *   q = power * softplus(lam) * rho,  a = exp(-q),
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) iota_t x_t,   y_t = h_t,   h_{-1} = h0.
+ * The states and everything that forms them are float32.  Where a gate's input
+ * lies below about -87 its sigmoid is 0.  Strides are in elements: batch, then
+ * channel; steps are contiguous; 0 (broadcast) for inputs only, whose gradients
+ * come back for every position.  batch, channels and length may be 0 (h_last is
+ * then h0 or 0, gh0 is gh_last or 0, parameter gradients are 0).
+ */
+#define SSM_GATED_CHUNK 128
+typedef struct {
+    int32_t dtype;           /* of x, r, i, y and their gradients: SSM_F32 or SSM_BF16       */
+    float   power;           /* > 0: the decay of a wide open gate is exp(-power softplus(lam)) */
+    int64_t batch, channels, length;
+    const void*  x;          /* (B,D,L) input                                                */
+    const void*  r;          /* (B,D,L) decay gate, before its sigmoid                       */
+    const void*  i;          /* (B,D,L) input gate, before its sigmoid                       */
+    const float* lam;        /* (D) f32                                                      */
+    const float* r_bias;     /* nullable (D) f32                                             */
+    const float* i_bias;     /* nullable (D) f32                                             */
+    const float* h0;         /* nullable (B,D) f32                                           */
+    int64_t x_stride[2], r_stride[2], i_stride[2];
+} ssm_gated_args;
+
+typedef struct {
+    void*  y;                /* nullable (B,D,L) dtype                                       */
+    float* h_last;           /* nullable (B,D)                                               */
+    float* ckpt;             /* nullable (B,D,ceil(L/SSM_GATED_CHUNK)): the state that every
+                                SSM_GATED_CHUNK steps begin with, for the backward           */
+    int64_t y_stride[2];
+} ssm_gated_fwd_out;
+
+typedef struct {
+    const void*  gy;         /* (B,D,L) dtype                                                */
+    const float* gh_last;    /* nullable (B,D)                                               */
+    const float* ckpt;       /* nullable: formed again in the workspace (the same bits)      */
+    int64_t gy_stride[2];
+} ssm_gated_bwd_in;
+
+typedef struct {
+    void  *gx, *gr, *gi;     /* nullable (B,D,L) dtype                                       */
+    float *glam, *gr_bias, *gi_bias;   /* nullable (D)                                       */
+    float* gh0;              /* nullable (B,D)                                               */
+    int64_t gx_stride[2], gr_stride[2], gi_stride[2];
+} ssm_gated_grads;
+
+int ssm_gated_fwd(const ssm_gated_args* args, const ssm_gated_fwd_out* out, void* stream);
+/* Gradients of Loss = sum <gy, y> + <gh_last, h_last>. */
+int ssm_gated_bwd(const ssm_gated_args* args, const ssm_gated_bwd_in* in, const ssm_gated_grads* grads,
+                  void* ws, size_t ws_bytes, void* stream);
+
+/* The gated recurrence over packed rows, with sequences, pool and rows as in ssm_tokens_conv above.  The workspace
+ * (SSM_OP_TOKENS_GATED) holds the states that cross from one range of rows to the next; the step form needs none. */
+typedef struct {
+    int32_t dtype;             /* of x, r, i and y                                           */
+    float   power;
+    int64_t tokens, channels, sequences, slots;
+    const void*  x;            /* (T,D)                                                      */
+    const void*  r;            /* (T,D)                                                      */
+    const void*  i;            /* (T,D)                                                      */
+    const float* lam;          /* (D)                                                        */
+    const float* r_bias;       /* nullable (D)                                               */
+    const float* i_bias;       /* nullable (D)                                               */
+    const int32_t* seq_start;
+    const int32_t* slot;
+    const uint8_t* fresh;
+    float* pool;               /* (slots,D) f32: the state h                                 */
+    void*  y;                  /* (T,D)                                                      */
+    int64_t x_stride, r_stride, i_stride, y_stride, pool_stride;
+} ssm_tokens_gated_args;
+int ssm_tokens_gated(const ssm_tokens_gated_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Group norm of rows, channels last, with activation and gate.  The channels of
+ * a row are `groups` groups of consecutive ones; statistics are those of one
+ * group of one row, so none crosses from token to token:
+ *   xh = (x - mean) / sqrt(var + eps),  v = xh w + bias,
+ *   u = v, or v sigmoid(v) with silu = 1,   y = u, or u z sigmoid(z) with z.
+ * The backward forms the statistics again from x.  Row strides as in the packed
+ * forms above.  rows may be 0 (gw, gbias are then 0).  Errors: SSM_ERR_SHAPE where
+ * groups does not divide channels, SSM_ERR_UNSUPPORTED for groups of more than 8192
+ * channels.
+ */
+typedef struct {
+    int32_t dtype;             /* of x, z, y and their gradients                             */
+    int32_t silu;              /* 0 or 1                                                     */
+    int64_t rows, channels, groups;
+    const void*  x;            /* (T,C)                                                      */
+    const void*  z;            /* nullable (T,C) gate                                        */
+    const float* w;            /* nullable (C) f32 (1)                                       */
+    const float* bias;         /* nullable (C) f32 (0)                                       */
+    int64_t x_stride, z_stride;
+    float eps;                 /* >= 0                                                       */
+} ssm_group_norm_args;
+
+typedef struct {
+    void  *gx, *gz;            /* nullable (T,C) dtype                                       */
+    float *gw, *gbias;         /* nullable (C)                                               */
+    int64_t gx_stride, gz_stride;
+} ssm_group_norm_grads;
+
+int ssm_group_norm_fwd(const ssm_group_norm_args* args, void* y, int64_t y_stride, void* stream);
+int ssm_group_norm_bwd(const ssm_group_norm_args* args, const void* gy, int64_t gy_stride,
+                       const ssm_group_norm_grads* grads, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Products in 8-bit integers.  ssm_tokens_pack8 holds each row in signed bytes
+ * and one float32 scale, in the format of the 8-bit checkpoints above with a row
+ * in place of a block of steps.  ssm_tokens_mm8 multiplies such rows with weights
+ * that have a scale for each output:
+ *   y[t][n] = x8_scale[t] w8_scale[n] sum_k x8[t][k] w8[n][k] + bias[n].
+ * The sums are whole numbers in 32 bits (inputs below 2^17: they cannot overflow),
+ * rounded once to float32 before the scales.  Rows may have any stride from 0 (inputs) or
+ * their own width (outputs) to 2^40 - 1.  With no inputs y is bias.
+ */
+typedef struct {
+    int32_t dtype;             /* of x                                                       */
+    int64_t tokens, channels;
+    const void* x;             /* (T,K)                                                      */
+    int8_t* x8;                /* (T,K)                                                      */
+    float*  x8_scale;          /* (T)                                                        */
+    int64_t x_stride, x8_stride;
+} ssm_tokens_pack8_args;
+int ssm_tokens_pack8(const ssm_tokens_pack8_args* args, void* stream);
+
+typedef struct {
+    int32_t dtype;             /* of y                                                       */
+    int64_t tokens, inputs, outputs;
+    const int8_t* x8;          /* (T,K)                                                      */
+    const float*  x8_scale;    /* (T)                                                        */
+    const int8_t* w8;          /* (N,K)                                                      */
+    const float*  w8_scale;    /* (N)                                                        */
+    const float*  bias;        /* nullable (N)                                               */
+    void* y;                   /* (T,N)                                                      */
+    int64_t x8_stride, w8_stride, y_stride;
+} ssm_tokens_mm8_args;
+int ssm_tokens_mm8(const ssm_tokens_mm8_args* args, void* stream);
 
 /* Diagnostics: per-kernel timing with HIP events.  After ssm_profile_begin(n)
  * every kernel the entry points enqueue from this thread is bracketed by two

@@ -3,7 +3,8 @@ sensitivity (one output row or a block of rows of the input Jacobian),
 forward-mode complex gradients, complex scans with given transitions and
 PD-transition scans, with the short causal convolution of a layer, 8-bit
 activation checkpoints and the serving forms over packed rows and single
-tokens, behind the C ABI of include/ssmscan.h.
+tokens; the gated linear recurrence, the group norm of its rows and products
+in 8-bit integers, behind the C ABI of include/ssmscan.h.
 
 The Python functions marshal torch tensors into the C ABI of libssmscan.so;
 all computation runs in the library's HIP kernels.
@@ -11,6 +12,7 @@ all computation runs in the library's HIP kernels.
 from .binding import (  # noqa: F401
     SSM_BF16,
     SSM_CKPT8_BLOCK,
+    SSM_GATED_CHUNK,
     SSM_EULER,
     SSM_ZOH,
     SSM_COMPLEX_DENSE,
@@ -25,6 +27,10 @@ from .binding import (  # noqa: F401
     complex_rtrl,
     conv_bwd,
     conv_fwd,
+    gated_bwd,
+    gated_fwd,
+    group_norm_bwd,
+    group_norm_fwd,
     impulse_sensitivity,
     lib,
     n_chunks,
@@ -37,5 +43,8 @@ from .binding import (  # noqa: F401
     sensitivity_rows,
     set_allocator,
     tokens_conv,
+    tokens_gated,
+    tokens_mm8,
+    tokens_pack8,
     tokens_scan,
 )

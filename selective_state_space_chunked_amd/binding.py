@@ -31,7 +31,8 @@ SSM_REAL_SELECTIVE, SSM_REAL_DENSE, SSM_COMPLEX_SHARED, SSM_COMPLEX_DENSE, SSM_H
 _COMPLEX_MODES = (SSM_COMPLEX_SHARED, SSM_COMPLEX_DENSE)
 (SSM_OP_SCAN_FWD, SSM_OP_SCAN_BWD, SSM_OP_IMPULSE, SSM_OP_PD_FWD, SSM_OP_PD_BWD, SSM_OP_COMPLEX_RTRL,
  SSM_OP_OUTPUT_SENS, SSM_OP_SENS_ROWS, SSM_OP_CONV_FWD, SSM_OP_CONV_BWD, SSM_OP_TOKENS_CONV,
- SSM_OP_TOKENS_SCAN) = range(12)
+ SSM_OP_TOKENS_SCAN, SSM_OP_GATED_FWD, SSM_OP_GATED_BWD, SSM_OP_TOKENS_GATED, SSM_OP_GROUP_NORM_BWD) = range(16)
+SSM_GATED_CHUNK = 128  # steps between the states that a gated recurrence keeps for its backward
 SSM_CKPT8_BLOCK = 64   # steps of a row that share one scale of an 8-bit checkpoint
 
 _vp = ctypes.c_void_p
@@ -146,6 +147,55 @@ class TokensScanArgs(ctypes.Structure):
                 ("z_stride", _i64), ("y_stride", _i64), ("pool_stride", _i64)]
 
 
+class GatedArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("power", ctypes.c_float),
+                ("batch", _i64), ("channels", _i64), ("length", _i64),
+                ("x", _vp), ("r", _vp), ("i", _vp), ("lam", _vp), ("r_bias", _vp), ("i_bias", _vp), ("h0", _vp),
+                ("x_stride", _i64 * 2), ("r_stride", _i64 * 2), ("i_stride", _i64 * 2)]
+
+
+class GatedFwdOut(ctypes.Structure):
+    _fields_ = [("y", _vp), ("h_last", _vp), ("ckpt", _vp), ("y_stride", _i64 * 2)]
+
+
+class GatedBwdIn(ctypes.Structure):
+    _fields_ = [("gy", _vp), ("gh_last", _vp), ("ckpt", _vp), ("gy_stride", _i64 * 2)]
+
+
+class GatedGrads(ctypes.Structure):
+    _fields_ = [("gx", _vp), ("gr", _vp), ("gi", _vp), ("glam", _vp), ("gr_bias", _vp), ("gi_bias", _vp), ("gh0", _vp),
+                ("gx_stride", _i64 * 2), ("gr_stride", _i64 * 2), ("gi_stride", _i64 * 2)]
+
+
+class TokensGatedArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("power", ctypes.c_float),
+                ("tokens", _i64), ("channels", _i64), ("sequences", _i64), ("slots", _i64),
+                ("x", _vp), ("r", _vp), ("i", _vp), ("lam", _vp), ("r_bias", _vp), ("i_bias", _vp),
+                ("seq_start", _vp), ("slot", _vp), ("fresh", _vp), ("pool", _vp), ("y", _vp),
+                ("x_stride", _i64), ("r_stride", _i64), ("i_stride", _i64), ("y_stride", _i64), ("pool_stride", _i64)]
+
+
+class GroupNormArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("silu", ctypes.c_int32), ("rows", _i64), ("channels", _i64), ("groups", _i64),
+                ("x", _vp), ("z", _vp), ("w", _vp), ("bias", _vp), ("x_stride", _i64), ("z_stride", _i64),
+                ("eps", ctypes.c_float)]
+
+
+class GroupNormGrads(ctypes.Structure):
+    _fields_ = [("gx", _vp), ("gz", _vp), ("gw", _vp), ("gbias", _vp), ("gx_stride", _i64), ("gz_stride", _i64)]
+
+
+class TokensPack8Args(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("tokens", _i64), ("channels", _i64), ("x", _vp), ("x8", _vp),
+                ("x8_scale", _vp), ("x_stride", _i64), ("x8_stride", _i64)]
+
+
+class TokensMm8Args(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("tokens", _i64), ("inputs", _i64), ("outputs", _i64), ("x8", _vp),
+                ("x8_scale", _vp), ("w8", _vp), ("w8_scale", _vp), ("bias", _vp), ("y", _vp), ("x8_stride", _i64),
+                ("w8_stride", _i64), ("y_stride", _i64)]
+
+
 _lib = None
 
 
@@ -176,6 +226,13 @@ def lib():
         L.ssm_ckpt8_unpack.argtypes = [_vp, _vp, _vp, _vp, _vp]
         L.ssm_tokens_conv.argtypes = [_vp, _vp]
         L.ssm_tokens_scan.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
+        L.ssm_gated_fwd.argtypes = [_vp, _vp, _vp]
+        L.ssm_gated_bwd.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+        L.ssm_tokens_gated.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
+        L.ssm_group_norm_fwd.argtypes = [_vp, _vp, _i64, _vp]
+        L.ssm_group_norm_bwd.argtypes = [_vp, _vp, _i64, _vp, _vp, ctypes.c_size_t, _vp]
+        L.ssm_tokens_pack8.argtypes = [_vp, _vp]
+        L.ssm_tokens_mm8.argtypes = [_vp, _vp]
         L.ssm_status_string.restype = ctypes.c_char_p
         L.ssm_status_string.argtypes = [ctypes.c_int]
         L.ssm_last_error_detail.restype = ctypes.c_char_p
@@ -710,6 +767,14 @@ _FOUR_PTRS = struct.Struct("@PPPP")               # ConvFwdOut, ConvGrads
 _CKPT8_ARGS = struct.Struct("@i4xqqqP")           # Ckpt8Args
 _TOKENS_CONV_ARGS = struct.Struct("@iiqqqqqPPPPPPPPqqq")            # TokensConvArgs
 _TOKENS_SCAN_ARGS = struct.Struct("@iiqqqqqPPPPPPPPPPPPPqqqqqqq")   # TokensScanArgs
+_GATED_ARGS = struct.Struct("@ifqqqPPPPPPPqqqqqq")                  # GatedArgs
+_GATED_IO = struct.Struct("@PPPqq")                                 # GatedFwdOut, GatedBwdIn
+_GATED_GRADS = struct.Struct("@PPPPPPPqqqqqq")                      # GatedGrads
+_TOKENS_GATED_ARGS = struct.Struct("@ifqqqqPPPPPPPPPPPqqqqq")       # TokensGatedArgs
+_GROUP_NORM_ARGS = struct.Struct("@iiqqqPPPPqqf4x")                 # GroupNormArgs
+_GROUP_NORM_GRADS = struct.Struct("@PPPPqq")                        # GroupNormGrads
+_TOKENS_PACK8_ARGS = struct.Struct("@i4xqqPPPqq")                   # TokensPack8Args
+_TOKENS_MM8_ARGS = struct.Struct("@i4xqqqPPPPPPqqq")                # TokensMm8Args
 
 
 def _stream_code(dtype, name):
@@ -992,7 +1057,7 @@ def _rows(t, name, dtype, T, D, dev):
         r, c = t.shape
         if r == T and c == D:
             s0, s1 = t.stride()
-            if s1 == 1 or D <= 1:
+            if s1 == 1 or D <= 1 or T == 0:
                 return t.data_ptr(), s0
     if t is None:
         raise ValueError(f"{name} is required")
@@ -1123,4 +1188,265 @@ def tokens_scan(*, delta, x, A, Bm, C, skip=None, z=None, delta_bias=None, delta
     nws = _tokens_scan_bytes(T, D, N) if seq_start is not None else 0
     ws, wp = _scratch(nws, dev)
     _launch(dev, lib().ssm_tokens_scan, args, wp, nws)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# gated linear recurrence
+# ---------------------------------------------------------------------------
+def _stream_of(t, name, dtype, shape, dev):
+    """A (B, D, L) stream: (address, batch stride, channel stride); steps contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and (shape[2] <= 1 or t.stride(2) == 1 or t.is_contiguous())):
+        if t is None:
+            raise ValueError(f"{name} is required")
+        _need(t, name, dtype, shape, dev, view=True)
+    s = t.stride()
+    return t.data_ptr(), s[0], s[1]
+
+
+def _out_stream(out, key, want, dtype, shape, dev):
+    """out[key], or a new stream where it is wanted; (0, 0, 0) for none."""
+    if out.get(key) is None:
+        if not want:
+            return 0, 0, 0
+        return _new(out, key, dtype, shape, dev), shape[1] * shape[2], shape[2]
+    t = _out(out, key, shape, dtype, dev, view=True)
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _gated_args(x, r, i, lam, r_bias, i_bias, power, h0, st):
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("x must be a torch.Tensor")
+    if x.dim() != 3:
+        raise ValueError(f"x has shape {tuple(x.shape)}; expected (B, D, L)")
+    if st is not None and x.dtype is not st:
+        raise TypeError(f"x has dtype {x.dtype}, expected {st}")
+    st, dev, shape = x.dtype, x.device, x.shape
+    code = _stream_code(st, "x")
+    Bsz, D, L = shape
+    xp, *sx = _stream_of(x, "x", st, shape, dev)
+    rp, *sr = _stream_of(r, "r", st, shape, dev)
+    ip, *si = _stream_of(i, "i", st, shape, dev)
+    if lam is None:
+        raise ValueError("lam is required")
+    lp, rb, ib = (_dense(t, n, _F32, (D,), dev) for t, n in ((lam, "lam"), (r_bias, "r_bias"), (i_bias, "i_bias")))
+    hp = _dense(h0, "h0", _F32, (Bsz, D), dev)
+    return _GATED_ARGS.pack(code, power, Bsz, D, L, xp, rp, ip, lp, rb, ib, hp, *sx, *sr, *si), shape, st, dev
+
+
+def gated_fwd(*, x, r, i, lam, r_bias=None, i_bias=None, power=8.0, h0=None, want_y=True, want_h_last=False,
+              want_ckpt=False, out=None):
+    """Gated linear recurrence, h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t + i_bias) x_t with
+    a_t = exp(-power * softplus(lam) * sigmoid(r_t + r_bias)) and y = h.
+
+    ``x``, ``r``, ``i`` (B, D, L) float32 or bfloat16, any batch and channel stride; ``lam``, ``r_bias``, ``i_bias``
+    (D,) and ``h0`` (B, D) float32.  Returns a dict with y, h_last (B, D) and ckpt (B, D, ceil(L / 128)), the states
+    that ``gated_bwd`` begins from, those requested."""
+    args, shape, st, dev = _gated_args(x, r, i, lam, r_bias, i_bias, power, h0, None)
+    Bsz, D, L = shape
+    out = dict(out) if out else {}
+    y = _out_stream(out, "y", want_y, st, shape, dev)
+    last = ckpt = 0
+    if want_h_last or out.get("h_last") is not None:
+        last = _new(out, "h_last", _F32, (Bsz, D), dev)
+    if want_ckpt or out.get("ckpt") is not None:
+        ckpt = _new(out, "ckpt", _F32, (Bsz, D, n_chunks(L, SSM_GATED_CHUNK)), dev)
+    _launch(dev, lib().ssm_gated_fwd, args, _GATED_IO.pack(y[0], last, ckpt, *y[1:]))
+    return out
+
+
+_GATED_GRADS_OF = ("gx", "gr", "gi", "glam", "gr_bias", "gi_bias", "gh0")
+
+
+@functools.lru_cache(maxsize=1024)
+def _gated_bwd_bytes(Bsz, D, L):
+    args = GatedArgs(dtype=SSM_F32, power=1.0, batch=Bsz, channels=D, length=L)   # sizes only
+    for s in (args.x_stride, args.r_stride, args.i_stride):
+        s[0], s[1] = D * L, L
+    n = ctypes.c_size_t(0)
+    _check(lib().ssm_workspace_bytes(SSM_OP_GATED_BWD, ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def gated_bwd(*, gy, x, r, i, lam, r_bias=None, i_bias=None, power=8.0, h0=None, gh_last=None, ckpt=None,
+              want=_GATED_GRADS_OF, out=None):
+    """Gradients of <gy, y> + <gh_last, h_last> of ``gated_fwd``; without ``ckpt`` its states are formed again first.
+    Returns a dict of the gradients named in ``want``; those of biases that were not given are of biases of 0."""
+    if not isinstance(gy, torch.Tensor):
+        raise ValueError("gy must be a torch.Tensor")
+    args, shape, st, dev = _gated_args(x, r, i, lam, r_bias, i_bias, power, h0, gy.dtype)
+    Bsz, D, L = shape
+    g, *sg = _stream_of(gy, "gy", st, shape, dev)
+    lp = _dense(gh_last, "gh_last", _F32, (Bsz, D), dev)
+    cp = _dense(ckpt, "ckpt", _F32, (Bsz, D, n_chunks(L, SSM_GATED_CHUNK)), dev)
+    out, want = dict(out) if out else {}, tuple(want)
+    for k in (*want, *out):
+        if k not in _GATED_GRADS_OF:
+            raise ValueError(f"unknown gradient {k}")
+    streams = [_out_stream(out, k, k in want, st, shape, dev) for k in _GATED_GRADS_OF[:3]]
+    par = [_new(out, k, _F32, (Bsz, D) if k == "gh0" else (D,), dev) if k in want or out.get(k) is not None else 0
+           for k in _GATED_GRADS_OF[3:]]
+    if dev.type != "cuda":
+        _on_gpu(dev)
+    nws = _gated_bwd_bytes(Bsz, D, L)
+    ws, wp = _scratch(nws, dev)
+    _launch(dev, lib().ssm_gated_bwd, args, _GATED_IO.pack(g, lp, cp, *sg),
+            _GATED_GRADS.pack(*(s[0] for s in streams), *par, *(v for s in streams for v in s[1:])), wp, nws)
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _tokens_gated_bytes(T, D):
+    # sizes only: the sequences do not change what the ranges of rows need
+    args = TokensGatedArgs(dtype=SSM_F32, power=1.0, tokens=T, channels=D, sequences=1, slots=1, seq_start=256,
+                           x_stride=D, r_stride=D, i_stride=D, y_stride=D, pool_stride=D)
+    n = ctypes.c_size_t(0)
+    _check(lib().ssm_workspace_bytes(SSM_OP_TOKENS_GATED, ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def tokens_gated(*, x, r, i, lam, r_bias=None, i_bias=None, power=8.0, pool, seq_start=None, slot=None, fresh=None,
+                 out=None):
+    """The recurrence of ``gated_fwd`` over the packed rows of a batch of sequences.
+
+    ``x``, ``r``, ``i`` (T, D) may be slices of wider rows; ``pool`` (slots, D) float32 holds the states, in place;
+    ``seq_start``, ``slot`` and ``fresh`` as in ``tokens_conv``.  Returns a dict with y (T, D)."""
+    T, D, st, code, dev = _row_input(x)
+    xp, sx = _rows(x, "x", st, T, D, dev)
+    rp, sr = _rows(r, "r", st, T, D, dev)
+    ip, si = _rows(i, "i", st, T, D, dev)
+    if lam is None:
+        raise ValueError("lam is required")
+    lp, rb, ib = (_dense(t, n, _F32, (D,), dev) for t, n in ((lam, "lam"), (r_bias, "r_bias"), (i_bias, "i_bias")))
+    if not isinstance(pool, torch.Tensor) or pool.dim() != 2 or pool.shape[1] != D:
+        raise ValueError(f"pool must be (slots, {D})")
+    S, slots, spool, start, sl, fr = _sequences(T, pool.unsqueeze(2), (D, 1), _F32, dev, seq_start, slot, fresh)
+    out = dict(out) if out else {}
+    yp, sy = _y_rows(out, st, T, D, dev)
+    args = _TOKENS_GATED_ARGS.pack(code, power, T, D, S, slots, xp, rp, ip, lp, rb, ib, start, sl, fr, pool.data_ptr(),
+                                   yp, sx, sr, si, sy, spool)
+    if dev.type != "cuda":
+        _on_gpu(dev)
+    nws = _tokens_gated_bytes(T, D) if seq_start is not None else 0
+    ws, wp = _scratch(nws, dev)
+    _launch(dev, lib().ssm_tokens_gated, args, wp, nws)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# group norm of rows
+# ---------------------------------------------------------------------------
+def _norm_args(x, groups, w, bias, eps, silu, z, st):
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("x must be a torch.Tensor")
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}; expected (T, C)")
+    T, C = x.shape
+    if st is not None and x.dtype is not st:
+        raise TypeError(f"x has dtype {x.dtype}, expected {st}")
+    st, dev = x.dtype, x.device
+    code = _stream_code(st, "x")
+    xp, sx = _rows(x, "x", st, T, C, dev)
+    zp, sz = _rows(z, "z", st, T, C, dev) if z is not None else (0, 0)
+    wp = _dense(w, "w", _F32, (C,), dev)
+    bp = _dense(bias, "bias", _F32, (C,), dev)
+    return _GROUP_NORM_ARGS.pack(code, 1 if silu else 0, T, C, groups, xp, zp, wp, bp, sx, sz, eps), T, C, st, dev
+
+
+def _out_rows(out, key, want, dtype, T, C, dev):
+    """out[key], or new rows where they are wanted: (address, row stride); (0, 0) for none."""
+    t = out.get(key)
+    if t is None:
+        return (_new(out, key, dtype, (T, C), dev), C) if want else (0, 0)
+    p, s = _rows(t, f"out[{key!r}]", dtype, T, C, dev)
+    if T > 1 and s < C:
+        raise ValueError(f"out[{key!r}]: an output view needs distinct elements (no stride 0)")
+    return p, s
+
+
+def group_norm_fwd(*, x, groups, w=None, bias=None, eps=1e-5, silu=False, z=None, out=None):
+    """Group norm of the rows x (T, C), channels last: y = act((x - mean) / sqrt(var + eps) * w + bias), times
+    z * sigmoid(z) with a gate ``z`` (T, C); act is the identity, or with ``silu`` v * sigmoid(v).
+
+    The statistics are those of one group (C / groups consecutive channels) of one row.  ``x`` and ``z`` may be slices
+    of wider rows; ``w``, ``bias`` (C,) float32.  Returns a dict with y (T, C)."""
+    args, T, C, st, dev = _norm_args(x, groups, w, bias, eps, silu, z, None)
+    out = dict(out) if out else {}
+    yp, sy = _y_rows(out, st, T, C, dev)
+    _launch(dev, lib().ssm_group_norm_fwd, args, yp, sy)
+    return out
+
+
+_NORM_GRADS = ("gx", "gz", "gw", "gbias")
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_bwd_bytes(code, T, C, groups):
+    args = GroupNormArgs(dtype=code, rows=T, channels=C, groups=groups, x_stride=C)   # sizes only
+    n = ctypes.c_size_t(0)
+    _check(lib().ssm_workspace_bytes(SSM_OP_GROUP_NORM_BWD, ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def group_norm_bwd(*, gy, x, groups, w=None, bias=None, eps=1e-5, silu=False, z=None, want=None, out=None):
+    """Gradients of <gy, y> of ``group_norm_fwd``: a dict of those named in ``want`` (by default gx, gw, gbias, and gz
+    with a gate); the statistics are formed again from x."""
+    if not isinstance(gy, torch.Tensor):
+        raise ValueError("gy must be a torch.Tensor")
+    args, T, C, st, dev = _norm_args(x, groups, w, bias, eps, silu, z, gy.dtype)
+    gp, sg = _rows(gy, "gy", st, T, C, dev)
+    out = dict(out) if out else {}
+    want = tuple(want) if want is not None else _NORM_GRADS if z is not None else ("gx", "gw", "gbias")
+    for k in (*want, *out):
+        if k not in _NORM_GRADS:
+            raise ValueError(f"unknown gradient {k}")
+    gx, sgx = _out_rows(out, "gx", "gx" in want, st, T, C, dev)
+    gz, sgz = _out_rows(out, "gz", "gz" in want, st, T, C, dev)
+    gw, gb = (_new(out, k, _F32, (C,), dev) if k in want or out.get(k) is not None else 0 for k in ("gw", "gbias"))
+    if dev.type != "cuda":
+        _on_gpu(dev)
+    nws = _norm_bwd_bytes(_STREAM[st], T, C, groups)
+    ws, wp = _scratch(nws, dev)
+    _launch(dev, lib().ssm_group_norm_bwd, args, gp, sg, _GROUP_NORM_GRADS.pack(gx, gz, gw, gb, sgx, sgz), wp, nws)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# products in 8-bit integers
+# ---------------------------------------------------------------------------
+def tokens_pack8(x, *, out=None):
+    """The rows x (T, K) in 8 bits: a dict with x8 (T, K) int8 and x8_scale (T,) float32, one scale a row."""
+    T, K, st, code, dev = _row_input(x)
+    xp, sx = _rows(x, "x", st, T, K, dev)
+    out = dict(out) if out else {}
+    qp, sq = _out_rows(out, "x8", True, torch.int8, T, K, dev)
+    sp = _new(out, "x8_scale", _F32, (T,), dev)
+    _launch(dev, lib().ssm_tokens_pack8, _TOKENS_PACK8_ARGS.pack(code, T, K, xp, qp, sp, sx, sq))
+    return out
+
+
+def tokens_mm8(*, x8, x8_scale, w8, w8_scale, bias=None, dtype=torch.bfloat16, out=None):
+    """The product of rows in 8 bits with weights in 8 bits, y = (x8 @ w8.T) * x8_scale[:, None] * w8_scale + bias.
+
+    ``x8`` (T, K) int8 with ``x8_scale`` (T,), as ``tokens_pack8`` makes them; ``w8`` (N, K) int8 with ``w8_scale`` (N,);
+    ``bias`` (N,) float32.  The sums are exact.  Returns a dict with y (T, N) of ``dtype`` (float32 or bfloat16)."""
+    for t, name in ((x8, "x8"), (w8, "w8")):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a torch.Tensor")
+        if t.dim() != 2:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}; expected two dimensions")
+    T, K = x8.shape
+    N, dev = w8.shape[0], x8.device
+    code = _stream_code(dtype, "dtype")
+    xp, sx = _rows(x8, "x8", torch.int8, T, K, dev)
+    wp, sw = _rows(w8, "w8", torch.int8, N, K, dev)
+    if x8_scale is None or w8_scale is None:
+        raise ValueError("x8_scale and w8_scale are required")
+    xs = _dense(x8_scale, "x8_scale", _F32, (T,), dev)
+    ws = _dense(w8_scale, "w8_scale", _F32, (N,), dev)
+    bp = _dense(bias, "bias", _F32, (N,), dev)
+    out = dict(out) if out else {}
+    yp, sy = _y_rows(out, dtype, T, N, dev)
+    _launch(dev, lib().ssm_tokens_mm8, _TOKENS_MM8_ARGS.pack(code, T, K, N, xp, xs, wp, ws, bp, yp, sx, sw, sy))
     return out

@@ -1018,6 +1018,7 @@ int sens_rows_impl(const ssm_scan_args* a, int64_t t0, int32_t rows, void* s, vo
 
 #include "api_modes.inc"
 #include "api_layer.inc"
+#include "api_gated.inc"
 
 // ===========================================================================
 // allocation-free forward (ssm_scan_fwd_noalloc): the scratch memory the
@@ -1093,6 +1094,13 @@ int ssm_workspace_bytes(int op, const void* args, size_t* out_bytes) {
         case SSM_OP_TOKENS_CONV: return tokens_conv_impl((const ssm_tokens_conv_args*)args, nullptr, out_bytes);
         case SSM_OP_TOKENS_SCAN:
             return tokens_scan_impl((const ssm_tokens_scan_args*)args, nullptr, 0, nullptr, out_bytes);
+        case SSM_OP_GATED_FWD: return gated_fwd_impl((const ssm_gated_args*)args, nullptr, nullptr, out_bytes);
+        case SSM_OP_GATED_BWD:
+            return gated_bwd_impl((const ssm_gated_args*)args, nullptr, nullptr, nullptr, 0, nullptr, out_bytes);
+        case SSM_OP_TOKENS_GATED:
+            return tokens_gated_impl((const ssm_tokens_gated_args*)args, nullptr, 0, nullptr, out_bytes);
+        case SSM_OP_GROUP_NORM_BWD:
+            return norm_bwd_impl((const ssm_group_norm_args*)args, nullptr, 0, nullptr, nullptr, 0, nullptr, out_bytes);
         default: return fail(SSM_ERR_UNSUPPORTED, "unknown op %d", op);
     }
 }
@@ -1158,6 +1166,29 @@ int ssm_tokens_conv(const ssm_tokens_conv_args* args, void* stream) {
 }
 int ssm_tokens_scan(const ssm_tokens_scan_args* args, void* ws, size_t ws_bytes, void* stream) {
     return tokens_scan_impl(args, ws, ws_bytes, (hipStream_t)stream, nullptr);
+}
+int ssm_gated_fwd(const ssm_gated_args* args, const ssm_gated_fwd_out* out, void* stream) {
+    return gated_fwd_impl(args, out, (hipStream_t)stream, nullptr);
+}
+int ssm_gated_bwd(const ssm_gated_args* args, const ssm_gated_bwd_in* in, const ssm_gated_grads* grads, void* ws,
+                  size_t ws_bytes, void* stream) {
+    return gated_bwd_impl(args, in, grads, ws, ws_bytes, (hipStream_t)stream, nullptr);
+}
+int ssm_tokens_gated(const ssm_tokens_gated_args* args, void* ws, size_t ws_bytes, void* stream) {
+    return tokens_gated_impl(args, ws, ws_bytes, (hipStream_t)stream, nullptr);
+}
+int ssm_group_norm_fwd(const ssm_group_norm_args* args, void* y, int64_t y_stride, void* stream) {
+    return norm_fwd_impl(args, y, y_stride, (hipStream_t)stream);
+}
+int ssm_group_norm_bwd(const ssm_group_norm_args* args, const void* gy, int64_t gy_stride,
+                       const ssm_group_norm_grads* grads, void* ws, size_t ws_bytes, void* stream) {
+    return norm_bwd_impl(args, gy, gy_stride, grads, ws, ws_bytes, (hipStream_t)stream, nullptr);
+}
+int ssm_tokens_pack8(const ssm_tokens_pack8_args* args, void* stream) {
+    return pack8_impl(args, (hipStream_t)stream);
+}
+int ssm_tokens_mm8(const ssm_tokens_mm8_args* args, void* stream) {
+    return mm8_impl(args, (hipStream_t)stream);
 }
 
 int ssm_profile_begin(int max_launches) {

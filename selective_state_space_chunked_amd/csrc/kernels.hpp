@@ -342,4 +342,71 @@ hipError_t launch_tok_scan(const TokScanParams& p, int dtype, bool sum, hipStrea
 hipError_t launch_tok_join(const TokScanParams& p, hipStream_t st);
 hipError_t launch_tok_step(const TokScanParams& p, int dtype, hipStream_t st);
 
+// ------------------------- gated linear recurrence --------------------------
+constexpr int kGatedChunk = 128;   // steps between the states kept for the backward: 16 lanes of eight
+struct GatedParams {
+    const void *x, *r, *i; const float *lam, *rb, *ib, *h0;
+    const void* gy; const float* gh_last; const float* ckpt;
+    void* y; float *h_last, *ckpt_out;                  // forward outputs
+    void *gx, *gr, *gi; float *glam, *grb, *gib, *gh0;  // backward outputs
+    float* part;                                        // (3, B, D) sums of the rows; written where `sums`
+    int64_t sx[2], sr[2], si[2], sy[2], sgy[2], sgx[2], sgr[2], sgi[2];   // batch, channel strides (steps contiguous)
+    float power;
+    int B, D, L, nchunk, lanes, sums;   // lanes of a row: 16, 64, 256 or 1024
+};
+// waves the lanes of a row are chosen for: four on each of the 1024 SIMDs
+constexpr int kGatedWaves = 4096;
+hipError_t launch_gated(const GatedParams& p, bool bwd, int dtype, hipStream_t st);
+hipError_t launch_gated_sum(const GatedParams& p, hipStream_t st);   // glam, grb, gib from part
+struct TokGatedParams {
+    const void *x, *r, *i; const float *lam, *rb, *ib;
+    float* pool; void* y;
+    Sequences q;
+    int64_t sx, sr, si, sy, spool;
+    float power;
+    int D;
+    // prompts: ranges of `rows` rows (the last may be shorter); workspace, per range and channel
+    int rows, nrange, joined;
+    float *h0, *hsum, *dsum;         // of the sequence that crosses a range's end: its first state if it begins there, its
+                                     // state at the end of the range, and the sum of its q in the range
+    int* through;                    // (nrange - 1) whether it runs through the whole range
+};
+constexpr int kTokGatedWaves = 4096;   // waves the ranges are made for
+hipError_t launch_tok_gated(const TokGatedParams& p, int dtype, bool sum, hipStream_t st);
+hipError_t launch_tok_gated_join(const TokGatedParams& p, hipStream_t st);
+hipError_t launch_tok_gated_step(const TokGatedParams& p, int dtype, hipStream_t st);
+
+// ------------------------------- group norm ---------------------------------
+struct NormParams {
+    const void *x, *z, *gy; const float *w, *bias;
+    void *y, *gx, *gz; float *gw, *gbias;
+    float* part;                     // (chunks, 2, C) sums of gw and gbias; written where `sums`
+    int64_t sx, sz, sgy, sy, sgx, sgz;
+    float eps, inv;                  // inv = 1 / Cg
+    int T, C, G, Cg, silu, sums;
+    int team, V, R, P;               // lanes of a team, channels of a vector, vectors of a lane, lanes of a group
+    int gblocks, chunks, per;        // teams' groups of a row; runs of `per` rows
+};
+constexpr int kNormMost = 8192;   // channels of a group: 1024 lanes of eight
+constexpr int kNormWG = 1024;     // workgroups the rows are divided over
+hipError_t launch_norm_fwd(const NormParams& p, int dtype, hipStream_t st);
+hipError_t launch_norm_bwd(const NormParams& p, int dtype, hipStream_t st);
+hipError_t launch_norm_sum(const NormParams& p, hipStream_t st);
+
+// ---------------------- products in 8-bit integers --------------------------
+struct Pack8Params {
+    const void* x; int8_t* o; float* scale;
+    int64_t sx, so;
+    int T, K;
+};
+struct Mm8Params {
+    const int8_t *x, *w; const float *xs, *ws, *bias;
+    void* y;
+    int64_t sx, sw, sy;
+    int T, K, N;
+    int tile;                        // side of a workgroup's tile, 0: the kernel for few rows
+};
+hipError_t launch_pack8(const Pack8Params& p, int dtype, hipStream_t st);
+hipError_t launch_mm8(const Mm8Params& p, int dtype, hipStream_t st);
+
 }  // namespace ssm

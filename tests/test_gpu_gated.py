@@ -1,0 +1,530 @@
+"""The gated linear recurrence (streams and packed rows), the group norm and the products in 8-bit integers on the GPU,
+against float64 references with bounds derived from the arithmetic (tests/_gated_ref.py)."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_chunked_amd as ssm
+
+from . import _gated_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+GATED_OUT = ("glam", "gr_bias", "gi_bias", "gh0", "h_last")   # float32 whatever the streams
+
+
+def gen(seed):
+    return np.random.default_rng(seed)
+
+
+def dev(a, dtype="f32"):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).to(DT[dtype]).to(DEV)
+
+
+def f64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+# ---------------------------------------------------------------------------
+# gated recurrence over streams
+# ---------------------------------------------------------------------------
+def gated_inputs(B, D, L, dtype, r, state=True, bias=True, spread=1.0):
+    t = {k: dev(spread * r.normal(size=(B, D, L)), dtype) for k in ("x", "r", "i")}
+    t["lam"] = dev(np.log(np.expm1(-np.log(r.uniform(0.9, 0.999, D)))))
+    t["r_bias"], t["i_bias"] = (dev(0.5 * r.normal(size=D)) if bias else None for _ in range(2))
+    t["h0"] = dev(r.normal(size=(B, D))) if state else None
+    gy = dev(r.normal(size=(B, D, L)), dtype)
+    return t, gy, dev(r.normal(size=(B, D))) if state else None
+
+
+def arrays(t):
+    return [f64(t[k]) for k in ("x", "r", "i", "lam", "r_bias", "i_bias")]
+
+
+def gated_check(t, gy, gl, dtype, power=8.0):
+    f = ssm.gated_fwd(want_h_last=True, want_ckpt=True, power=power, **t)
+    for k, (ref, err) in R.gated_fwd(*arrays(t), power, f64(t["h0"])).items():
+        R.check(k, f[k], ref, err, "f32" if k in GATED_OUT else dtype)
+    g = ssm.gated_bwd(gy=gy, gh_last=gl, ckpt=f["ckpt"], power=power, **t)
+    assert set(g) == {"gx", "gr", "gi", "glam", "gr_bias", "gi_bias", "gh0"}
+    for k, (ref, err) in R.gated_bwd(*arrays(t), power, f64(t["h0"]), f64(gy), f64(gl)).items():
+        R.check(k, g[k], ref, err, "f32" if k in GATED_OUT else dtype)
+    return f, g
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,D,L", [(1, 1, 1), (2, 3, 2), (3, 5, 7), (1, 17, 8), (2, 9, 9), (1, 4, 127), (2, 33, 128),
+                                   (1, 3, 129), (2, 5, 512), (1, 6, 513), (3, 2, 1000), (1, 2, 2048), (2, 3, 2057),
+                                   (1, 2, 8192), (1, 3, 9001), (1, 1, 20011)])
+def test_gated(B, D, L, dtype):
+    t, gy, gl = gated_inputs(B, D, L, dtype, gen(B + D + L), state=L % 2 == 1, bias=L % 3 != 0)
+    gated_check(t, gy, gl, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,D,L", [(8, 2051, 299), (5, 900, 700), (3, 350, 2500), (3, 350, 130)])
+def test_gated_many_rows(B, D, L, dtype):
+    """Rows enough that 16, 64 and 256 lanes share one, over several tiles."""
+    t, gy, gl = gated_inputs(B, D, L, dtype, gen(7))
+    gated_check(t, gy, gl, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gated_views_and_outputs(dtype):
+    """Streams that are slices and broadcasts, outputs in slices of wider buffers; what lies around them stays."""
+    r = gen(3)
+    B, D, L = 3, 5, 301
+    t, gy, gl = gated_inputs(B, D, L, dtype, r)
+    wide = {k: dev(r.normal(size=(B, D + 1, L + 9)), dtype) for k in ("x", "i", "gy")}
+    t["x"], t["i"], gy = wide["x"][:, 1:, 3:3 + L], wide["i"][:, :D, 1:1 + L], wide["gy"][:, 1:, 8:8 + L]
+    t["r"] = dev(r.normal(size=(B, 1, L)), dtype).expand(B, D, L)
+    ref = R.gated_fwd(*arrays(t), 8.0, f64(t["h0"]))
+    back = R.gated_bwd(*arrays(t), 8.0, f64(t["h0"]), f64(gy), f64(gl))
+    bufs = {k: torch.full((D, B + 1, L + 7), 7.0, dtype=DT[dtype], device=DEV) for k in ("y", "gx", "gr", "gi")}
+    outs = {k: b[:, :B, 2:2 + L].transpose(0, 1) for k, b in bufs.items()}   # channels outside the batch
+    f = ssm.gated_fwd(want_ckpt=True, out={"y": outs["y"]}, **t)
+    assert f["y"] is outs["y"]
+    R.check("y", f["y"], *ref["y"], dtype)
+    g = ssm.gated_bwd(gy=gy, gh_last=gl, ckpt=f["ckpt"], out={k: outs[k] for k in ("gx", "gr", "gi")}, **t)
+    for k, v in back.items():
+        R.check(k, g[k], *v, "f32" if k in GATED_OUT else dtype)
+    for b in bufs.values():
+        assert (b[:, B] == 7).all() and (b[:, :, :2] == 7).all() and (b[:, :, 2 + L:] == 7).all()
+
+
+def test_gated_states_again_and_determinism():
+    """Without the states the backward forms them again: the same bits.  Each wanted output alone: the same bits too."""
+    t, gy, gl = gated_inputs(2, 33, 1300, "bf16", gen(4))
+    f = ssm.gated_fwd(want_h_last=True, want_ckpt=True, **t)
+    par = dict(gy=gy, gh_last=gl, **t)
+    g, again = ssm.gated_bwd(ckpt=f["ckpt"], **par), ssm.gated_bwd(**par)
+    for k in g:
+        assert torch.equal(g[k], again[k]), k
+        one = ssm.gated_bwd(ckpt=f["ckpt"], want=(k,), **par)
+        assert list(one) == [k] and torch.equal(one[k], g[k]), k
+    for k in ("y", "h_last", "ckpt"):
+        one = ssm.gated_fwd(**t, want_y=k == "y", want_h_last=k == "h_last", want_ckpt=k == "ckpt")
+        assert list(one) == [k] and torch.equal(one[k], f[k]), k
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gated_segments(dtype):
+    """A stream in two calls, the state handed on: forward, and the gradients of the first with gh_last from the second."""
+    t, gy, _ = gated_inputs(2, 7, 700, dtype, gen(5))
+    whole = R.gated_bwd(*arrays(t), 8.0, f64(t["h0"]), f64(gy), None)
+    y = R.gated_fwd(*arrays(t), 8.0, f64(t["h0"]))["y"]
+    cut = 333
+    part = [{**t, **{k: t[k][..., s] for k in ("x", "r", "i")}} for s in (slice(0, cut), slice(cut, None))]
+    a = ssm.gated_fwd(want_h_last=True, want_ckpt=True, **part[0])
+    part[1]["h0"] = a["h_last"]
+    b = ssm.gated_fwd(want_ckpt=True, **part[1])
+    R.check("y", torch.cat([a["y"], b["y"]], -1), y[0], 2 * y[1], dtype)
+    gb = ssm.gated_bwd(gy=gy[..., cut:], ckpt=b["ckpt"], **part[1])
+    ga = ssm.gated_bwd(gy=gy[..., :cut], gh_last=gb["gh0"], ckpt=a["ckpt"], **part[0])
+    for k in ("gx", "gr", "gi"):
+        R.check(k, torch.cat([ga[k], gb[k]], -1), whole[k][0], 2 * whole[k][1], dtype)
+    for k in ("glam", "gr_bias", "gi_bias"):
+        R.check(k, ga[k] + gb[k], whole[k][0], 2 * whole[k][1] + R.U * np.abs(f64(ga[k])), "f32")
+    R.check("gh0", ga["gh0"], whole["gh0"][0], 2 * whole["gh0"][1], "f32")
+
+
+def test_gated_gradient_by_differences():
+    """Directional differences of the loss in float64, formed by the reference's forward alone."""
+    r = gen(6)
+    t, gy, gl = gated_inputs(2, 4, 150, "f32", r)
+    g = ssm.gated_bwd(gy=gy, gh_last=gl, **t)
+    names = {"gx": "x", "gr": "r", "gi": "i", "glam": "lam", "gr_bias": "r_bias", "gi_bias": "i_bias", "gh0": "h0"}
+    base = {k: f64(v) for k, v in t.items()}
+
+    def loss(v):
+        f = R.gated_fwd(*(v[k] for k in ("x", "r", "i", "lam", "r_bias", "i_bias")), 8.0, v["h0"])
+        return (f64(gy) * f["y"][0]).sum() + (f64(gl) * f["h_last"][0]).sum()
+
+    for k, n in names.items():
+        d = r.normal(size=base[n].shape)
+        eps = 1e-5
+        num = (loss({**base, n: base[n] + eps * d}) - loss({**base, n: base[n] - eps * d})) / (2 * eps)
+        want = (f64(g[k]) * d).sum()
+        # a central difference is off by about eps^2 times the third derivative, the gradient by fp32's errors
+        assert abs(num - want) <= 1e-4 * np.linalg.norm(f64(g[k])) * np.linalg.norm(d), k
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gated_extremes(dtype):
+    """Gates that are shut and wide open, slow and fast channels: finite, and the formula's values."""
+    r = gen(8)
+    B, D, L = 2, 6, 400
+    t, gy, gl = gated_inputs(B, D, L, dtype, r, spread=4.0)
+    t["r"][0, :, 50:60] = -80.0
+    t["r"][1, :, 100:] = 30.0
+    t["i"][0, :, 200:] = -60.0
+    t["i"][1, :, :50] = 25.0
+    t["lam"] = dev(np.array([-30.0, -12.0, -3.0, 0.0, 3.0, 25.0]))
+    for power in (0.25, 8.0, 64.0):
+        f, g = gated_check(t, gy, gl, dtype, power)
+        assert all(torch.isfinite(v).all() for v in (*f.values(), *g.values()))
+    # a gate below the exponential's range is shut: the state stays as it is, and nothing becomes NaN
+    t["r"][:] = -200.0
+    t["x"][:] = 1e30
+    f = ssm.gated_fwd(want_h_last=True, want_ckpt=True, **t)
+    assert torch.equal(f["h_last"], t["h0"])
+    g = ssm.gated_bwd(gy=gy, gh_last=gl, ckpt=f["ckpt"], **t)
+    for k in ("gx", "gr", "gi", "glam", "gr_bias", "gi_bias"):
+        assert (g[k] == 0).all(), k
+
+
+def test_gated_non_finite_values_stay_in_their_row():
+    """A NaN or an infinity reaches the later steps of its row (and, backward, the earlier ones), no other row."""
+    t, gy, gl = gated_inputs(2, 5, 300, "f32", gen(9))
+    ref = ssm.gated_fwd(want_ckpt=True, **t)
+    rg = ssm.gated_bwd(gy=gy, gh_last=gl, ckpt=ref["ckpt"], **t)
+    for name, v in (("x", float("nan")), ("r", float("nan")), ("i", float("nan")), ("x", float("inf"))):
+        u = {**t, name: t[name].clone()}
+        u[name][1, 2, 297] = v
+        f = ssm.gated_fwd(want_ckpt=True, want_h_last=True, **u)
+        assert torch.equal(f["y"][1, 2, :297], ref["y"][1, 2, :297])
+        assert not torch.isfinite(f["y"][1, 2, 297:]).any() and not torch.isfinite(f["h_last"][1, 2])
+        g = ssm.gated_bwd(gy=gy, gh_last=gl, ckpt=f["ckpt"], **u)
+        for k in ("gx", "gr", "gi"):
+            keep = torch.ones(2, 5, dtype=torch.bool, device=DEV)
+            keep[1, 2] = False
+            assert torch.equal(g[k][keep], rg[k][keep]), (name, k)
+            assert torch.isfinite(f["y"][keep]).all()
+        if name != "r":   # the decay does not depend on x and i: mu is as it was
+            assert torch.equal(g["gh0"], rg["gh0"])
+
+
+@pytest.mark.parametrize("B,D,L", [(0, 3, 5), (2, 0, 5), (2, 3, 0)])
+def test_gated_empty(B, D, L):
+    t, gy, gl = gated_inputs(B, D, L, "bf16", gen(10))
+    f = ssm.gated_fwd(want_h_last=True, want_ckpt=True, **t)
+    assert f["y"].shape == (B, D, L) and torch.equal(f["h_last"], t["h0"])
+    g = ssm.gated_bwd(gy=gy, gh_last=gl, **t)
+    assert torch.equal(g["gh0"], gl)
+    for k in ("glam", "gr_bias", "gi_bias"):
+        assert g[k].shape == (D,) and (g[k] == 0).all()
+    t["h0"] = None
+    if L == 0:
+        assert (ssm.gated_fwd(want_h_last=True, **t)["h_last"] == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# gated recurrence over packed rows
+# ---------------------------------------------------------------------------
+def rows(T, D, dtype, r, view):
+    """(T, D) values, as a slice of wider rows that do not start on a whole vector."""
+    if not view:
+        return dev(r.normal(size=(T, D)), dtype)
+    return dev(r.normal(size=(T, D + 11)), dtype)[:, 3:3 + D]
+
+
+def tok_inputs(T, D, dtype, r, view=False, bias=True):
+    t = {k: rows(T, D, dtype, r, view) for k in ("x", "r", "i")}
+    t["lam"] = dev(np.log(np.expm1(-np.log(r.uniform(0.9, 0.999, D)))))
+    t["r_bias"], t["i_bias"] = (dev(0.5 * r.normal(size=D)) if bias else None for _ in range(2))
+    return t
+
+
+def tok_reference(t, start, slot, fresh, pool, y):
+    """Sequence by sequence through the streams' reference: rows and slots, with bounds; what none owns stays."""
+    x, r, i, lam, rb, ib = arrays(t)
+    y, dy, pool, dpool = f64(y), np.zeros(y.shape), f64(pool), np.zeros(pool.shape)
+    taken = set()
+    for s in range(len(slot)):
+        a, b = start[s], start[s + 1]
+        if not 0 <= slot[s] < len(pool) or a >= b or slot[s] in taken:
+            taken.add(slot[s])
+            continue
+        taken.add(slot[s])
+        h0 = None if fresh is not None and fresh[s] else pool[slot[s]][None]
+        f = R.gated_fwd(*(v[a:b].T[None] for v in (x, r, i)), lam, rb, ib, 8.0, h0)
+        y[a:b], dy[a:b] = f["y"][0][0].T, f["y"][1][0].T
+        pool[slot[s]], dpool[slot[s]] = f["h_last"][0][0], f["h_last"][1][0]
+    return y, dy, pool, dpool
+
+
+def tok_check(t, start, slot, fresh, slots, dtype, r, step=False):
+    T, D = t["x"].shape
+    whole = dev(r.normal(size=(slots + 2, D + 5)))
+    pool = whole[1:-1, :D]
+    wide = torch.full((T + 2, D + 9), 7.0, dtype=DT[dtype], device=DEV)
+    y = wide[1:T + 1, 5:5 + D]
+    ref = tok_reference(t, start, slot, fresh, pool, y)
+    keep = whole.clone()
+    at = dict(seq_start=None if step else torch.tensor(start, dtype=torch.int32, device=DEV),
+              slot=torch.tensor(slot, dtype=torch.int32, device=DEV),
+              fresh=None if fresh is None else torch.tensor(fresh, dtype=torch.bool, device=DEV))
+    f = ssm.tokens_gated(pool=pool, out={"y": y}, **at, **t)
+    assert f["y"] is y
+    R.check("y", y, ref[0], ref[1], dtype)
+    R.check("pool", pool, ref[2], ref[3], "f32")
+    owned = ref[1].max(1) > 0
+    assert (wide[0] == 7).all() and (wide[-1] == 7).all() and (wide[:, :5] == 7).all() and (wide[:, 5 + D:] == 7).all()
+    assert (y[torch.from_numpy(~owned).to(DEV)] == 7).all()
+    assert torch.equal(whole[0], keep[0]) and torch.equal(whole[-1], keep[-1]) and torch.equal(whole[:, D:], keep[:, D:])
+    untouched = [k for k in range(slots) if not ref[3][k].any()]
+    assert torch.equal(pool[untouched], keep[1:-1, :D][untouched])
+
+
+LISTS = {
+    "one": ([0, 100], [0], None, 1),
+    "long": ([0, 1500], [1], [True], 3),
+    "ragged": ([0, 1, 40, 40, 41, 300, 333], [3, 0, 5, 2, -1, 4], [True, False, True, False, False, True], 7),
+    "gap behind": ([5, 90, 200], [1, 0], [False, True], 2),
+    "same slot": ([0, 50, 100, 150], [1, 1, 0], [False, False, True], 2),
+    "past the pool": ([0, 50, 100], [7, 1], None, 3),
+}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D,view", [(1, False), (3, True), (64, False), (258, True), (1028, False)])
+@pytest.mark.parametrize("name", LISTS)
+def test_tokens_gated(name, D, view, dtype):
+    start, slot, fresh, slots = LISTS[name]
+    r = gen(D + len(name))
+    T = start[-1] + (13 if name == "gap behind" else 0)
+    tok_check(tok_inputs(T, D, dtype, r, view, bias=D != 64), start, slot, fresh, slots, dtype, r)
+
+
+def test_tokens_gated_many_ranges():
+    """Ranges enough that a kernel of its own composes the states between them, in more than one turn of it."""
+    r = gen(12)
+    T, D = 9000, 40
+    start = [0, 17, 4000, 4000, 8990, 9000]
+    tok_check(tok_inputs(T, D, "f32", r), start, [2, 0, 4, 3, 1], [False, True, False, False, True], 5, "f32", r)
+
+
+def test_tokens_gated_thousands_of_sequences():
+    r = gen(13)
+    n = r.integers(0, 5, 1500)
+    start = [0, *np.cumsum(n)]
+    slot = r.permutation(1600)[:1500]
+    slot[r.integers(0, 1500, 60)] = -1
+    tok_check(tok_inputs(int(start[-1]), 36, "bf16", r), [int(v) for v in start], [int(v) for v in slot],
+              [bool(v) for v in r.random(1500) < 0.5], 1600, "bf16", r)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("S,D,view", [(1, 1, False), (3, 7, True), (64, 260, False), (130, 1030, True)])
+def test_tokens_gated_step(S, D, view, dtype):
+    r = gen(S + D)
+    slot = [int(v) for v in r.permutation(S + 4)[:S]]
+    if S > 2:
+        slot[1], slot[2] = -1, S + 9
+    if S > 60:
+        slot[40] = slot[7]   # the later one is an empty place
+    fresh = [bool(v) for v in r.random(S) < 0.3] if D != 7 else None
+    tok_check(tok_inputs(S, D, dtype, r, view), list(range(S + 1)), slot, fresh, S + 4, dtype, r, step=True)
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_gated_lists_that_do_not_ascend_stay_inside_the_buffers(many):
+    """seq_start, slot and fresh are not checked on the host: whatever they hold, nothing outside the rows of y and the
+    slots of the pool is written (what the rows then hold is unspecified)."""
+    r = gen(14)
+    D, T, S = 40, 300, 90 if many else 6
+    big = np.iinfo(np.int32)
+    starts = [[250, 0, 10, 290, 20, 300, 0], [500, 600, -7, 40, big.max, big.min, 299], [big.max] * 7,
+              [-3, 200, 100, 299, 298, 10, 1000], [300, 250, 200, 150, 100, 50, 0]]
+    if many:
+        starts = [r.integers(-50, 400, S + 1) for _ in range(4)] + [np.arange(S, -1, -1) * 4]
+    wide = torch.full((T + 2, D + 9), 7.0, device=DEV)
+    pool = torch.full((S + 2, D), 7.0, device=DEV)
+    t = tok_inputs(T, D, "f32", r, view=True)
+    for i, st in enumerate(starts):
+        slot = r.integers(0, S, S)
+        slot[i % S] = (big.max, big.min, S, -1)[i % 4]
+        ssm.tokens_gated(pool=pool[1:-1], out={"y": wide[1:T + 1, 4:4 + D]},
+                         seq_start=torch.tensor(np.asarray(st), dtype=torch.int32, device=DEV),
+                         slot=torch.tensor(slot, dtype=torch.int32, device=DEV),
+                         fresh=torch.tensor(r.integers(0, 256, S), dtype=torch.uint8, device=DEV), **t)
+        torch.cuda.synchronize()
+        assert (wide[0] == 7).all() and (wide[-1] == 7).all() and (wide[:, :4] == 7).all() and (wide[:, 4 + D:] == 7).all()
+        assert (pool[0] == 7).all() and (pool[-1] == 7).all()
+
+
+# ---------------------------------------------------------------------------
+# group norm
+# ---------------------------------------------------------------------------
+def norm_inputs(T, C, dtype, r, view=False, gate=True, par=True):
+    x = rows(T, C, dtype, r, view)
+    x += dev(0.5 * r.normal(size=C), dtype)
+    t = dict(x=x, z=rows(T, C, dtype, r, view) if gate else None)
+    t["w"], t["bias"] = (dev(1 + 0.3 * r.normal(size=C)), dev(0.3 * r.normal(size=C))) if par else (None, None)
+    return t, rows(T, C, dtype, r, view)
+
+
+def norm_check(t, gy, groups, dtype, silu, eps=1e-5):
+    f = ssm.group_norm_fwd(groups=groups, eps=eps, silu=silu, **t)
+    g = ssm.group_norm_bwd(gy=gy, groups=groups, eps=eps, silu=silu, **t)
+    ref = R.norm(f64(t["x"]), groups, f64(t["w"]), f64(t["bias"]), eps, silu, f64(t["z"]), f64(gy))
+    assert {**f, **g}.keys() == ref.keys()
+    for k, v in {**f, **g}.items():
+        R.check(k, v, *ref[k], "f32" if k in ("gw", "gbias") else dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,G,per", [(1, 1, 1), (3, 5, 1), (7, 1, 3), (2, 3, 8), (9, 7, 16), (33, 64, 8), (5, 3, 65), (17, 2, 64),
+                                     (4, 3, 130), (3, 1, 136), (11, 33, 40), (2, 2, 519), (3, 3, 520), (6, 1, 1024),
+                                     (3, 2, 2056), (2, 1, 2501), (5, 1, 4096), (2, 2, 8192), (2, 1, 8191), (1500, 4, 24)])
+@pytest.mark.parametrize("silu,gate", [(False, False), (True, False), (False, True), (True, True)])
+def test_norm(T, G, per, silu, gate, dtype):
+    t, gy = norm_inputs(T, G * per, dtype, gen(T + G + per), view=T % 2 == 1, gate=gate, par=G != 7)
+    norm_check(t, gy, G, dtype, silu)
+
+
+def test_norm_means_far_from_zero():
+    """Groups whose mean is many times their spread: the statistics come from the differences to it."""
+    r = gen(20)
+    t, gy = norm_inputs(40, 256, "f32", r)
+    t["x"] = t["x"] + 300.0
+    norm_check(t, gy, 4, "f32", True)
+    t["x"] = torch.full_like(t["x"], 3.0)     # no spread at all: y is the bias's
+    y = ssm.group_norm_fwd(groups=4, w=t["w"], bias=t["bias"], x=t["x"])["y"]
+    assert torch.equal(y, t["bias"].expand_as(y))
+
+
+def test_norm_outputs_and_determinism():
+    r = gen(21)
+    T, C, G = 300, 96, 3
+    t, gy = norm_inputs(T, C, "bf16", r)
+    f = ssm.group_norm_fwd(groups=G, **t)["y"]
+    g = ssm.group_norm_bwd(gy=gy, groups=G, **t)
+    bufs = {k: torch.full((T + 2, C + 7), 7.0, dtype=torch.bfloat16, device=DEV) for k in ("y", "gx", "gz")}
+    outs = {k: b[1:-1, 3:3 + C] for k, b in bufs.items()}
+    assert torch.equal(ssm.group_norm_fwd(groups=G, out={"y": outs["y"]}, **t)["y"], f)
+    h = ssm.group_norm_bwd(gy=gy, groups=G, out={k: outs[k] for k in ("gx", "gz")}, **t)
+    for k in g:
+        assert torch.equal(h[k], g[k]), k
+        one = ssm.group_norm_bwd(gy=gy, groups=G, want=(k,), **t)
+        assert list(one) == [k] and torch.equal(one[k], g[k]), k
+    for b in bufs.values():
+        assert (b[0] == 7).all() and (b[-1] == 7).all() and (b[:, :3] == 7).all() and (b[:, 3 + C:] == 7).all()
+    bad = t["x"].clone()   # a NaN stays in its group
+    bad[5, 40] = float("nan")
+    y = ssm.group_norm_fwd(groups=G, **{**t, "x": bad})["y"]
+    assert torch.isnan(y[5, 32:64]).all()
+    y[5, 32:64] = f[5, 32:64]
+    assert torch.equal(y, f)
+
+
+def test_norm_gradient_by_differences():
+    r = gen(22)
+    t, gy = norm_inputs(6, 40, "f32", r)
+    g = ssm.group_norm_bwd(gy=gy, groups=5, silu=True, **t)
+    base = {k: f64(v) for k, v in t.items()}
+
+    def loss(v):
+        return (f64(gy) * R.norm(v["x"], 5, v["w"], v["bias"], 1e-5, True, v["z"])["y"][0]).sum()
+
+    for k, n in {"gx": "x", "gz": "z", "gw": "w", "gbias": "bias"}.items():
+        d = r.normal(size=base[n].shape)
+        num = (loss({**base, n: base[n] + 1e-5 * d}) - loss({**base, n: base[n] - 1e-5 * d})) / 2e-5
+        assert abs(num - (f64(g[k]) * d).sum()) <= 1e-4 * np.linalg.norm(f64(g[k])) * np.linalg.norm(d), k
+
+
+@pytest.mark.parametrize("T,C", [(0, 12), (5, 0)])
+def test_norm_empty(T, C):
+    t, gy = norm_inputs(T, C, "bf16", gen(23))
+    assert ssm.group_norm_fwd(groups=3, **t)["y"].shape == (T, C)
+    g = ssm.group_norm_bwd(gy=gy, groups=3, **t)
+    assert g["gx"].shape == (T, C) and (g["gw"] == 0).all() and (g["gbias"] == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# products in 8-bit integers
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,K", [(1, 1), (3, 2), (5, 3), (2, 4), (7, 63), (9, 515), (4, 2048), (3, 2049), (5, 8193), (2, 20001),
+                                 (600, 64)])
+def test_pack8(T, K, dtype):
+    r = gen(T + K)
+    x = rows(T, K, dtype, r, K % 2 == 1)
+    x *= dev(np.exp(3 * r.normal(size=(T, 1))), dtype)
+    q, s = R.pack(f64(x))
+    f = ssm.tokens_pack8(x)
+    assert np.array_equal(f["x8"].cpu().numpy(), q) and np.array_equal(f["x8_scale"].cpu().numpy(), s)
+    wide = torch.full((T + 2, K + 9), 7, dtype=torch.int8, device=DEV)
+    ssm.tokens_pack8(x, out={"x8": wide[1:-1, 5:5 + K]})
+    assert torch.equal(wide[1:-1, 5:5 + K], f["x8"])
+    assert (wide[0] == 7).all() and (wide[-1] == 7).all() and (wide[:, :5] == 7).all() and (wide[:, 5 + K:] == 7).all()
+
+
+def test_pack8_special_rows():
+    x = torch.randn(8, 700, device=DEV)
+    x[0] = 0
+    x[1] = 2.0 ** -101
+    x[2, 5] = float("inf")
+    x[3, 6] = float("nan")
+    x[4, 9] = torch.finfo(torch.float32).max
+    x[5, 699] = -1e30
+    q, s = R.pack(f64(x))
+    f = ssm.tokens_pack8(x)
+    assert np.array_equal(f["x8"].cpu().numpy(), q) and np.array_equal(f["x8_scale"].cpu().numpy(), s, equal_nan=True)
+    w = torch.ones(3, 700, dtype=torch.int8, device=DEV)
+    # (in float32: the largest float is past bfloat16's)
+    y = ssm.tokens_mm8(x8=f["x8"], x8_scale=f["x8_scale"], w8=w, w8_scale=torch.ones(3, device=DEV), dtype=torch.float32)["y"]
+    assert torch.isnan(y[2:4]).all() and torch.isfinite(y[[0, 1, 4, 5, 6, 7]]).all() and (y[:2] == 0).all()
+
+
+def mm8_inputs(T, K, N, r, view=False, bias=True):
+    def bytes_(n):
+        b = torch.from_numpy(r.integers(-128, 128, (n, K + 13)).astype(np.int8)).to(DEV)
+        return b[:, 5:5 + K] if view else b[:, :K].contiguous()
+
+    return dict(x8=bytes_(T), x8_scale=dev(r.uniform(0.01, 1, T)), w8=bytes_(N), w8_scale=dev(r.uniform(0.01, 1, N)),
+                bias=dev(r.normal(size=N)) if bias else None)
+
+
+def mm8_check(t, dtype, **kw):
+    got = ssm.tokens_mm8(dtype=DT[dtype], **t, **kw)["y"]
+    v = {k: None if a is None else a.cpu().numpy() for k, a in t.items()}
+    ref, err = R.mm8(v["x8"], v["x8_scale"], v["w8"], v["w8_scale"], None if v["bias"] is None else v["bias"].astype(np.float64))
+    R.check("y", got, ref, err, dtype)
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [1, 3, 15, 16, 17, 64, 100, 127, 128, 129, 515, 1024, 1100])
+@pytest.mark.parametrize("T,N", [(1, 1), (2, 17), (16, 16), (17, 33), (40, 30), (64, 250), (65, 63), (130, 129), (300, 5)])
+def test_mm8(T, N, K, dtype):
+    r = gen(T + N + K)
+    mm8_check(mm8_inputs(T, K, N, r, view=(T + K) % 2 == 1, bias=N % 2 == 1), dtype)
+
+
+@pytest.mark.parametrize("T,K,N", [(2100, 640, 2000), (2049, 384, 4100), (1000, 200, 8200), (512, 4096, 512), (4096, 256, 264),
+                                   (70, 8192, 500), (200, 131071, 40)])
+def test_mm8_large(T, K, N):
+    mm8_check(mm8_inputs(T, K, N, gen(31)), "bf16")
+    mm8_check(mm8_inputs(T, K, N, gen(32), view=True), "f32")
+
+
+def test_mm8_largest_sums():
+    """The largest sum there is, 131071 products of (-128)^2, and its opposite."""
+    K = 131071
+    x = torch.full((70, K), -128, dtype=torch.int8, device=DEV)
+    w = torch.full((3, K), -128, dtype=torch.int8, device=DEV)
+    w[1] = 127
+    one = torch.ones(70, device=DEV)
+    for T in (1, 70):
+        y = ssm.tokens_mm8(x8=x[:T], x8_scale=one[:T], w8=w, w8_scale=one[:3], dtype=torch.float32)["y"]
+        assert torch.equal(y[:, 0], torch.full((T,), float(np.float32(K * 16384)), device=DEV))
+        assert torch.equal(y[:, 1], torch.full((T,), float(np.float32(-K * 16256)), device=DEV))
+
+
+def test_mm8_outputs_and_empty():
+    r = gen(33)
+    t = mm8_inputs(90, 200, 77, r)
+    ref = mm8_check(t, "bf16")
+    wide = torch.full((92, 90), 7.0, dtype=torch.bfloat16, device=DEV)
+    y = ssm.tokens_mm8(out={"y": wide[1:-1, 3:80]}, **t)["y"]
+    assert torch.equal(y, ref)
+    assert (wide[0] == 7).all() and (wide[-1] == 7).all() and (wide[:, :3] == 7).all() and (wide[:, 80:] == 7).all()
+    none = {**t, "x8": t["x8"][:, :0].contiguous(), "w8": t["w8"][:, :0].contiguous()}
+    y = ssm.tokens_mm8(dtype=torch.float32, **none)["y"]   # no inputs: the bias
+    assert torch.equal(y, t["bias"].expand_as(y))
+    assert ssm.tokens_mm8(**{**t, "x8": t["x8"][:0], "x8_scale": t["x8_scale"][:0]})["y"].shape == (0, 77)
+    f = ssm.tokens_pack8(torch.zeros(4, 0, device=DEV))
+    assert f["x8"].shape == (4, 0) and (f["x8_scale"] == 0).all()
+    assert ssm.tokens_pack8(torch.zeros(0, 9, device=DEV))["x8"].shape == (0, 9)
