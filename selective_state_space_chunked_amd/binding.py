@@ -259,7 +259,8 @@ def _load_pycall():
         return False
     native.bind(*(ctypes.cast(getattr(L, f), _vp).value for f in (
         "ssm_conv_fwd", "ssm_conv_bwd", "ssm_ckpt8_pack", "ssm_ckpt8_unpack", "ssm_tokens_conv", "ssm_tokens_scan",
-        "ssm_workspace_bytes")))
+        "ssm_gated_fwd", "ssm_gated_bwd", "ssm_tokens_gated", "ssm_group_norm_fwd", "ssm_group_norm_bwd",
+        "ssm_tokens_pack8", "ssm_tokens_mm8", "ssm_workspace_bytes")))
     _pycall = native
     return native
 
@@ -1243,6 +1244,11 @@ def gated_fwd(*, x, r, i, lam, r_bias=None, i_bias=None, power=8.0, h0=None, wan
     ``x``, ``r``, ``i`` (B, D, L) float32 or bfloat16, any batch and channel stride; ``lam``, ``r_bias``, ``i_bias``
     (D,) and ``h0`` (B, D) float32.  Returns a dict with y, h_last (B, D) and ckpt (B, D, ceil(L / 128)), the states
     that ``gated_bwd`` begins from, those requested."""
+    if not out and (nat := _native(x)):
+        m, di, stream = nat
+        t = m.gated_fwd(di, stream, x, r, i, lam, r_bias, i_bias, power, h0, want_y, want_h_last, want_ckpt)
+        if _done(t):
+            return {k: v for k, v in zip(("y", "h_last", "ckpt"), t) if v is not None}
     args, shape, st, dev = _gated_args(x, r, i, lam, r_bias, i_bias, power, h0, None)
     Bsz, D, L = shape
     out = dict(out) if out else {}
@@ -1273,6 +1279,14 @@ def gated_bwd(*, gy, x, r, i, lam, r_bias=None, i_bias=None, power=8.0, h0=None,
               want=_GATED_GRADS_OF, out=None):
     """Gradients of <gy, y> + <gh_last, h_last> of ``gated_fwd``; without ``ckpt`` its states are formed again first.
     Returns a dict of the gradients named in ``want``; those of biases that were not given are of biases of 0."""
+    if want is not _GATED_GRADS_OF:
+        want = tuple(want)
+    if not out and (nat := _native(gy)) and (want is _GATED_GRADS_OF or set(want) <= set(_GATED_GRADS_OF)):
+        m, di, stream = nat
+        t = m.gated_bwd(di, stream, gy, gh_last, ckpt, x, r, i, lam, r_bias, i_bias, power, h0,
+                        *[k in want for k in _GATED_GRADS_OF])
+        if _done(t):
+            return {k: v for k, v in zip(_GATED_GRADS_OF, t) if v is not None}
     if not isinstance(gy, torch.Tensor):
         raise ValueError("gy must be a torch.Tensor")
     args, shape, st, dev = _gated_args(x, r, i, lam, r_bias, i_bias, power, h0, gy.dtype)
@@ -1280,7 +1294,7 @@ def gated_bwd(*, gy, x, r, i, lam, r_bias=None, i_bias=None, power=8.0, h0=None,
     g, *sg = _stream_of(gy, "gy", st, shape, dev)
     lp = _dense(gh_last, "gh_last", _F32, (Bsz, D), dev)
     cp = _dense(ckpt, "ckpt", _F32, (Bsz, D, n_chunks(L, SSM_GATED_CHUNK)), dev)
-    out, want = dict(out) if out else {}, tuple(want)
+    out = dict(out) if out else {}
     for k in (*want, *out):
         if k not in _GATED_GRADS_OF:
             raise ValueError(f"unknown gradient {k}")
@@ -1312,6 +1326,12 @@ def tokens_gated(*, x, r, i, lam, r_bias=None, i_bias=None, power=8.0, pool, seq
 
     ``x``, ``r``, ``i`` (T, D) may be slices of wider rows; ``pool`` (slots, D) float32 holds the states, in place;
     ``seq_start``, ``slot`` and ``fresh`` as in ``tokens_conv``.  Returns a dict with y (T, D)."""
+    if nat := _native(x):
+        m, di, stream = nat
+        y = out.get("y") if out else None
+        t = m.tokens_gated(di, stream, x, r, i, lam, r_bias, i_bias, power, seq_start, slot, fresh, pool, y)
+        if _done(t):
+            return dict(out) if y is not None else {**(out or {}), "y": t}
     T, D, st, code, dev = _row_input(x)
     xp, sx = _rows(x, "x", st, T, D, dev)
     rp, sr = _rows(r, "r", st, T, D, dev)
@@ -1371,6 +1391,12 @@ def group_norm_fwd(*, x, groups, w=None, bias=None, eps=1e-5, silu=False, z=None
 
     The statistics are those of one group (C / groups consecutive channels) of one row.  ``x`` and ``z`` may be slices
     of wider rows; ``w``, ``bias`` (C,) float32.  Returns a dict with y (T, C)."""
+    if nat := _native(x):
+        m, di, stream = nat
+        y = out.get("y") if out else None
+        t = m.group_norm_fwd(di, stream, x, groups, w, bias, eps, silu, z, y)
+        if _done(t):
+            return dict(out) if y is not None else {**(out or {}), "y": t}
     args, T, C, st, dev = _norm_args(x, groups, w, bias, eps, silu, z, None)
     out = dict(out) if out else {}
     yp, sy = _y_rows(out, st, T, C, dev)
@@ -1392,12 +1418,17 @@ def _norm_bwd_bytes(code, T, C, groups):
 def group_norm_bwd(*, gy, x, groups, w=None, bias=None, eps=1e-5, silu=False, z=None, want=None, out=None):
     """Gradients of <gy, y> of ``group_norm_fwd``: a dict of those named in ``want`` (by default gx, gw, gbias, and gz
     with a gate); the statistics are formed again from x."""
+    want = tuple(want) if want is not None else _NORM_GRADS if z is not None else ("gx", "gw", "gbias")
+    if not out and (nat := _native(gy)) and (want is _NORM_GRADS or set(want) <= set(_NORM_GRADS)):
+        m, di, stream = nat
+        t = m.group_norm_bwd(di, stream, gy, x, groups, w, bias, eps, silu, z, *[k in want for k in _NORM_GRADS])
+        if _done(t):
+            return {k: v for k, v in zip(_NORM_GRADS, t) if v is not None}
     if not isinstance(gy, torch.Tensor):
         raise ValueError("gy must be a torch.Tensor")
     args, T, C, st, dev = _norm_args(x, groups, w, bias, eps, silu, z, gy.dtype)
     gp, sg = _rows(gy, "gy", st, T, C, dev)
     out = dict(out) if out else {}
-    want = tuple(want) if want is not None else _NORM_GRADS if z is not None else ("gx", "gw", "gbias")
     for k in (*want, *out):
         if k not in _NORM_GRADS:
             raise ValueError(f"unknown gradient {k}")
@@ -1417,6 +1448,11 @@ def group_norm_bwd(*, gy, x, groups, w=None, bias=None, eps=1e-5, silu=False, z=
 # ---------------------------------------------------------------------------
 def tokens_pack8(x, *, out=None):
     """The rows x (T, K) in 8 bits: a dict with x8 (T, K) int8 and x8_scale (T,) float32, one scale a row."""
+    if not out and (nat := _native(x)):
+        m, di, stream = nat
+        t = m.tokens_pack8(di, stream, x)
+        if _done(t):
+            return {"x8": t[0], "x8_scale": t[1]}
     T, K, st, code, dev = _row_input(x)
     xp, sx = _rows(x, "x", st, T, K, dev)
     out = dict(out) if out else {}
@@ -1431,6 +1467,12 @@ def tokens_mm8(*, x8, x8_scale, w8, w8_scale, bias=None, dtype=torch.bfloat16, o
 
     ``x8`` (T, K) int8 with ``x8_scale`` (T,), as ``tokens_pack8`` makes them; ``w8`` (N, K) int8 with ``w8_scale`` (N,);
     ``bias`` (N,) float32.  The sums are exact.  Returns a dict with y (T, N) of ``dtype`` (float32 or bfloat16)."""
+    if dtype in _STREAM and (nat := _native(x8)):
+        m, di, stream = nat
+        y = out.get("y") if out else None
+        t = m.tokens_mm8(di, stream, x8, x8_scale, w8, w8_scale, bias, dtype is torch.bfloat16, y)
+        if _done(t):
+            return dict(out) if y is not None else {**(out or {}), "y": t}
     for t, name in ((x8, "x8"), (w8, "w8")):
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a torch.Tensor")

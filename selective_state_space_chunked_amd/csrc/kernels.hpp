@@ -404,7 +404,7 @@ struct Mm8Params {
     void* y;
     int64_t sx, sw, sy;
     int T, K, N;
-    int tile;                        // side of a workgroup's tile, 0: the kernel for few rows
+    int tile, direct;                // side of a workgroup's tile, 0: the kernel for few rows; loads from memory to LDS
 };
 hipError_t launch_pack8(const Pack8Params& p, int dtype, hipStream_t st);
 hipError_t launch_mm8(const Mm8Params& p, int dtype, hipStream_t st);

@@ -43,6 +43,8 @@ __device__ __forceinline__ i4 row_chunk(const int8_t* row, int k, int K) {
     return i4{(int)(uint32_t)lo, (int)(lo >> 32), (int)(uint32_t)hi, (int)(hi >> 32)};
 }
 
+constexpr int kFewWaves = 16;
+
 // four channels of a row of y, the first n of them
 template <typename T>
 __device__ __forceinline__ void put4(T* y, const float (&v)[4], int n) {
@@ -71,39 +73,56 @@ __device__ __forceinline__ void channels4(const Mm8Params& p, int n0, float (&sw
     }
 }
 
-// Few rows: bound by reading the weights once.  A workgroup takes 16 channels and up to 16 TT rows, its waves the
-// k of a row in turns of 128 bytes -- whole lines of the weights -- and the waves' sums are added in LDS.
-constexpr int kFewWaves = 8, kFewStep = 128;
+// Few rows: bound by reading the weights once.  A workgroup takes 16 channels and 16 TT rows, its waves the k of a row in
+// turns of 128 bytes -- whole lines of the weights -- and the waves' sums are added in LDS.
+constexpr int kFewStep = 128;
 template <typename T, int TT>
 __global__ __launch_bounds__(64 * kFewWaves) void mm8_few_kernel(Mm8Params p) {
     __shared__ i4 part[kFewWaves][TT][64];
-    const int l = lane_id(), w = uniform(threadIdx.x >> 6), K = p.K;
-    const int n0 = blockIdx.x * 16;
+    const int l = lane_id(), w = uniform(threadIdx.x >> 6), waves = blockDim.x >> 6, K = p.K;
+    const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 16 * TT;
     const int8_t* const wr = p.w + (int64_t)min(n0 + l % 16, p.N - 1) * p.sw;
     const int8_t* xr[TT];
     i4 acc[TT];
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-        xr[i] = p.x + (int64_t)min(16 * i + l % 16, p.T - 1) * p.sx;
+        xr[i] = p.x + (int64_t)min(t0 + 16 * i + l % 16, p.T - 1) * p.sx;
         acc[i] = i4(0);
     }
-    const int kl = (l / 16) * 16;
-    int k = w * kFewStep;
-#pragma unroll 2
-    for (; k + kFewStep <= K; k += kFewStep * kFewWaves) {
+    const int kl = (l / 16) * 16, turn = waves * kFewStep;
+    // one step's operands, and its products
+    struct Step {
         i4 a[2], b[2][TT];
+    };
+    auto load = [&](Step& s, int k) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            a[h] = *reinterpret_cast<const i4u*>(wr + k + 64 * h + kl);
+            s.a[h] = *reinterpret_cast<const i4u*>(wr + k + 64 * h + kl);
 #pragma unroll
-            for (int i = 0; i < TT; ++i) b[h][i] = *reinterpret_cast<const i4u*>(xr[i] + k + 64 * h + kl);
+            for (int i = 0; i < TT; ++i) s.b[h][i] = *reinterpret_cast<const i4u*>(xr[i] + k + 64 * h + kl);
         }
+    };
+    auto products = [&](const Step& s) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < TT; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[h], b[h][i], acc[i], 0, 0, 0);
+            for (int i = 0; i < TT; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(s.a[h], s.b[h][i], acc[i], 0, 0, 0);
+    };
+    int k = w * kFewStep;
+    for (; k + turn + kFewStep <= K; k += 2 * turn) {   // two steps' loads under way together
+        Step s, u;
+        load(s, k);
+        load(u, k + turn);
+        products(s);
+        products(u);
     }
-    if (k < K) {
+    if (k + kFewStep <= K) {
+        Step s;
+        load(s, k);
+        products(s);
+        k += turn;
+    }
+    if (k < K) {   // the row's end
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const i4 a = row_chunk(wr, k + 64 * h + kl, K);
@@ -114,26 +133,92 @@ __global__ __launch_bounds__(64 * kFewWaves) void mm8_few_kernel(Mm8Params p) {
     }
 #pragma unroll
     for (int i = 0; i < TT; ++i) part[w][i][l] = acc[i];
-    __syncthreads();
     // wave i finishes the i-th 16 rows: lane l has row l % 16 and channels 4 (l / 16) ..
-    if (w >= TT) return;
     const int n = n0 + 4 * (l / 16);
     float sw[4], bias[4];
-    channels4(p, n, sw, bias);
+    if (w < TT) channels4(p, n, sw, bias);
+    __syncthreads();
+    if (w >= TT) return;
     i4 s(0);
+    for (int v = 0; v < waves; ++v) s += part[v][w][l];
+    finish4<T>(p, s, t0 + 16 * w + l % 16, n, sw, bias);
+}
+
+// What a tile's results are scaled with, in LDS (places past the last one: the last one's).
+template <int BN, int BT> struct Scales {
+    float w[BN], bias[BN], x[BT];
+};
+
+// A wave's MN x MT tiles of sums, from channel n0 + wn and row t0 + wt on: lane l has row l % 32 of a tile and four times
+// four consecutive channels.  Where all of them are places of y they go by way of LDS, 32 rows at a time and up to 256
+// bytes of each, and out in whole lines: stored from where they are, 8 bytes to each of 32 rows, they took 104 of
+// 371 us (8192 x 4096 x 8192, bf16).  Returns whether they did.
+template <typename T, bool WHOLE, int MN, int MT, int BN, int BT>
+__device__ __forceinline__ void finish_wave(const Mm8Params& p, const i16v (&acc)[MN][MT], int n0, int t0, int wn, int wt,
+                                            const Scales<BN, BT>& sc, i4* lds) {
+    constexpr int E = 16 / (int)sizeof(T), IW = MN * 32 < 16 * E ? MN : 16 * E / 32, NC = IW * 32 / E;
+    const int l = lane_id(), t = l % 32, q = l / 32;
 #pragma unroll
-    for (int v = 0; v < kFewWaves; ++v) s += part[v][w][l];
-    finish4<T>(p, s, 16 * w + l % 16, n, sw, bias);
+    for (int j = 0; j < MT; ++j) {
+        const int row = t0 + wt + 32 * j;
+        const float sx = sc.x[wt + 32 * j + t];
+#pragma unroll
+        for (int i0 = 0; i0 < MN; i0 += IW) {
+#pragma unroll
+            for (int i = i0; i < i0 + IW; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int n = 32 * i + 8 * g + 4 * q;
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = fmaf((float)acc[i][j][4 * g + e], sx * sc.w[wn + n + e], sc.bias[wn + n + e]);
+                    if (WHOLE) {   // chunk c of a row of NC lies at c ^ row % NC
+                        const int in = n - 32 * i0, c = in / E;
+                        put4<T>((T*)(lds + t * NC + (c ^ (t % NC))) + in % E, v, 4);
+                    } else if (row + t < p.T) {
+                        put4<T>((T*)p.y + (int64_t)(row + t) * p.sy + n0 + wn + n, v, p.N - n0 - wn - n);
+                    }
+                }
+            if (WHOLE) {
+#pragma unroll
+                for (int k = 0; k < NC / 2; ++k) {
+                    const int u = (64 * k + l) / NC, c = l % NC;
+                    const i4 o = lds[u * NC + (c ^ (u % NC))];
+                    typedef int i4e __attribute__((ext_vector_type(4), aligned(2)));
+                    *reinterpret_cast<i4e*>((T*)p.y + (int64_t)(row + u) * p.sy + n0 + wn + 32 * i0 + c * E) = o;
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);   // not all of it at once: the sums fill the registers
+        }
+    }
+}
+template <typename T, int MN, int MT, int BN, int BT>
+__device__ __forceinline__ bool finish_tiles(const Mm8Params& p, const i16v (&acc)[MN][MT], int n0, int t0, int wn, int wt,
+                                             const Scales<BN, BT>& sc, i4* lds) {
+    const bool whole = n0 + wn + 32 * MN <= p.N && t0 + wt + 32 * MT <= p.T;
+    if (whole) finish_wave<T, true>(p, acc, n0, t0, wn, wt, sc, lds);
+    else finish_wave<T, false>(p, acc, n0, t0, wn, wt, sc, lds);
+    return whole;
+}
+// A workgroup's tile: the workgroups of an XCD (every eighth one) take neighbouring tiles, in patches of up to eight
+// tiles of rows by as many of channels as come next, so that what they read at a time is in its L2.
+__device__ __forceinline__ int2 tile_of(int id, int nblocks, int tblocks) {
+    const int total = nblocks * tblocks, per = total / 8, rest = total % 8, xcd = id % 8;
+    const int i = xcd * per + min(xcd, rest) + id / 8;   // the first `rest` XCDs have one tile more
+    const int rows = 8, patch = rows * nblocks, t = i / patch * rows, in = i % patch, h = min(rows, tblocks - t);
+    return {in / h, t + in % h};
 }
 
 // Many rows: a workgroup takes BN channels and BT rows, 128 bytes of k at a time through LDS, WN x WT waves of 32 x 32
-// tiles each.  A row's eight 16-byte chunks lie in LDS at places exchanged by the row's number (chunk c of row r at
-// c ^ r % 8), so the lanes of a matrix instruction, which read the same chunk of 32 rows, meet all banks.
+// tiles each.  A row's eight 16-byte chunks lie in LDS at places exchanged by half the row's number (chunk c of row r
+// at c ^ r / 2 % 8): the 16 lanes that are read together, a chunk of 16 rows, meet all 64 banks.
 constexpr int kStep = 128;
 template <typename T, int BN, int BT, int WN, int WT>
 __global__ __launch_bounds__(64 * WN * WT) void mm8_tile_kernel(Mm8Params p, int nblocks) {
     constexpr int TH = 64 * WN * WT, CH = (BN + BT) * 8 / TH, MN = BN / WN / 32, MT = BT / WT / 32;
-    __shared__ i4 lds[(BN + BT) * 8];
+    __shared__ __align__(16) i4 lds[(BN + BT) * 8];
+    __shared__ Scales<BN, BT> sc;
     const int l = lane_id(), wave = uniform(threadIdx.x >> 6), K = p.K;
     const int n0 = (blockIdx.x % nblocks) * BN, t0 = (blockIdx.x / nblocks) * BT;
     const int wn = (wave % WN) * (BN / WN), wt = (wave / WN) * (BT / WT);
@@ -145,7 +230,12 @@ __global__ __launch_bounds__(64 * WN * WT) void mm8_tile_kernel(Mm8Params p, int
         const int r = i * (TH / 8) + threadIdx.x / 8;
         src[i] = r < BN ? p.w + (int64_t)min(n0 + r, p.N - 1) * p.sw : p.x + (int64_t)min(t0 + r - BN, p.T - 1) * p.sx;
     }
-    const int put = (threadIdx.x / 8) * 8 + (c ^ (threadIdx.x / 8) % 8);   // TH / 8 is a multiple of 8
+    const int put = (threadIdx.x / 8) * 8 + (c ^ (threadIdx.x / 16) % 8);   // TH / 8 is a multiple of 16
+    for (int i = threadIdx.x; i < BN; i += TH) {
+        sc.w[i] = p.ws[min(n0 + i, p.N - 1)];
+        sc.bias[i] = p.bias ? p.bias[min(n0 + i, p.N - 1)] : 0.0f;
+    }
+    for (int i = threadIdx.x; i < BT; i += TH) sc.x[i] = p.xs[min(t0 + i, p.T - 1)];
     i4 next[CH];
     auto load = [&](int k) {
         if (k + kStep <= K) {
@@ -170,7 +260,7 @@ __global__ __launch_bounds__(64 * WN * WT) void mm8_tile_kernel(Mm8Params p, int
         if (k + kStep < K) load(k + kStep);
 #pragma unroll
         for (int s = 0; s < kStep / 32; ++s) {
-            const int ch = (2 * s + l / 32) ^ (l % 8);
+            const int ch = (2 * s + l / 32) ^ (l / 2 % 8);
             i4 a[MN], b[MT];
 #pragma unroll
             for (int i = 0; i < MN; ++i) a[i] = lds[(wn + 32 * i + l % 32) * 8 + ch];
@@ -183,19 +273,134 @@ __global__ __launch_bounds__(64 * WN * WT) void mm8_tile_kernel(Mm8Params p, int
                     acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
         }
     }
+    __syncthreads();
+    finish_tiles<T, MN, MT>(p, acc, n0, t0, wn, wt, sc, lds + wave * ((BN + BT) * 8 / (WN * WT)));
+}
+
+// Many rows whose starts are aligned to 16 bytes and K a multiple of 128: the same with loads that go from memory to
+// LDS directly, a step ahead of the products, and one barrier a step.  A workgroup
+// goes on from tile to tile: the next tile's first step comes while a tile's results go out.
+constexpr int kDirectStep = 128;
+// 16 or 4 bytes of every lane's address, one lane's after the other's, to a place in LDS (no register takes the data).
+// Of the builtins for it the compiler waits for all before the next read of LDS, the step's own among them, whatever part
+// of LDS is read; these are waited for by wait_barrier alone.
+__device__ __forceinline__ uint32_t lds_place(const void* p) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p);
+}
+__device__ __forceinline__ void to_lds16(const void* from, const void* to) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds_place(to)) : "memory", "m0");
+}
+__device__ __forceinline__ void to_lds4(const void* from, const void* to) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(lds_place(to)) : "memory", "m0");
+}
+// The wave's memory accesses but the last N, and its LDS accesses, are done, then the workgroup's.
+template <int N = 0> __device__ __forceinline__ void wait_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+template <typename T, int BN, int BT, int WN, int WT>
+__global__ __launch_bounds__(64 * WN * WT) void mm8_direct_kernel(Mm8Params p, int nblocks, int tblocks) {
+    constexpr int W = WN * WT, MN = BN / WN / 32, MT = BT / WT / 32;
+    constexpr int ROWS = BN + BT, LD = ROWS / 8 / W;   // loads of a wave, 8 rows each
+    static_assert(BN % (8 * LD) == 0, "a wave's loads are of one operand");
+    static_assert(BN / 64 + BT / 64 <= W, "a wave loads 64 scales");
+    __shared__ __align__(16) i4 lds[2][ROWS * 8];
+    __shared__ __align__(16) Scales<BN, BT> scales[2];
+    const int l = lane_id(), wave = uniform(threadIdx.x >> 6), total = nblocks * tblocks;
+    const int wn = (wave % WN) * (BN / WN), wt = (wave / WN) * (BT / WT);
+    const int r0 = wave * LD * 8;   // the wave's first row of a step
+    const bool of_w = r0 < BN;
+    const int last = (of_w ? p.N : p.T) - 1;
+    const int64_t stride = of_w ? p.sw : p.sx;
+    const int8_t* src;
+    uint32_t off[LD];
+    int n0, t0;
+    const int steps = p.K / kDirectStep;
+    auto load = [&](int k, int j0, int j1) {
 #pragma unroll
-    for (int i = 0; i < MN; ++i)
+        for (int j = j0; j < j1; ++j)
+            to_lds16(src + (int64_t)k * kDirectStep + off[j], &lds[k & 1][(r0 + 8 * j) * 8]);
+    };
+    // tile `id`, its scales and its first step
+    auto begin = [&](int id, Scales<BN, BT>& sc) {
+        const int2 tile = tile_of(id, nblocks, tblocks);
+        n0 = tile.x * BN;
+        t0 = tile.y * BT;
+        const int first = of_w ? n0 + r0 : t0 + r0 - BN;
+        src = (of_w ? p.w : p.x) + min(first, last) * stride;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int n = n0 + wn + 32 * i + 8 * g + 4 * (l / 32);
-            float sw[4], bias[4];
-            channels4(p, n, sw, bias);
+        for (int j = 0; j < LD; ++j) {
+            const int r = 8 * j + l / 8;   // of the wave's rows; those past the operand's last one repeat it
+            off[j] = (uint32_t)(max(0, min(first + r, last) - min(first, last)) * stride) + (((l % 8) ^ ((r0 + r) / 2 % 8)) * 16);
+        }
+        if (wave < BN / 64) {
+            const int n = min(n0 + 64 * wave + l, p.N - 1);
+            to_lds4(p.ws + n, &sc.w[64 * wave]);
+            if (p.bias) to_lds4(p.bias + n, &sc.bias[64 * wave]);
+        } else if (wave < BN / 64 + BT / 64) {
+            const int at = 64 * (wave - BN / 64);
+            to_lds4(p.xs + min(t0 + at + l, p.T - 1), &sc.x[at]);
+        }
+        load(0, 0, LD);
+    };
+    const int fa = (wn + l % 32) * 8, fb = (BN + wt + l % 32) * 8, sw = l / 2 % 8;
+    i4 a[2][MN], b[2][MT];   // of two quarters of a step
+    i16v acc[MN][MT];
+    auto fragments = [&](int k, int s) {
+        const i4* const at = lds[k & 1] + ((2 * s + l / 32) ^ sw);
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const i4 s = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-                finish4<T>(p, s, t0 + wt + 32 * j + l % 32, n, sw, bias);
+        for (int i = 0; i < MN; ++i) a[s & 1][i] = at[fa + 256 * i];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) b[s & 1][j] = at[fb + 256 * j];
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto products = [&](int s, int i0, int i1) {
+#pragma unroll
+        for (int i = i0; i < i1; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[s & 1][i], b[s & 1][j], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // A quarter's products run while the next quarter's operands are read, the first few before the reads so that what
+    // they wait for is behind them already; the next step's loads go out between those of the first quarter.
+    auto step = [&](int k, bool more) {
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+            products(s, 0, 1);
+            fragments(k, s + 1);
+#pragma unroll
+            for (int i = 1; i < MN; ++i) {
+                if (s == 0 && more) load(k + 1, LD * (i - 1) / (MN - 1), LD * i / (MN - 1));
+                products(s, i, i + 1);
             }
         }
+        products(3, 0, 1);
+        wait_barrier();   // step k + 1 has come, and every wave has read step k
+        products(3, 1, MN / 2 + 1);
+        if (more) fragments(k + 1, 0);
+        products(3, MN / 2 + 1, MN);
+    };
+    int buf = 0;
+    for (int i = threadIdx.x; !p.bias && i < BN; i += 64 * W) scales[0].bias[i] = scales[1].bias[i] = 0.0f;
+    begin(blockIdx.x, scales[0]);
+    wait_barrier();
+    for (int id = blockIdx.x;; buf ^= 1) {
+#pragma unroll
+        for (int i = 0; i < MN; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[i][j] = i16v(0);
+        fragments(0, 0);
+        for (int k = 0; k + 1 < steps; ++k) step(k, true);
+        step(steps - 1, false);
+        // The next tile's first step comes while this one's results go out, by way of the other stage.
+        const int n = n0, t = t0;
+        id += gridDim.x;
+        if (id < total) begin(id, scales[buf ^ 1]);
+        const bool whole = finish_tiles<T, MN, MT>(p, acc, n, t, wn, wt, scales[buf], lds[1] + wave * (ROWS * 8 / W));
+        if (id >= total) break;
+        if (whole) wait_barrier<MN * MT * (int)sizeof(T)>();   // its stores may be under way: 16 bytes of 64 lanes each
+        else wait_barrier();
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -281,16 +486,23 @@ __global__ __launch_bounds__(256) void pack8_kernel(Pack8Params p) {
 
 template <typename T>
 hipError_t launch(const Mm8Params& p, hipStream_t st) {
-    const int few = (p.T + 15) / 16;
     if (p.tile == 0) {
-        const unsigned blocks = (unsigned)((p.N + 15) / 16);
-        if (few == 1) mm8_few_kernel<T, 1><<<blocks, 64 * kFewWaves, 0, st>>>(p);
-        else if (few == 2) mm8_few_kernel<T, 2><<<blocks, 64 * kFewWaves, 0, st>>>(p);
-        else mm8_few_kernel<T, 4><<<blocks, 64 * kFewWaves, 0, st>>>(p);
+        const int nb = (p.N + 15) / 16, few = (p.T + 15) / 16;
+        // waves of a workgroup: as many as have a step, at least one for each 16 rows it finishes
+        const int TT = few == 1 ? 1 : few == 2 || nb < 256 ? 2 : 4;
+        const int waves = std::max(TT, std::min(kFewWaves, (p.K + kFewStep - 1) / kFewStep));
+        const dim3 grid(nb, (few + TT - 1) / TT);
+        if (TT == 1) mm8_few_kernel<T, 1><<<grid, 64 * waves, 0, st>>>(p);
+        else if (TT == 2) mm8_few_kernel<T, 2><<<grid, 64 * waves, 0, st>>>(p);
+        else mm8_few_kernel<T, 4><<<grid, 64 * waves, 0, st>>>(p);
     } else {
-        const int nb = (p.N + p.tile - 1) / p.tile;
-        const unsigned blocks = (unsigned)nb * (unsigned)((p.T + p.tile - 1) / p.tile);
-        if (p.tile == 64) mm8_tile_kernel<T, 64, 64, 2, 2><<<blocks, 256, 0, st>>>(p, nb);
+        const int nb = (p.N + p.tile - 1) / p.tile, tb = (p.T + p.tile - 1) / p.tile;
+        const unsigned blocks = (unsigned)nb * (unsigned)tb;
+        if (p.direct && p.tile == 256)
+            mm8_direct_kernel<T, 256, 256, 2, 4><<<std::min(blocks, 256u), 512, 0, st>>>(p, nb, tb);
+        else if (p.direct)
+            mm8_direct_kernel<T, 128, 128, 2, 2><<<std::min(blocks, 512u), 256, 0, st>>>(p, nb, tb);
+        else if (p.tile == 64) mm8_tile_kernel<T, 64, 64, 2, 2><<<blocks, 256, 0, st>>>(p, nb);
         else mm8_tile_kernel<T, 128, 128, 2, 2><<<blocks, 256, 0, st>>>(p, nb);
     }
     return hipGetLastError();

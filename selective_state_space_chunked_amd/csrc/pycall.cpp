@@ -10,6 +10,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <cstdlib>
 
 #include "../../include/ssmscan.h"
 
@@ -23,9 +24,16 @@ struct Calls {
     decltype(&ssm_ckpt8_unpack) unpack;
     decltype(&ssm_tokens_conv) tokens_conv;
     decltype(&ssm_tokens_scan) tokens_scan;
+    decltype(&ssm_gated_fwd) gated_fwd;
+    decltype(&ssm_gated_bwd) gated_bwd;
+    decltype(&ssm_tokens_gated) tokens_gated;
+    decltype(&ssm_group_norm_fwd) norm_fwd;
+    decltype(&ssm_group_norm_bwd) norm_bwd;
+    decltype(&ssm_tokens_pack8) pack_rows;
+    decltype(&ssm_tokens_mm8) mm8;
     decltype(&ssm_workspace_bytes) bytes;
 } g{};
-constexpr int kCalls = 7;
+constexpr int kCalls = 14;
 
 // The arguments of one call, checked one by one; `ok` turns false at the first that is not as expected.
 struct Args {
@@ -45,6 +53,28 @@ struct Args {
         return v == 1;
     }
     int64_t whole() { return PyLong_AsLongLong(next()); }
+    // a count, and a real number (nothing else is taken for one: the binding's own path says what is wrong with it)
+    int64_t count() {
+        PyObject* o = next();
+        if (!PyLong_CheckExact(o)) {
+            ok = false;
+            return 0;
+        }
+        const int64_t v = PyLong_AsLongLong(o);
+        if (v == -1 && PyErr_Occurred()) {
+            PyErr_Clear();
+            ok = false;
+        }
+        return v;
+    }
+    float real() {
+        PyObject* o = next();
+        if (!PyFloat_CheckExact(o)) {
+            ok = false;
+            return 0.0f;
+        }
+        return (float)PyFloat_AS_DOUBLE(o);
+    }
     // the next argument as a tensor of the call's device; null for None (or where not ok)
     const at::Tensor* tensor(bool required) {
         PyObject* o = next();
@@ -117,7 +147,7 @@ PyObject* guarded(F f) {   // what C++ throws reaches the interpreter as torch's
     END_HANDLE_TH_ERRORS
 }
 
-// sequences of a packed-row call: seq_start, slot, fresh, pool; pool (slots, D, inner)
+// sequences of a packed-row call: seq_start, slot, fresh, pool; pool (slots, D, inner), or (slots, D) with inner -1
 struct Seq {
     const int32_t *start, *slot;
     const uint8_t* fresh;
@@ -147,8 +177,9 @@ bool sequences(Args& in, int64_t T, int64_t D, int64_t inner, at::ScalarType poo
     }
     const at::Tensor* pool = in.tensor(true);
     if (!pool) return false;
-    if (pool->scalar_type() != pool_type || pool->dim() != 3 || pool->size(1) != D || pool->size(2) != inner ||
-        pool->numel() == 0 || (pool->stride(2) != 1 && inner > 1) || (pool->stride(1) != inner && D > 1))
+    if (pool->scalar_type() != pool_type || pool->dim() != (inner < 0 ? 2 : 3) || pool->size(1) != D || pool->numel() == 0 ||
+        (pool->stride(1) != std::abs(inner) && D > 1) ||
+        (inner >= 0 && (pool->size(2) != inner || (pool->stride(2) != 1 && inner > 1))))
         return in.ok = false;
     q->pool = pool->data_ptr();
     q->slots = pool->size(0);
@@ -377,6 +408,244 @@ PyObject* ckpt8_unpack(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
     });
 }
 
+// x, r, i, lam, r_bias, i_bias, power, h0 of a gated recurrence over dense streams
+bool gated_input(Args& in, ssm_gated_args* a, at::ScalarType* dt) {
+    const at::Tensor* x = in.tensor(true);
+    if (!x || x->dim() != 3 || !stream_type(x->scalar_type()) || !x->is_contiguous()) return false;
+    *dt = x->scalar_type();
+    a->dtype = code(*dt);
+    const int64_t B = a->batch = x->size(0), D = a->channels = x->size(1), L = a->length = x->size(2);
+    a->x = x->data_ptr();
+    a->r = in.dense(*dt, {B, D, L}, true);
+    a->i = in.dense(*dt, {B, D, L}, true);
+    a->lam = (const float*)in.dense(at::kFloat, {D}, true);
+    a->r_bias = (const float*)in.dense(at::kFloat, {D});
+    a->i_bias = (const float*)in.dense(at::kFloat, {D});
+    a->power = in.real();
+    a->h0 = (const float*)in.dense(at::kFloat, {B, D});
+    for (int64_t* s : {a->x_stride, a->r_stride, a->i_stride}) {
+        s[0] = D * L;
+        s[1] = L;
+    }
+    return in.ok;
+}
+int64_t gated_chunks(int64_t L) { return (L + SSM_GATED_CHUNK - 1) / SSM_GATED_CHUNK; }
+
+// x, r, i, lam, r_bias, i_bias, power, h0, want_y, want_h_last, want_ckpt -> (y, h_last, ckpt)
+PyObject* gated_fwd(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+    return guarded([&]() -> PyObject* {
+        Args in{argv, argc};
+        in.dev = (int)in.whole();
+        void* stream = (void*)(intptr_t)in.whole();
+        ssm_gated_args a{};
+        at::ScalarType dt;
+        if (!gated_input(in, &a, &dt)) return none_of_these();
+        ssm_gated_fwd_out o{};
+        at::Tensor y, last, ck;
+        const int want_y = in.flag(), want_last = in.flag(), want_ckpt = in.flag();
+        if (!in.ok) return none_of_these();
+        if (want_y) o.y = (y = fresh({a.batch, a.channels, a.length}, dt, in.dev)).data_ptr();
+        if (want_last) o.h_last = (float*)(last = fresh({a.batch, a.channels}, at::kFloat, in.dev)).data_ptr();
+        if (want_ckpt)
+            o.ckpt = (float*)(ck = fresh({a.batch, a.channels, gated_chunks(a.length)}, at::kFloat, in.dev)).data_ptr();
+        o.y_stride[0] = a.channels * a.length;
+        o.y_stride[1] = a.length;
+        if (int rc = g.gated_fwd(&a, &o, stream)) return PyLong_FromLong(rc);
+        return Py_BuildValue("(NNN)", wrapped(y), wrapped(last), wrapped(ck));
+    });
+}
+
+// gy, gh_last, ckpt, x, r, i, lam, r_bias, i_bias, power, h0, and which of gx, gr, gi, glam, gr_bias, gi_bias, gh0 -> these
+PyObject* gated_bwd(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+    return guarded([&]() -> PyObject* {
+        Args in{argv, argc};
+        in.dev = (int)in.whole();
+        void* stream = (void*)(intptr_t)in.whole();
+        const at::Tensor* gy = in.tensor(true);
+        const at::Tensor* gl = in.tensor(false);
+        const at::Tensor* ck = in.tensor(false);
+        ssm_gated_args a{};
+        at::ScalarType dt;
+        if (!in.ok || !gated_input(in, &a, &dt)) return none_of_these();
+        const int64_t B = a.batch, D = a.channels, L = a.length;
+        if (gy->scalar_type() != dt || gy->sizes() != at::IntArrayRef({B, D, L}) || !gy->is_contiguous() ||
+            (gl && (gl->scalar_type() != at::kFloat || gl->sizes() != at::IntArrayRef({B, D}) || !gl->is_contiguous())) ||
+            (ck && (ck->scalar_type() != at::kFloat || ck->sizes() != at::IntArrayRef({B, D, gated_chunks(L)}) ||
+                    !ck->is_contiguous())))
+            return none_of_these();
+        ssm_gated_bwd_in b{gy->data_ptr(), gl ? (const float*)gl->data_ptr() : nullptr,
+                           ck ? (const float*)ck->data_ptr() : nullptr, {D * L, L}};
+        ssm_gated_grads o{};
+        at::Tensor t[7];
+        void** streams[3] = {&o.gx, &o.gr, &o.gi};
+        float** par[4] = {&o.glam, &o.gr_bias, &o.gi_bias, &o.gh0};
+        for (int k = 0; k < 3; ++k)
+            if (in.flag()) *streams[k] = (t[k] = fresh({B, D, L}, dt, in.dev)).data_ptr();
+        for (int k = 0; k < 4; ++k)
+            if (in.flag()) {
+                t[3 + k] = k == 3 ? fresh({B, D}, at::kFloat, in.dev) : fresh({D}, at::kFloat, in.dev);
+                *par[k] = (float*)t[3 + k].data_ptr();
+            }
+        for (int64_t* s : {o.gx_stride, o.gr_stride, o.gi_stride}) {
+            s[0] = D * L;
+            s[1] = L;
+        }
+        Scratch ws;
+        if (int rc = ws.get(SSM_OP_GATED_BWD, &a, in.dev)) return PyLong_FromLong(rc);
+        if (int rc = g.gated_bwd(&a, &b, &o, ws.p, ws.n, stream)) return PyLong_FromLong(rc);
+        return Py_BuildValue("(NNNNNNN)", wrapped(t[0]), wrapped(t[1]), wrapped(t[2]), wrapped(t[3]), wrapped(t[4]),
+                             wrapped(t[5]), wrapped(t[6]));
+    });
+}
+
+// x, r, i, lam, r_bias, i_bias, power, seq_start, slot, fresh, pool, y -> y
+PyObject* tokens_gated(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+    return guarded([&]() -> PyObject* {
+        Args in{argv, argc};
+        in.dev = (int)in.whole();
+        void* stream = (void*)(intptr_t)in.whole();
+        ssm_tokens_gated_args a{};
+        const at::Tensor* x = in.tensor(true);
+        if (!x || x->dim() != 2 || !stream_type(x->scalar_type())) return none_of_these();
+        const at::ScalarType dt = x->scalar_type();
+        const int64_t T = x->size(0), D = x->size(1);
+        if (x->stride(1) != 1 && D > 1) return none_of_these();
+        a.dtype = code(dt);
+        a.tokens = T; a.channels = D;
+        a.x = x->data_ptr(); a.x_stride = x->stride(0);
+        a.r = in.rows(dt, T, D, &a.r_stride);
+        a.i = in.rows(dt, T, D, &a.i_stride);
+        a.lam = (const float*)in.dense(at::kFloat, {D}, true);
+        a.r_bias = (const float*)in.dense(at::kFloat, {D});
+        a.i_bias = (const float*)in.dense(at::kFloat, {D});
+        a.power = in.real();
+        Seq q;
+        if (!in.ok || !sequences(in, T, D, -1, at::kFloat, &q)) return none_of_these();
+        at::Tensor y;
+        a.y = out_rows(in, dt, T, D, &a.y_stride, &y);
+        if (!in.ok) return none_of_these();
+        a.seq_start = q.start; a.slot = q.slot; a.fresh = q.fresh; a.pool = (float*)q.pool;
+        a.sequences = q.S; a.slots = q.slots; a.pool_stride = q.stride;
+        Scratch ws;
+        if (q.start)
+            if (int rc = ws.get(SSM_OP_TOKENS_GATED, &a, in.dev)) return PyLong_FromLong(rc);
+        if (int rc = g.tokens_gated(&a, ws.p, ws.n, stream)) return PyLong_FromLong(rc);
+        return wrapped(y);
+    });
+}
+
+// x, groups, w, bias, eps, silu, z of a group norm
+bool norm_input(Args& in, ssm_group_norm_args* a, at::ScalarType* dt) {
+    const at::Tensor* x = in.tensor(true);
+    if (!x || x->dim() != 2 || !stream_type(x->scalar_type()) || (x->stride(1) != 1 && x->size(1) > 1)) return false;
+    *dt = x->scalar_type();
+    a->dtype = code(*dt);
+    const int64_t T = a->rows = x->size(0), C = a->channels = x->size(1);
+    a->x = x->data_ptr(); a->x_stride = x->stride(0);
+    a->groups = in.count();
+    a->w = (const float*)in.dense(at::kFloat, {C});
+    a->bias = (const float*)in.dense(at::kFloat, {C});
+    a->eps = in.real();
+    a->silu = in.flag();
+    if (in.a[in.i] == Py_None) ++in.i;
+    else a->z = in.rows(*dt, T, C, &a->z_stride);
+    return in.ok;
+}
+// x, groups, w, bias, eps, silu, z, y -> y
+PyObject* group_norm_fwd(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+    return guarded([&]() -> PyObject* {
+        Args in{argv, argc};
+        in.dev = (int)in.whole();
+        void* stream = (void*)(intptr_t)in.whole();
+        ssm_group_norm_args a{};
+        at::ScalarType dt;
+        if (!norm_input(in, &a, &dt)) return none_of_these();
+        at::Tensor y;
+        int64_t sy = 0;
+        void* p = out_rows(in, dt, a.rows, a.channels, &sy, &y);
+        if (!in.ok) return none_of_these();
+        if (int rc = g.norm_fwd(&a, p, sy, stream)) return PyLong_FromLong(rc);
+        return wrapped(y);
+    });
+}
+// gy, x, groups, w, bias, eps, silu, z, and which of gx, gz, gw, gbias -> these
+PyObject* group_norm_bwd(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+    return guarded([&]() -> PyObject* {
+        Args in{argv, argc};
+        in.dev = (int)in.whole();
+        void* stream = (void*)(intptr_t)in.whole();
+        const at::Tensor* gy = in.tensor(true);
+        ssm_group_norm_args a{};
+        at::ScalarType dt;
+        if (!in.ok || !norm_input(in, &a, &dt)) return none_of_these();
+        const int64_t T = a.rows, C = a.channels;
+        if (gy->scalar_type() != dt || gy->sizes() != at::IntArrayRef({T, C}) || (gy->stride(1) != 1 && C > 1))
+            return none_of_these();
+        ssm_group_norm_grads o{};
+        at::Tensor gx, gz, gw, gb;
+        if (in.flag()) o.gx = (gx = fresh({T, C}, dt, in.dev)).data_ptr();
+        if (in.flag()) o.gz = (gz = fresh({T, C}, dt, in.dev)).data_ptr();
+        if (in.flag()) o.gw = (float*)(gw = fresh({C}, at::kFloat, in.dev)).data_ptr();
+        if (in.flag()) o.gbias = (float*)(gb = fresh({C}, at::kFloat, in.dev)).data_ptr();
+        o.gx_stride = o.gz_stride = C;
+        Scratch ws;
+        if (int rc = ws.get(SSM_OP_GROUP_NORM_BWD, &a, in.dev)) return PyLong_FromLong(rc);
+        if (int rc = g.norm_bwd(&a, gy->data_ptr(), gy->stride(0), &o, ws.p, ws.n, stream)) return PyLong_FromLong(rc);
+        return Py_BuildValue("(NNNN)", wrapped(gx), wrapped(gz), wrapped(gw), wrapped(gb));
+    });
+}
+
+// x -> (x8, x8_scale)
+PyObject* tokens_pack8(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+    return guarded([&]() -> PyObject* {
+        Args in{argv, argc};
+        in.dev = (int)in.whole();
+        void* stream = (void*)(intptr_t)in.whole();
+        const at::Tensor* x = in.tensor(true);
+        if (!x || x->dim() != 2 || !stream_type(x->scalar_type()) || (x->stride(1) != 1 && x->size(1) > 1))
+            return none_of_these();
+        ssm_tokens_pack8_args a{};
+        a.dtype = code(x->scalar_type());
+        a.tokens = x->size(0); a.channels = x->size(1);
+        a.x = x->data_ptr(); a.x_stride = x->stride(0);
+        at::Tensor x8 = fresh(x->sizes(), at::kChar, in.dev), sc = fresh({a.tokens}, at::kFloat, in.dev);
+        a.x8 = (int8_t*)x8.data_ptr(); a.x8_scale = (float*)sc.data_ptr();
+        a.x8_stride = a.channels;
+        if (int rc = g.pack_rows(&a, stream)) return PyLong_FromLong(rc);
+        return Py_BuildValue("(NN)", wrapped(x8), wrapped(sc));
+    });
+}
+
+// x8, x8_scale, w8, w8_scale, bias, 1 for bf16, y -> y
+PyObject* tokens_mm8(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+    return guarded([&]() -> PyObject* {
+        Args in{argv, argc};
+        in.dev = (int)in.whole();
+        void* stream = (void*)(intptr_t)in.whole();
+        ssm_tokens_mm8_args a{};
+        const at::Tensor* x = in.tensor(true);
+        if (!x || x->dim() != 2 || x->scalar_type() != at::kChar || (x->stride(1) != 1 && x->size(1) > 1))
+            return none_of_these();
+        const int64_t T = a.tokens = x->size(0), K = a.inputs = x->size(1);
+        a.x8 = (const int8_t*)x->data_ptr(); a.x8_stride = x->stride(0);
+        a.x8_scale = (const float*)in.dense(at::kFloat, {T}, true);
+        const at::Tensor* w = in.tensor(true);
+        if (!in.ok || w->dim() != 2 || w->scalar_type() != at::kChar || w->size(1) != K || (w->stride(1) != 1 && K > 1))
+            return none_of_these();
+        const int64_t N = a.outputs = w->size(0);
+        a.w8 = (const int8_t*)w->data_ptr(); a.w8_stride = w->stride(0);
+        a.w8_scale = (const float*)in.dense(at::kFloat, {N}, true);
+        a.bias = (const float*)in.dense(at::kFloat, {N});
+        const at::ScalarType dt = in.flag() ? at::kBFloat16 : at::kFloat;
+        a.dtype = code(dt);
+        at::Tensor y;
+        a.y = out_rows(in, dt, T, N, &a.y_stride, &y);
+        if (!in.ok) return none_of_these();
+        if (int rc = g.mm8(&a, stream)) return PyLong_FromLong(rc);
+        return wrapped(y);
+    });
+}
+
 // addresses of the library's functions, in the order of Calls
 PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
     if (argc != kCalls) {
@@ -391,9 +660,11 @@ PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
             return nullptr;
         }
     }
-    g = Calls{(decltype(g.conv_fwd))p[0], (decltype(g.conv_bwd))p[1],    (decltype(g.pack))p[2],
-              (decltype(g.unpack))p[3],   (decltype(g.tokens_conv))p[4], (decltype(g.tokens_scan))p[5],
-              (decltype(g.bytes))p[6]};
+    g = Calls{(decltype(g.conv_fwd))p[0],     (decltype(g.conv_bwd))p[1],    (decltype(g.pack))p[2],
+              (decltype(g.unpack))p[3],       (decltype(g.tokens_conv))p[4], (decltype(g.tokens_scan))p[5],
+              (decltype(g.gated_fwd))p[6],    (decltype(g.gated_bwd))p[7],   (decltype(g.tokens_gated))p[8],
+              (decltype(g.norm_fwd))p[9],     (decltype(g.norm_bwd))p[10],   (decltype(g.pack_rows))p[11],
+              (decltype(g.mm8))p[12],         (decltype(g.bytes))p[13]};
     Py_RETURN_NONE;
 }
 
@@ -418,6 +689,13 @@ PyMethodDef methods[] = {
     {"conv_bwd", (PyCFunction)(void (*)(void))counted<conv_bwd, 15>, METH_FASTCALL, nullptr},
     {"ckpt8_pack", (PyCFunction)(void (*)(void))counted<ckpt8_pack, 3>, METH_FASTCALL, nullptr},
     {"ckpt8_unpack", (PyCFunction)(void (*)(void))counted<ckpt8_unpack, 5>, METH_FASTCALL, nullptr},
+    {"gated_fwd", (PyCFunction)(void (*)(void))counted<gated_fwd, 13>, METH_FASTCALL, nullptr},
+    {"gated_bwd", (PyCFunction)(void (*)(void))counted<gated_bwd, 20>, METH_FASTCALL, nullptr},
+    {"tokens_gated", (PyCFunction)(void (*)(void))counted<tokens_gated, 14>, METH_FASTCALL, nullptr},
+    {"group_norm_fwd", (PyCFunction)(void (*)(void))counted<group_norm_fwd, 10>, METH_FASTCALL, nullptr},
+    {"group_norm_bwd", (PyCFunction)(void (*)(void))counted<group_norm_bwd, 14>, METH_FASTCALL, nullptr},
+    {"tokens_pack8", (PyCFunction)(void (*)(void))counted<tokens_pack8, 3>, METH_FASTCALL, nullptr},
+    {"tokens_mm8", (PyCFunction)(void (*)(void))counted<tokens_mm8, 9>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pycall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -494,7 +494,7 @@ def test_mm8(T, N, K, dtype):
 
 
 @pytest.mark.parametrize("T,K,N", [(2100, 640, 2000), (2049, 384, 4100), (1000, 200, 8200), (512, 4096, 512), (4096, 256, 264),
-                                   (70, 8192, 500), (200, 131071, 40)])
+                                   (70, 8192, 500), (200, 131071, 40), (4000, 192, 3900), (3800, 64, 3700)])
 def test_mm8_large(T, K, N):
     mm8_check(mm8_inputs(T, K, N, gen(31)), "bf16")
     mm8_check(mm8_inputs(T, K, N, gen(32), view=True), "f32")
