@@ -663,7 +663,7 @@ int ssm_gated_bwd(const ssm_gated_args* args, const ssm_gated_bwd_in* in, const 
                   void* ws, size_t ws_bytes, void* stream);
 
 /* The gated recurrence over packed rows, with sequences, pool and rows as in ssm_tokens_conv above.  The workspace
- * (SSM_OP_TOKENS_GATED) holds the states that cross from one range of rows to the next; the step form needs none. */
+ * (SSM_OP_TOKENS_GATED) holds what one tile of rows hands on to the next; the step form needs none. */
 typedef struct {
     int32_t dtype;             /* of x, r, i and y                                           */
     float   power;

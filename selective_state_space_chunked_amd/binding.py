@@ -1311,9 +1311,9 @@ def gated_bwd(*, gy, x, r, i, lam, r_bias=None, i_bias=None, power=8.0, h0=None,
 
 
 @functools.lru_cache(maxsize=1024)
-def _tokens_gated_bytes(T, D):
-    # sizes only: the sequences do not change what the ranges of rows need
-    args = TokensGatedArgs(dtype=SSM_F32, power=1.0, tokens=T, channels=D, sequences=1, slots=1, seq_start=256,
+def _tokens_gated_bytes(code, T, D, S):
+    # sizes only
+    args = TokensGatedArgs(dtype=code, power=1.0, tokens=T, channels=D, sequences=S, slots=S, seq_start=256,
                            x_stride=D, r_stride=D, i_stride=D, y_stride=D, pool_stride=D)
     n = ctypes.c_size_t(0)
     _check(lib().ssm_workspace_bytes(SSM_OP_TOKENS_GATED, ctypes.byref(args), ctypes.byref(n)))
@@ -1348,7 +1348,7 @@ def tokens_gated(*, x, r, i, lam, r_bias=None, i_bias=None, power=8.0, pool, seq
                                    yp, sx, sr, si, sy, spool)
     if dev.type != "cuda":
         _on_gpu(dev)
-    nws = _tokens_gated_bytes(T, D) if seq_start is not None else 0
+    nws = _tokens_gated_bytes(code, T, D, S) if seq_start is not None else 0
     ws, wp = _scratch(nws, dev)
     _launch(dev, lib().ssm_tokens_gated, args, wp, nws)
     return out

@@ -198,18 +198,14 @@ template <int LANES> struct RowOf {
     }
 };
 
-template <typename T, int LANES>
-__global__ __launch_bounds__(threads_of(LANES)) void gated_fwd_kernel(GatedParams p) {
-    constexpr int NW = LANES > 64 ? LANES / 64 : 1, TILE = LANES * kRun;
-    __shared__ WaveMaps<NW> maps;
-    const RowOf<LANES> at(p.B, p.D);
-    if (LANES == 64 && !at.live) return;
+template <typename T, int LANES, bool SLOW, int NW>
+__device__ __forceinline__ void gated_fwd(const GatedParams& p, const RowOf<LANES>& at, const GateChannel& c, WaveMaps<NW>& maps) {
+    constexpr int TILE = LANES * kRun;
     const T* const x = (const T*)p.x + at.b * p.sx[0] + at.d * p.sx[1];
     const T* const r = (const T*)p.r + at.b * p.sr[0] + at.d * p.sr[1];
     const T* const g = (const T*)p.i + at.b * p.si[0] + at.d * p.si[1];
     T* const y = (T*)p.y + at.b * p.sy[0] + at.d * p.sy[1];
     float* const ck = p.ckpt_out + (int64_t)at.row * p.nchunk;
-    const GateChannel c = gate_channel(p.lam, p.rb, p.ib, p.power, at.d);
     const int L = p.L;
     const bool tiny = L < kRun;
     float carry = p.h0 ? p.h0[at.row] : 0.0f;
@@ -230,9 +226,9 @@ __global__ __launch_bounds__(threads_of(LANES)) void gated_fwd_kernel(GatedParam
         load_run_at(ri, g, next, tiny);
 #pragma unroll
         for (int j = 0; j < kRun; ++j) {
-            const float q = c.rate * gate_open(rv[j], c.rb);
-            a[j] = gate_decay(q);
-            b[j] = __builtin_amdgcn_sqrtf(gate_rest(q, a[j])) * gate_open(iv[j], c.ib) * xv[j];
+            const float t = c.rate * gate_open(rv[j], c.rb);
+            const float v = SLOW ? gate_rest<true>(t, a[j]) : gate_rest<false>(t, a[j]);
+            b[j] = __builtin_amdgcn_sqrtf(v) * (gate_open(iv[j], c.ib) * xv[j]);
         }
         if (t0 + TILE > L) {
 #pragma unroll
@@ -264,12 +260,9 @@ __global__ __launch_bounds__(threads_of(LANES)) void gated_fwd_kernel(GatedParam
     if (p.h_last && at.l == 0 && at.live) p.h_last[at.row] = carry;
 }
 
-template <typename T, int LANES>
-__global__ __launch_bounds__(threads_of(LANES)) void gated_bwd_kernel(GatedParams p) {
-    constexpr int NW = LANES > 64 ? LANES / 64 : 1, TILE = LANES * kRun;
-    __shared__ WaveMaps<NW> maps;
-    const RowOf<LANES> at(p.B, p.D);
-    if (LANES == 64 && !at.live) return;
+template <typename T, int LANES, bool SLOW, int NW>
+__device__ __forceinline__ void gated_bwd(const GatedParams& p, const RowOf<LANES>& at, const GateChannel& c, WaveMaps<NW>& maps) {
+    constexpr int TILE = LANES * kRun;
     const T* const x = (const T*)p.x + at.b * p.sx[0] + at.d * p.sx[1];
     const T* const r = (const T*)p.r + at.b * p.sr[0] + at.d * p.sr[1];
     const T* const g = (const T*)p.i + at.b * p.si[0] + at.d * p.si[1];
@@ -278,7 +271,7 @@ __global__ __launch_bounds__(threads_of(LANES)) void gated_bwd_kernel(GatedParam
     T* const gr = (T*)p.gr + at.b * p.sgr[0] + at.d * p.sgr[1];
     T* const gi = (T*)p.gi + at.b * p.sgi[0] + at.d * p.sgi[1];
     const float* const ck = p.ckpt + (int64_t)at.row * p.nchunk;
-    const GateChannel c = gate_channel(p.lam, p.rb, p.ib, p.power, at.d);
+    const float rate = c.rate * kLn2;
     const int L = p.L;
     const bool tiny = L < kRun;
     float carry = p.gh_last ? p.gh_last[at.row] : 0.0f;   // a mu of the step after the tile's last
@@ -310,9 +303,7 @@ __global__ __launch_bounds__(threads_of(LANES)) void gated_bwd_kernel(GatedParam
         for (int j = 0; j < kRun; ++j) {
             rho[j] = gate_open(rho[j], c.rb);
             iota[j] = gate_open(iota[j], c.ib);
-            const float q = c.rate * rho[j];
-            a[j] = gate_decay(q);
-            const float v = gate_rest(q, a[j]);
+            const float v = SLOW ? gate_rest<true>(c.rate * rho[j], a[j]) : gate_rest<false>(c.rate * rho[j], a[j]);
             rs[j] = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));   // 1 / beta, finite where a gate is shut
             beta[j] = v * rs[j];
         }
@@ -357,7 +348,7 @@ __global__ __launch_bounds__(threads_of(LANES)) void gated_bwd_kernel(GatedParam
             const float m = gv[j] + mu;
             mu = a[j] * m;
             const float u = iota[j] * xv[j], gu = m * beta[j];
-            const float q = c.rate * rho[j];
+            const float q = rate * rho[j];
             // E = m a (q / beta a u - q h); q / beta first, which stays below 1 + q where 1 / beta grows
             const float E = mu * fmaf(a[j] * u, q * rs[j], -q * hp[j]);
             const float er = E * (1.0f - rho[j]), ei = gu * u * (1.0f - iota[j]);
@@ -411,6 +402,24 @@ __global__ __launch_bounds__(threads_of(LANES)) void gated_bwd_kernel(GatedParam
     }
 }
 
+template <typename T, int LANES, bool BWD>
+__global__ __launch_bounds__(threads_of(LANES)) void gated_kernel(GatedParams p) {
+    constexpr int NW = LANES > 64 ? LANES / 64 : 1;
+    __shared__ WaveMaps<NW> maps;
+    const RowOf<LANES> at(p.B, p.D);
+    if (LANES == 64 && !at.live) return;
+    const GateChannel c = gate_channel(p.lam, p.rb, p.ib, p.power, at.d);
+    // (a workgroup of several waves has one row, so its waves go the same way)
+    const bool slow = __ballot(!(c.rate < kGateSlow)) == 0;
+    if (BWD) {
+        if (slow) gated_bwd<T, LANES, true, NW>(p, at, c, maps);
+        else gated_bwd<T, LANES, false, NW>(p, at, c, maps);
+    } else {
+        if (slow) gated_fwd<T, LANES, true, NW>(p, at, c, maps);
+        else gated_fwd<T, LANES, false, NW>(p, at, c, maps);
+    }
+}
+
 // Sums of the rows' parts over the batch, in a fixed order: 16 waves of 64 channels take the batch rows in turn.
 constexpr int kSumWaves = 16;
 __global__ __launch_bounds__(64 * kSumWaves) void gated_sum_kernel(GatedParams p) {
@@ -438,8 +447,8 @@ template <typename T, int LANES>
 hipError_t launch(const GatedParams& p, bool bwd, hipStream_t st) {
     constexpr int TH = threads_of(LANES);
     const unsigned blocks = (unsigned)(((int64_t)p.B * p.D + TH / LANES - 1) / (TH / LANES));
-    if (bwd) gated_bwd_kernel<T, LANES><<<blocks, TH, 0, st>>>(p);
-    else gated_fwd_kernel<T, LANES><<<blocks, TH, 0, st>>>(p);
+    if (bwd) gated_kernel<T, LANES, true><<<blocks, TH, 0, st>>>(p);
+    else gated_kernel<T, LANES, false><<<blocks, TH, 0, st>>>(p);
     return hipGetLastError();
 }
 template <typename T>

@@ -354,8 +354,9 @@ struct GatedParams {
     float power;
     int B, D, L, nchunk, lanes, sums;   // lanes of a row: 16, 64, 256 or 1024
 };
-// waves the lanes of a row are chosen for: four on each of the 1024 SIMDs
-constexpr int kGatedWaves = 4096;
+// Waves the lanes of a row are chosen for: 16 on each of the 1024 SIMDs.  B=8 D=2048 L=4096 bf16, forward and backward:
+// 4096 waves of 16 lanes a row 141 and 195 us, 16384 of 64 lanes 123 and 186, 65536 of 256 lanes 117 and 207.
+constexpr int kGatedWaves = 16384;
 hipError_t launch_gated(const GatedParams& p, bool bwd, int dtype, hipStream_t st);
 hipError_t launch_gated_sum(const GatedParams& p, hipStream_t st);   // glam, grb, gib from part
 struct TokGatedParams {
@@ -365,15 +366,17 @@ struct TokGatedParams {
     int64_t sx, sr, si, sy, spool;
     float power;
     int D;
-    // prompts: ranges of `rows` rows (the last may be shorter); workspace, per range and channel
-    int rows, nrange, joined;
-    float *h0, *hsum, *dsum;         // of the sequence that crosses a range's end: its first state if it begins there, its
-                                     // state at the end of the range, and the sum of its q in the range
-    int* through;                    // (nrange - 1) whether it runs through the whole range
+    // prompts: tiles of kGatedTile rows; workspace
+    int tiles, columns;              // columns: of 64 lanes' channels
+    uint64_t* maps;                  // (tiles, D) maps of the tiles' rows, then (tiles, D) words of 32 bits: the states at
+                                     // the tiles' ends
+    int* ticket;                     // (columns) tiles taken
+    int* slots;                      // (S) the sequences' slots, -1 for empty places
 };
-constexpr int kTokGatedWaves = 4096;   // waves the ranges are made for
-hipError_t launch_tok_gated(const TokGatedParams& p, int dtype, bool sum, hipStream_t st);
-hipError_t launch_tok_gated_join(const TokGatedParams& p, hipStream_t st);
+constexpr int kGatedTile = 128;
+template <int DTYPE> constexpr int kGatedFew = DTYPE == 1 ? 2 : 1;   // channels of a lane: two of bf16, one of fp32
+hipError_t launch_tok_gated_plan(const TokGatedParams& p, hipStream_t st);
+hipError_t launch_tok_gated(const TokGatedParams& p, int dtype, hipStream_t st);
 hipError_t launch_tok_gated_step(const TokGatedParams& p, int dtype, hipStream_t st);
 
 // ------------------------------- group norm ---------------------------------

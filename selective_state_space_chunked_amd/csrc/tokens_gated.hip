@@ -1,10 +1,17 @@
 // The gated linear recurrence (gated.hpp) over packed rows, with a pool of states.
 //
-// Prompts.  A lane holds four channels, so a wave walks 256 channels down a range of rows and reads the streams
-// along the channels, as the projections write them.  Few long sequences do not fill the GPU, so the rows are cut
-// into ranges whatever the sequences' lengths: a first pass leaves, for the sequence that crosses the end of each
-// range, its state there (from zero where it runs through the whole range) and the sum of its q; the states between
-// ranges are composed, h <- e^(-sum q) h + S, and the second pass walks every range from the state that enters it.
+// Prompts, in one pass.  A workgroup takes a tile of 128 rows and 64 lanes' channels, each of its eight waves 16 of the
+// rows: the streams are read once, along the channels as the projections write them, and what the gates make of them,
+// a and b of h <- a h + b, stays in registers.  Where a sequence begins, its first state goes into b and
+// nothing comes in from the row before, nor does it where no sequence owns a row: so from there on the rows are one
+// recurrence, whatever the sequences' lengths.
+// Waves compose their rows' maps, the workgroup its waves' through LDS, and tiles theirs through memory: a tile leaves
+// the map of its rows as soon as it has it (for each channel one word of 64 bits, so that no reader sees half of it), the
+// state at its end as soon as it knows that, and reads the tiles before its own, from the last one back, up to one whose
+// state is there.  The tiles of the same
+// channels are taken in the order of a counter, so a workgroup waits only for ones that run already, and for
+// nothing that these wait for; all the same the wait is bounded, and gives NaN where the bound is reached.
+//
 // Single tokens: a row a sequence, four channels a lane.
 #include <algorithm>
 
@@ -13,278 +20,343 @@
 namespace ssm {
 namespace {
 
-constexpr int kGrp = 4;   // rows loaded together
-constexpr int kCh = 4;    // channels of a lane
+constexpr int kTileWaves = 8, kWaveRows = kGatedTile / kTileWaves;
+constexpr uint32_t kNone = 0xffffffffu;   // a word that is not there yet; of the NaNs that a state may be, not one
+constexpr int kPolls = 1 << 20;           // a second and more
 
-// A lane's channels.  EVEN: all four are channels of the layer, or (past the last one, where D is a multiple of four)
-// the last four again, whose results go nowhere; otherwise the first n, one by one.
-template <typename T, bool EVEN>
-struct GatedLane {
-    const T *x, *r, *i;
-    T* y;
-    int64_t sx, sr, si, sy;
-    int n;
-    bool live;
-    GateChannel c[kCh];
-    float h[kCh], qsum[kCh];
-    Vec<T> vx[kGrp], vr[kGrp], vi[kGrp];
+__device__ __forceinline__ uint32_t word_of(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return u == kNone ? 0x7fc00000u : u;
+}
+template <typename W> __device__ __forceinline__ void put_word(W* p, W v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename W> __device__ __forceinline__ W get_word(const W* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 
-    __device__ __forceinline__ GatedLane(const TokGatedParams& p, int d0) {
-        live = d0 < p.D;
-        n = max(0, min(kCh, p.D - d0));
-        const int d = EVEN ? min(d0, p.D - kCh) : min(d0, p.D - 1);
-        x = (const T*)p.x + d; r = (const T*)p.r + d; i = (const T*)p.i + d; y = (T*)p.y + d;
-        sx = p.sx; sr = p.sr; si = p.si; sy = p.sy;
-#pragma unroll
-        for (int e = 0; e < kCh; ++e) {
-            c[e] = gate_channel(p.lam, p.rb, p.ib, p.power, EVEN ? d + e : min(d + e, p.D - 1));
-            h[e] = qsum[e] = 0.0f;
-        }
+// Before the tiles: no words, no tiles taken, and each sequence's slot, or -1 for an empty place.
+__global__ __launch_bounds__(256) void tok_gated_plan_kernel(TokGatedParams p, int64_t words) {
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
+    for (int64_t i = id; i < words; i += all) p.maps[i] = ~0ull;
+    for (int64_t i = id; i < p.columns; i += all) p.ticket[i] = 0;
+    for (int64_t s = id / 64; s < p.q.S; s += all / 64) {
+        const int v = slot_of(p.q, (int)s);
+        if (lane_id() == 0) p.slots[s] = v;
     }
-    __device__ __forceinline__ void get(const float* at) {   // the state, from its first channel's place
-        Vec<float> v;
-        if (EVEN) v.load(at); else v.load(at, n);
-        v.get(h);
+}
+
+// Two channels of bf16 or one of fp32: 256 or 128 .. bytes of a row a wave.  EVEN: the lane's channels are all channels of
+// the layer, or, past the last one, the last ones again, whose results go nowhere; otherwise one by one.
+template <typename T> struct Few;
+template <> struct Few<bf16_t> {
+    static constexpr int V = kGatedFew<1>;
+    typedef uint32_t raw __attribute__((aligned(2)));
+    uint32_t r;
+    template <bool EVEN> __device__ __forceinline__ void load(const bf16_t* row, int d, int D) {
+        if (EVEN) r = *reinterpret_cast<const raw*>(row + d);
+        else r = (uint32_t)row[min(d, D - 1)] | (uint32_t)row[min(d + 1, D - 1)] << 16;
     }
-    __device__ __forceinline__ void put(float* at, const float (&s)[kCh]) const {
-        Vec<float> v;
-        v.set(s);
+    __device__ __forceinline__ float get(int e) const { return __uint_as_float(e ? r & 0xffff0000u : r << 16); }
+    template <bool EVEN> __device__ __forceinline__ static void store(bf16_t* row, int d, int n, const float (&v)[2]) {
         if (EVEN) {
-            if (live) v.store(at);
+            if (n > 0) *reinterpret_cast<raw*>(row + d) = (uint32_t)to_stream<bf16_t>(v[0]) | (uint32_t)to_stream<bf16_t>(v[1]) << 16;
         } else {
-            v.store(at, n);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (e < n) row[d + e] = to_stream<bf16_t>(v[e]);
         }
     }
-    __device__ __forceinline__ void load(int g, int t) {
-        if (EVEN) {
-            vx[g].load(x + t * sx);
-            vr[g].load(r + t * sr);
-            vi[g].load(i + t * si);
-        } else {
-            vx[g].load(x + t * sx, n);
-            vr[g].load(r + t * sr, n);
-            vi[g].load(i + t * si, n);
-        }
+};
+template <> struct Few<float> {
+    static constexpr int V = kGatedFew<0>;
+    float r;
+    template <bool EVEN> __device__ __forceinline__ void load(const float* row, int d, int D) { r = row[min(d, D - 1)]; }
+    __device__ __forceinline__ float get(int) const { return r; }
+    template <bool EVEN> __device__ __forceinline__ static void store(float* row, int d, int n, const float (&v)[1]) {
+        if (n > 0) row[d] = v[0];
     }
-    template <bool OUT>
-    __device__ __forceinline__ void row(const Vec<T>& wx, const Vec<T>& wr, const Vec<T>& wi, int t) {
-        float xv[kCh], rv[kCh], iv[kCh];
-        wx.get(xv);
-        wr.get(rv);
-        wi.get(iv);
-#pragma unroll
-        for (int e = 0; e < kCh; ++e) {
-            const float q = c[e].rate * gate_open(rv[e], c[e].rb);
-            const float a = gate_decay(q);
-            const float b = __builtin_amdgcn_sqrtf(gate_rest(q, a)) * gate_open(iv[e], c[e].ib) * xv[e];
-            h[e] = fmaf(a, h[e], b);
-            if (!OUT) qsum[e] += q;
-        }
-        if (OUT) {
-            Vec<T> o;
-            o.set(h);
-            if (EVEN) {
-                if (live) o.store(y + t * sy);
-            } else {
-                o.store(y + t * sy, n);
-            }
-        }
-    }
-    // rows [t0, t1), t0 < t1, with the next group's loads under way
-    template <bool OUT>
-    __device__ __forceinline__ void walk(int t0, int t1) {
-#pragma unroll
-        for (int g = 0; g < kGrp; ++g) load(g, min(t0 + g, t1 - 1));
-        for (int t = t0; t < t1; t += kGrp) {
-            Vec<T> wx[kGrp], wr[kGrp], wi[kGrp];
-#pragma unroll
-            for (int g = 0; g < kGrp; ++g) {
-                wx[g] = vx[g];
-                wr[g] = vr[g];
-                wi[g] = vi[g];
-            }
-#pragma unroll
-            for (int g = 0; g < kGrp; ++g) load(g, min(t + kGrp + g, t1 - 1));
-            if (t + kGrp <= t1) {
-#pragma unroll
-                for (int g = 0; g < kGrp; ++g) row<OUT>(wx[g], wr[g], wi[g], t + g);
-            } else {
-#pragma unroll
-                for (int g = 0; g < kGrp; ++g)
-                    if (t + g < t1) row<OUT>(wx[g], wr[g], wi[g], t + g);
+};
+
+// What a wave's rows are, in lane j that of row j: the slot of the sequence that owns it (-1: none), whether the row is
+// its first one, its last one, and whether it begins with zeros.
+struct RowInfo {
+    int slot = -1, first = 0, last = 0, fresh = 0;
+    RowInfo() = default;
+    __device__ __forceinline__ RowInfo(const TokGatedParams& p, const SeqTable& q, int r0) {
+        const int t = r0 + lane_id(), end = min(r0 + kWaveRows, p.q.T);
+        int s = max(q.find(r0), 0);
+        for (; s < p.q.S; ++s) {
+            const int st = q.first(s);
+            if (st >= end) break;
+            const int en = q.end(s);
+            if (st < 0 || en <= max(st, r0)) continue;
+            const int v = uniform(p.slots[s]);
+            const bool f = q.fresh(s);
+            if (t >= st && t < min(en, end)) {
+                slot = v;
+                first = t == st;
+                last = t == en - 1;
+                fresh = f;
             }
         }
     }
 };
 
-struct Rows {
-    int r0, r1;
+// The waves' maps, whether a wave's map forgets what comes in, and the state that comes into the tile.
+template <int V> struct TileMaps {
+    float P[kTileWaves][64 * V], S[kTileWaves][64 * V], carry[64 * V];
+    int cut[kTileWaves];
 };
-__device__ __forceinline__ Rows rows_of(const TokGatedParams& p, int c) {
-    const int r0 = c * p.rows;
-    return {r0, min(r0 + p.rows, p.q.T)};
-}
 
-// First pass, ranges 0 .. nrange-2: what the sequence that crosses the range's end does there.
-template <typename T, bool EVEN>
-__device__ __forceinline__ void sum_range(const TokGatedParams& p, int c, int d0, int s, int st, int slot, bool fresh) {
-    const Rows r = rows_of(p, c);
-    const int64_t at = (int64_t)c * p.D + d0;
-    GatedLane<T, EVEN> l(p, d0);
-    if (st >= r.r0) {   // it begins here: its first state, kept for the second pass (which may find it overwritten)
-        if (!fresh) l.get(p.pool + slot * p.spool + (EVEN ? min(d0, p.D - kCh) : d0));
-        l.put(p.h0 + at, l.h);
+template <typename T, bool EVEN, bool SLOW>
+__device__ __forceinline__ void gated_tile(const TokGatedParams& p, int tile, int d0, const GateChannel (&c)[Few<T>::V],
+                                           const SeqTable& seqs, TileMaps<Few<T>::V>& maps) {
+    constexpr int V = Few<T>::V, R = kWaveRows;
+    const int l = lane_id(), w = uniform(threadIdx.x >> 6), r0 = tile * kGatedTile + w * R;
+    const int d = d0 + V * l, at = EVEN ? min(d, p.D - V) : d, n = max(0, min(V, p.D - d));
+    float a[R][V], b[R][V];
+    RowInfo info;
+    {
+        Few<T> x[R], r[R], g[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const int t = min(r0 + j, p.q.T - 1);
+            x[j].template load<EVEN>((const T*)p.x + t * p.sx, at, p.D);
+            r[j].template load<EVEN>((const T*)p.r + t * p.sr, at, p.D);
+            g[j].template load<EVEN>((const T*)p.i + t * p.si, at, p.D);
+        }
+        info = RowInfo(p, seqs, r0);   // while the rows come
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float v = gate_rest<SLOW>(c[e].rate * gate_open(r[j].get(e), c[e].rb), a[j][e]);
+                b[j][e] = __builtin_amdgcn_sqrtf(v) * (gate_open(g[j].get(e), c[e].ib) * x[j].get(e));
+            }
+        }
     }
-    l.template walk<false>(max(st, r.r0), r.r1);
-    l.put(p.hsum + at, l.h);
-    l.put(p.dsum + at, l.qsum);
-}
-template <typename T>
-__global__ __launch_bounds__(256) void tok_gated_sum_kernel(TokGatedParams p, int cblocks) {
-    const int d0 = ((blockIdx.x % cblocks) * 4 + uniform(threadIdx.x >> 6)) * 64 * kCh;
-    const int c = blockIdx.x / cblocks;
-    if (d0 >= p.D) return;
-    const Rows r = rows_of(p, c);
-    const SeqTable q(p.q);
-    const int s = q.find(r.r1 - 1);
-    int st = 0, slot = -1;
-    if (s >= 0 && s < p.q.S) {
-        st = q.first(s);
-        if (st >= 0 && st < r.r1 && q.end(s) > r.r1) slot = q.slot(s);   // st beyond: the list does not ascend
-    }
-    if (d0 == 0 && lane_id() == 0) p.through[c] = slot >= 0 && st < r.r0;
-    if (slot < 0) return;   // none crosses the end
-    const bool fresh = q.fresh(s);
-    const int d = d0 + lane_id() * kCh;
-    if (p.D % kCh == 0 || d0 + 64 * kCh <= p.D) sum_range<T, true>(p, c, d, s, st, slot, fresh);
-    else sum_range<T, false>(p, c, d, s, st, slot, fresh);
-}
-
-// The states at the ranges' ends from what each range leaves alone, where there are more than kTokChain of them: a
-// workgroup takes 64 channels, its 16 waves the ranges in runs of PER; each composes its run, then the runs before its
-// own, and goes over its ranges again.
-constexpr int kRuns = 16, PER = 16;
-__global__ __launch_bounds__(64 * kRuns) void tok_gated_join_kernel(TokGatedParams p) {
-    __shared__ float end_[kRuns][64], decay_[kRuns][64];
-    const int lane = lane_id(), w = uniform(threadIdx.x >> 6);
-    const int d = min((int)blockIdx.x * 64 + lane, p.D - 1);
-    const int ends = p.nrange - 1;
-    float* const S = p.hsum + d;
-    float carry = 0.0f;
-    for (int base = 0; base < ends; base += kRuns * PER) {
-        const int k0 = base + w * PER;
-        float s[PER], e[PER];
-        int f[PER];
+    // cut: rows that nothing comes into from the row before.  They are chosen, not multiplied by 0: a sequence's NaN or
+    // infinity stays its own.
+    const uint32_t owned = (uint32_t)__ballot(info.slot >= 0), first = (uint32_t)__ballot(info.first != 0) & owned;
+    const uint32_t cut = first | (~owned & ((1u << R) - 1));
+    if (cut) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int j = min(k0 + i, ends - 1);
-            s[i] = S[(int64_t)j * p.D];
-            e[i] = p.dsum[(int64_t)j * p.D + d];
-            f[i] = p.through[j];
-        }
-        // the run as a map: through a run with a beginning in it nothing comes (decay -1)
-        float h = 0.0f, decay = 1.0f;
-        bool all = true;
+        for (int j = 0; j < R; ++j) {
+            if (!(owned >> j & 1)) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const bool has = k0 + i < ends;
-            e[i] = gate_decay(e[i]);
-            const float g = f[i] ? fmaf(e[i], h, s[i]) : s[i];
-            h = has ? g : h;
-            decay *= has ? e[i] : 1.0f;
-            all = all && (f[i] || !has);
-        }
-        end_[w][lane] = h;
-        decay_[w][lane] = all ? decay : -1.0f;
-        __syncthreads();
-        float in = carry;
-        for (int i = 0; i < w; ++i) {
-            const float q = decay_[i][lane];
-            in = q < 0.0f ? end_[i][lane] : fmaf(q, in, end_[i][lane]);
-        }
-        h = in;
+                for (int e = 0; e < V; ++e) b[j][e] = 0.0f;
+            } else if (first >> j & 1) {
+                const float* const h0 = p.pool + __builtin_amdgcn_readlane(info.slot, j) * p.spool;
+                if (!__builtin_amdgcn_readlane(info.fresh, j)) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            h = f[i] ? fmaf(e[i], h, s[i]) : s[i];
-            if (k0 + i < ends) S[(int64_t)(k0 + i) * p.D] = h;
-        }
-        for (int i = w; i < kRuns; ++i) {   // on to what the next turn begins with
-            const float q = decay_[i][lane];
-            in = q < 0.0f ? end_[i][lane] : fmaf(q, in, end_[i][lane]);
-        }
-        carry = in;
-        __syncthreads();
-    }
-}
-
-// Second pass: every row's output and every sequence's last state.
-template <typename T, bool EVEN>
-__device__ __forceinline__ void walk_range(const TokGatedParams& p, const SeqTable& q, int c, int d0, int s) {
-    const Rows r = rows_of(p, c);
-    GatedLane<T, EVEN> l(p, d0);
-    const int dc = EVEN ? min(d0, p.D - kCh) : d0;   // where the lane reads its states
-    for (; s < p.q.S; ++s) {
-        const int st = q.first(s);
-        if (st >= r.r1) break;
-        const int en = q.end(s);
-        if (st < 0 || en <= max(st, r.r0)) continue;
-        const int slot = q.slot(s);
-        if (slot < 0) continue;
-        float* const pool = p.pool + slot * p.spool;
-#pragma unroll
-        for (int e = 0; e < kCh; ++e) l.h[e] = 0.0f;
-        if (st < r.r0) {   // from the ranges before: the state that crosses into this one
-            const int k0 = p.joined ? c - 1 : st / p.rows;
-            l.get(p.hsum + (int64_t)k0 * p.D + dc);
-#pragma unroll 1
-            for (int k = k0 + 1; k < c; ++k) {
-                Vec<float> vs, vq;
-                if (EVEN) {
-                    vs.load(p.hsum + (int64_t)k * p.D + dc);
-                    vq.load(p.dsum + (int64_t)k * p.D + dc);
-                } else {
-                    vs.load(p.hsum + (int64_t)k * p.D + dc, l.n);
-                    vq.load(p.dsum + (int64_t)k * p.D + dc, l.n);
+                    for (int e = 0; e < V; ++e) b[j][e] = fmaf(a[j][e], h0[min(d + e, p.D - 1)], b[j][e]);
                 }
-                float S[kCh], Q[kCh];
-                vs.get(S);
-                vq.get(Q);
-#pragma unroll
-                for (int e = 0; e < kCh; ++e) l.h[e] = fmaf(gate_decay(Q[e]), l.h[e], S[e]);
             }
-        } else if (en > r.r1) {
-            l.get(p.h0 + (int64_t)c * p.D + dc);
-        } else if (!q.fresh(s)) {
-            l.get(pool + dc);
         }
-        l.template walk<true>(max(st, r.r0), min(en, r.r1));
-        if (en <= r.r1) l.put(pool + d0, l.h);
+    }
+    float P[V], S[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        P[e] = a[0][e];
+        S[e] = b[0][e];
+#pragma unroll
+        for (int j = 1; j < R; ++j) {
+            S[e] = cut >> j & 1 ? b[j][e] : fmaf(a[j][e], S[e], b[j][e]);
+            P[e] *= a[j][e];
+        }
+        maps.P[w][V * l + e] = P[e];
+        maps.S[w][V * l + e] = S[e];
+    }
+    if (l == 0) maps.cut[w] = cut != 0;
+    __syncthreads();
+    // the map of the rows of the workgroup before the wave's own; the first wave: of all, for the tiles behind
+    bool forgets = false;   // nothing comes through: S is a state
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        P[e] = 1.0f;
+        S[e] = 0.0f;
+    }
+    for (int k = 0; k < (w ? w : kTileWaves); ++k) {
+        const bool c = uniform(maps.cut[k]) != 0;
+        forgets |= c;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float m = maps.P[k][V * l + e], v = maps.S[k][V * l + e];
+            S[e] = c ? v : fmaf(m, S[e], v);
+            P[e] *= m;
+        }
+    }
+    if (w == 0) {
+        uint64_t* const map = p.maps + (int64_t)tile * p.D;
+        uint32_t* const state = (uint32_t*)(p.maps + (int64_t)p.tiles * p.D) + (int64_t)tile * p.D;
+        float C[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            C[e] = 0.0f;
+            if (e < n) {   // (into the first tile nothing comes)
+                if (tile == 0 || forgets) put_word(state + d + e, word_of(S[e]));
+                else put_word(map + d + e, (uint64_t)word_of(S[e]) << 32 | word_of(P[e]));
+            }
+        }
+        if (tile > 0 && !(cut & 1)) {   // otherwise no row takes what comes in
+            float Pa[V], Sa[V];
+            bool open[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                Pa[e] = 1.0f;
+                Sa[e] = 0.0f;
+                open[e] = e < n;
+            }
+            int k = tile - 1, polls = 0;
+            while (k >= 0) {
+                // the words of up to four tiles are under way together
+                constexpr int AHEAD = 4;
+                uint64_t m[AHEAD][V];
+                uint32_t h[AHEAD][V];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const int64_t o = (int64_t)(max(k - i, 0) - tile) * p.D + min(d + e, p.D - 1);
+                        m[i][e] = get_word(map + o);
+                        h[i][e] = get_word(state + o);
+                    }
+                bool wait = false;
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    if (k < 0 || wait) continue;
+                    bool none = false;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) none |= open[e] && h[i][e] == kNone && (uint32_t)m[i][e] == kNone;
+                    wait = __ballot(none) != 0;
+                    if (wait) continue;
+                    polls = 0;
+                    bool more = false;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        if (!open[e]) continue;
+                        const bool known = h[i][e] != kNone;
+                        Sa[e] = fmaf(Pa[e], __uint_as_float(known ? h[i][e] : (uint32_t)(m[i][e] >> 32)), Sa[e]);
+                        Pa[e] *= __uint_as_float((uint32_t)m[i][e]);
+                        open[e] = !known;
+                        more |= !known;
+                    }
+                    k = __ballot(more) ? k - 1 : -1;
+                }
+                if (wait) {
+                    if (++polls > kPolls) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) Sa[e] = __uint_as_float(0x7fc00000u);
+                        break;
+                    }
+                    __builtin_amdgcn_s_sleep(1);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                C[e] = Sa[e];
+                if (e < n && !forgets) put_word(state + d + e, word_of(fmaf(P[e], C[e], S[e])));
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            maps.carry[V * l + e] = C[e];
+            P[e] = 1.0f;
+            S[e] = 0.0f;
+        }
+    }
+    __syncthreads();
+    // the state that the wave's rows begin with
+    float h[V];
+    const bool through = w == 0 || !forgets;
+#pragma unroll
+    for (int e = 0; e < V; ++e) h[e] = through ? fmaf(P[e], maps.carry[V * l + e], S[e]) : S[e];
+    const uint32_t last = (uint32_t)__ballot(info.last != 0) & owned;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) h[e] = cut >> j & 1 ? b[j][e] : fmaf(a[j][e], h[e], b[j][e]);
+        if (owned >> j & 1) Few<T>::template store<EVEN>((T*)p.y + (r0 + j) * p.sy, at, n, h);
+        if (last >> j & 1) {
+            float* const pool = p.pool + __builtin_amdgcn_readlane(info.slot, j) * p.spool;
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (e < n) pool[d + e] = h[e];
+        }
     }
 }
 template <typename T>
-__global__ __launch_bounds__(256) void tok_gated_kernel(TokGatedParams p, int cblocks) {
-    const int d0 = ((blockIdx.x % cblocks) * 4 + uniform(threadIdx.x >> 6)) * 64 * kCh;
-    const int c = blockIdx.x / cblocks;
-    if (d0 >= p.D) return;
-    const Rows r = rows_of(p, c);
-    const SeqTable q(p.q);
-    const int s = q.find(r.r0);
-    if (s >= p.q.S) return;
-    const int d = d0 + lane_id() * kCh;
-    if (p.D % kCh == 0 || d0 + 64 * kCh <= p.D) walk_range<T, true>(p, q, c, d, max(s, 0));
-    else walk_range<T, false>(p, q, c, d, max(s, 0));
+__global__ __launch_bounds__(64 * kTileWaves, 4) void tok_gated_kernel(TokGatedParams p) {
+    constexpr int V = Few<T>::V;
+    __shared__ TileMaps<V> maps;
+    __shared__ int taken;
+    const int column = blockIdx.x % p.columns, d0 = column * 64 * V;
+    const SeqTable seqs(p.q);
+    if (threadIdx.x == 0) taken = __hip_atomic_fetch_add(p.ticket + column, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    GateChannel c[V];
+    bool fast = false;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        c[e] = gate_channel(p.lam, p.rb, p.ib, p.power, min(d0 + V * lane_id() + e, p.D - 1));
+        fast |= !(c[e].rate < kGateSlow);
+    }
+    const bool slow = __ballot(fast) == 0, even = p.D % V == 0 || d0 + 64 * V <= p.D;
+    __syncthreads();
+    const int tile = uniform(taken);
+    if (even && slow) gated_tile<T, true, true>(p, tile, d0, c, seqs, maps);
+    else if (even) gated_tile<T, true, false>(p, tile, d0, c, seqs, maps);
+    else gated_tile<T, false, false>(p, tile, d0, c, seqs, maps);
 }
 
-// One row a sequence.
+constexpr int kCh = 4;    // channels of a lane of the step kernel
+
+// One row a sequence.  EVEN: as above, of four channels a lane.
 template <typename T, bool EVEN>
 __device__ __forceinline__ void step_row(const TokGatedParams& p, int s, int slot, int d0) {
-    GatedLane<T, EVEN> l(p, d0);
-    float* const pool = p.pool + slot * p.spool;
-    l.load(0, s);
-    if (!(p.q.fresh && p.q.fresh[s])) l.get(pool + (EVEN ? min(d0, p.D - kCh) : d0));
+    const bool live = d0 < p.D;
+    const int n = max(0, min(kCh, p.D - d0)), d = EVEN ? min(d0, p.D - kCh) : min(d0, p.D - 1);
+    float* const pool = p.pool + slot * p.spool + d;
+    const T* const rows[3] = {(const T*)p.x + s * p.sx + d, (const T*)p.r + s * p.sr + d, (const T*)p.i + s * p.si + d};
+    Vec<T> v[3];
+    Vec<float> st;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        if (EVEN) v[k].load(rows[k]);
+        else v[k].load(rows[k], n);
+    }
+    if (EVEN) st.load(pool);
+    else st.load(pool, n);
+    const bool fresh = p.q.fresh && p.q.fresh[s];
+    GateChannel c[kCh];
+#pragma unroll
+    for (int e = 0; e < kCh; ++e) c[e] = gate_channel(p.lam, p.rb, p.ib, p.power, min(d + e, p.D - 1));
     if (slot_taken(p.q, s, slot)) return;
-    l.template row<true>(l.vx[0], l.vr[0], l.vi[0], s);
-    l.put(pool + d0, l.h);
+    float x[kCh], r[kCh], g[kCh], h[kCh];
+    v[0].get(x);
+    v[1].get(r);
+    v[2].get(g);
+    st.get(h);
+#pragma unroll
+    for (int e = 0; e < kCh; ++e) {
+        float a;
+        const float rest = gate_rest<false>(c[e].rate * gate_open(r[e], c[e].rb), a);
+        const float b = __builtin_amdgcn_sqrtf(rest) * (gate_open(g[e], c[e].ib) * x[e]);
+        h[e] = fresh ? b : fmaf(a, h[e], b);
+    }
+    Vec<T> o;
+    o.set(h);
+    st.set(h);
+    T* const y = (T*)p.y + s * p.sy + d;
+    if (EVEN) {
+        if (live) {
+            o.store(y);
+            st.store(pool);
+        }
+    } else {
+        o.store(y, n);
+        st.store(pool, n);
+    }
 }
 template <typename T>
 __global__ __launch_bounds__(256) void tok_gated_step_kernel(TokGatedParams p, int cblocks) {
@@ -300,20 +372,16 @@ __global__ __launch_bounds__(256) void tok_gated_step_kernel(TokGatedParams p, i
 
 }  // namespace
 
-hipError_t launch_tok_gated(const TokGatedParams& p, int dtype, bool sum, hipStream_t st) {
-    const int cblocks = (p.D + 256 * kCh - 1) / (256 * kCh);
-    const unsigned blocks = (unsigned)cblocks * (unsigned)(sum ? p.nrange - 1 : p.nrange);
-    if (sum) {
-        if (dtype) tok_gated_sum_kernel<bf16_t><<<blocks, 256, 0, st>>>(p, cblocks);
-        else tok_gated_sum_kernel<float><<<blocks, 256, 0, st>>>(p, cblocks);
-    } else {
-        if (dtype) tok_gated_kernel<bf16_t><<<blocks, 256, 0, st>>>(p, cblocks);
-        else tok_gated_kernel<float><<<blocks, 256, 0, st>>>(p, cblocks);
-    }
+hipError_t launch_tok_gated_plan(const TokGatedParams& p, hipStream_t st) {
+    const int64_t words = (int64_t)p.tiles * p.D + ((int64_t)p.tiles * p.D + 1) / 2;
+    const int64_t blocks = std::max<int64_t>((words + 511) / 512, (p.q.S + 3) / 4);
+    tok_gated_plan_kernel<<<(unsigned)std::min<int64_t>(blocks, 4096), 256, 0, st>>>(p, words);
     return hipGetLastError();
 }
-hipError_t launch_tok_gated_join(const TokGatedParams& p, hipStream_t st) {
-    tok_gated_join_kernel<<<(unsigned)((p.D + 63) / 64), 64 * kRuns, 0, st>>>(p);
+hipError_t launch_tok_gated(const TokGatedParams& p, int dtype, hipStream_t st) {
+    const unsigned blocks = (unsigned)p.columns * (unsigned)p.tiles;
+    if (dtype) tok_gated_kernel<bf16_t><<<blocks, 64 * kTileWaves, 0, st>>>(p);
+    else tok_gated_kernel<float><<<blocks, 64 * kTileWaves, 0, st>>>(p);
     return hipGetLastError();
 }
 hipError_t launch_tok_gated_step(const TokGatedParams& p, int dtype, hipStream_t st) {

@@ -305,6 +305,47 @@ def test_tokens_gated_thousands_of_sequences():
               [bool(v) for v in r.random(1500) < 0.5], 1600, "bf16", r)
 
 
+def test_tokens_gated_non_finite_values_stay_in_their_sequence():
+    """A NaN or an infinity, in a row or in a state, reaches the later rows of its sequence and no other one, inside a
+    tile of rows, across tiles and across rows that no sequence owns."""
+    r = gen(15)
+    T, D = 700, 70
+    start, slot = [0, 5, 20, 310, 320, 600, 690], [0, 1, 2, -1, 3, 4]
+    t = tok_inputs(T, D, "f32", r)
+    at = dict(seq_start=torch.tensor(start, dtype=torch.int32, device=DEV),
+              slot=torch.tensor(slot, dtype=torch.int32, device=DEV))
+    first = dev(r.normal(size=(5, D)))
+    pool = first.clone()
+    ref = ssm.tokens_gated(pool=pool, out={"y": torch.zeros(T, D, device=DEV)}, **at, **t)["y"]
+    for name, row, v in (("x", 25, float("inf")), ("r", 2, float("nan")), ("i", 300, float("nan")), ("r", 315, float("nan")),
+                         ("x", 599, float("nan")), ("pool", 2, float("nan")), ("pool", 3, float("-inf")), ("r", 695, float("nan"))):
+        u, p = dict(t), first.clone()
+        if name == "pool":
+            p[row] = v
+            row, seq = start[row if row < 3 else 4], row if row < 3 else 4
+        else:
+            u[name] = t[name].clone()
+            u[name][row] = v
+            seq = max(k for k in range(6) if start[k] <= row)
+        y = ssm.tokens_gated(pool=p, out={"y": torch.zeros(T, D, device=DEV)}, **at, **u)["y"]
+        own = torch.zeros(T, dtype=torch.bool, device=DEV)
+        if slot[seq] >= 0 and row < start[6]:
+            own[row:start[seq + 1]] = True
+            assert not torch.isfinite(y[own]).any() and not torch.isfinite(p[slot[seq]]).any(), (name, row)
+            p[slot[seq]] = pool[slot[seq]]
+        assert torch.equal(y[~own], ref[~own]) and torch.equal(p, pool), (name, row)
+
+
+def test_tokens_gated_slow_channels_over_many_tiles():
+    """Channels that keep what they have, so that what a row brings is handed on from tile to tile to the last row, and
+    many tiles of few channels, whose workgroups run at the same time."""
+    r = gen(16)
+    for T, D in ((20000, 3), (3000, 200)):
+        t = tok_inputs(T, D, "f32", r)
+        t["lam"] = dev(np.full(D, -14.0))
+        tok_check(t, [0, T - 5, T], [1, 0], [False, True], 2, "f32", r)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("S,D,view", [(1, 1, False), (3, 7, True), (64, 260, False), (130, 1030, True)])
 def test_tokens_gated_step(S, D, view, dtype):
