@@ -388,10 +388,10 @@ struct NormParams {
     float eps, inv;                  // inv = 1 / Cg
     int T, C, G, Cg, silu, sums;
     int team, V, R, P;               // lanes of a team, channels of a vector, vectors of a lane, lanes of a group
-    int gblocks, chunks, per;        // teams' groups of a row; runs of `per` rows
+    int gblocks, chunks;             // teams' groups of a row; workgroups that share its rows
 };
 constexpr int kNormMost = 8192;   // channels of a group: 1024 lanes of eight
-constexpr int kNormWG = 1024;     // workgroups the rows are divided over
+constexpr int kNormWG = 512;     // workgroups the rows are divided over
 hipError_t launch_norm_fwd(const NormParams& p, int dtype, hipStream_t st);
 hipError_t launch_norm_bwd(const NormParams& p, int dtype, hipStream_t st);
 hipError_t launch_norm_sum(const NormParams& p, hipStream_t st);

@@ -73,6 +73,18 @@ __device__ __forceinline__ void channels4(const Mm8Params& p, int n0, float (&sw
     }
 }
 
+// 16 or 4 bytes of every lane's address, one lane's after the other's, to a place in LDS (no register takes the data).
+// Of the builtins for it the compiler waits for all before the next read of LDS, the step's own among them, whatever part
+// of LDS is read; these are waited for by wait_barrier alone.
+__device__ __forceinline__ uint32_t lds_place(const void* p) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p);
+}
+__device__ __forceinline__ void to_lds16(const void* from, const void* to) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds_place(to)) : "memory", "m0");
+}
+__device__ __forceinline__ void to_lds4(const void* from, const void* to) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(lds_place(to)) : "memory", "m0");
+}
 // Few rows: bound by reading the weights once.  A workgroup takes 16 channels and 16 TT rows, its waves the k of a row in
 // turns of 128 bytes -- whole lines of the weights -- and the waves' sums are added in LDS.
 constexpr int kFewStep = 128;
@@ -142,6 +154,67 @@ __global__ __launch_bounds__(64 * kFewWaves) void mm8_few_kernel(Mm8Params p) {
     i4 s(0);
     for (int v = 0; v < waves; ++v) s += part[v][w][l];
     finish4<T>(p, s, t0 + 16 * w + l % 16, n, sw, bias);
+}
+
+// The same for rows aligned to 16 bytes and K a multiple of 128: a wave's steps come by loads of whole lines to LDS (a
+// line by eight neighbouring lanes; as the matrix instructions hold them, every lane's 16 bytes are a request of their
+// own, 64 x 4096 x 2048: 8.7 us), two steps under way.  The waves' stages are their own, so there is no barrier
+// before the sums.
+constexpr int kFewDirect = 8;   // waves
+template <typename T, int TT>
+__global__ __launch_bounds__(64 * kFewDirect) void mm8_few_direct_kernel(Mm8Params p) {
+    constexpr int ROWS = 16 + 16 * TT, LD = ROWS / 8;
+    __shared__ __align__(16) i4 lds[kFewDirect][2][ROWS * 8];
+    const int l = lane_id(), w = uniform(threadIdx.x >> 6), steps = p.K / kFewStep;
+    const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 16 * TT;
+    const int8_t* src[LD];
+#pragma unroll
+    for (int j = 0; j < LD; ++j) {
+        const int r = 8 * j + l / 8;
+        src[j] = (j < 2 ? p.w + (int64_t)min(n0 + r, p.N - 1) * p.sw : p.x + (int64_t)min(t0 + r - 16, p.T - 1) * p.sx) +
+                 ((l % 8) ^ (r / 2 % 8)) * 16;   // chunk c of row r lies at c ^ r / 2 % 8
+    }
+    auto load = [&](int k, int stage) {
+#pragma unroll
+        for (int j = 0; j < LD; ++j) to_lds16(src[j] + (int64_t)k * kFewStep, &lds[w][stage][64 * j]);
+    };
+    i4 acc[TT];
+#pragma unroll
+    for (int i = 0; i < TT; ++i) acc[i] = i4(0);
+    if (w < steps) load(w, 0);
+    if (w + kFewDirect < steps) load(w + kFewDirect, 1);
+    const int r = l % 16, sw = r / 2 % 8;
+    int stage = 0;
+    for (int k = w; k < steps; k += kFewDirect, stage ^= 1) {
+        if (k + kFewDirect < steps) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LD) : "memory");   // the next step may be under way
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        i4 a[2], b[2][TT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const i4* const at = lds[w][stage] + r * 8 + ((4 * h + l / 16) ^ sw);
+            a[h] = at[0];
+#pragma unroll
+            for (int i = 0; i < TT; ++i) b[h][i] = at[128 * (i + 1)];
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage is read
+        if (k + 2 * kFewDirect < steps) load(k + 2 * kFewDirect, stage);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < TT; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[h], b[h][i], acc[i], 0, 0, 0);
+    }
+    i4* const part = lds[w][0];   // the wave's own: nothing is under way to it
+#pragma unroll
+    for (int i = 0; i < TT; ++i) part[64 * i + l] = acc[i];
+    const int n = n0 + 4 * (l / 16);
+    float scale[4], bias[4];
+    if (w < TT) channels4(p, n, scale, bias);
+    __syncthreads();
+    if (w >= TT) return;
+    i4 s(0);
+#pragma unroll
+    for (int v = 0; v < kFewDirect; ++v) s += lds[v][0][64 * w + l];
+    finish4<T>(p, s, t0 + 16 * w + l % 16, n, scale, bias);
 }
 
 // What a tile's results are scaled with, in LDS (places past the last one: the last one's).
@@ -281,18 +354,6 @@ __global__ __launch_bounds__(64 * WN * WT) void mm8_tile_kernel(Mm8Params p, int
 // LDS directly, a step ahead of the products, and one barrier a step.  A workgroup
 // goes on from tile to tile: the next tile's first step comes while a tile's results go out.
 constexpr int kDirectStep = 128;
-// 16 or 4 bytes of every lane's address, one lane's after the other's, to a place in LDS (no register takes the data).
-// Of the builtins for it the compiler waits for all before the next read of LDS, the step's own among them, whatever part
-// of LDS is read; these are waited for by wait_barrier alone.
-__device__ __forceinline__ uint32_t lds_place(const void* p) {
-    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p);
-}
-__device__ __forceinline__ void to_lds16(const void* from, const void* to) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds_place(to)) : "memory", "m0");
-}
-__device__ __forceinline__ void to_lds4(const void* from, const void* to) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(lds_place(to)) : "memory", "m0");
-}
 // The wave's memory accesses but the last N, and its LDS accesses, are done, then the workgroup's.
 template <int N = 0> __device__ __forceinline__ void wait_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
@@ -368,6 +429,7 @@ __global__ __launch_bounds__(64 * WN * WT) void mm8_direct_kernel(Mm8Params p, i
         for (int s = 0; s < 3; ++s) {
             products(s, 0, 1);
             fragments(k, s + 1);
+            if (MN == 1 && s == 0 && more) load(k + 1, 0, LD);
 #pragma unroll
             for (int i = 1; i < MN; ++i) {
                 if (s == 0 && more) load(k + 1, LD * (i - 1) / (MN - 1), LD * i / (MN - 1));
@@ -491,6 +553,11 @@ hipError_t launch(const Mm8Params& p, hipStream_t st) {
         // waves of a workgroup: as many as have a step, at least one for each 16 rows it finishes
         const int TT = few == 1 ? 1 : few == 2 || nb < 256 ? 2 : 4;
         const int waves = std::max(TT, std::min(kFewWaves, (p.K + kFewStep - 1) / kFewStep));
+        if (p.direct) {
+            if (few == 1) mm8_few_direct_kernel<T, 1><<<dim3(nb, 1), 64 * kFewDirect, 0, st>>>(p);
+            else mm8_few_direct_kernel<T, 2><<<dim3(nb, (few + 1) / 2), 64 * kFewDirect, 0, st>>>(p);
+            return hipGetLastError();
+        }
         const dim3 grid(nb, (few + TT - 1) / TT);
         if (TT == 1) mm8_few_kernel<T, 1><<<grid, 64 * waves, 0, st>>>(p);
         else if (TT == 2) mm8_few_kernel<T, 2><<<grid, 64 * waves, 0, st>>>(p);
@@ -500,8 +567,10 @@ hipError_t launch(const Mm8Params& p, hipStream_t st) {
         const unsigned blocks = (unsigned)nb * (unsigned)tb;
         if (p.direct && p.tile == 256)
             mm8_direct_kernel<T, 256, 256, 2, 4><<<std::min(blocks, 256u), 512, 0, st>>>(p, nb, tb);
-        else if (p.direct)
+        else if (p.direct && p.tile == 128)
             mm8_direct_kernel<T, 128, 128, 2, 2><<<std::min(blocks, 512u), 256, 0, st>>>(p, nb, tb);
+        else if (p.direct)
+            mm8_direct_kernel<T, 64, 64, 2, 2><<<std::min(blocks, 1024u), 256, 0, st>>>(p, nb, tb);
         else if (p.tile == 64) mm8_tile_kernel<T, 64, 64, 2, 2><<<blocks, 256, 0, st>>>(p, nb);
         else mm8_tile_kernel<T, 128, 128, 2, 2><<<blocks, 256, 0, st>>>(p, nb);
     }

@@ -108,10 +108,10 @@ struct Share {
             has[i] = g < p.G && j + i * lanes < nv;
             at[i] = has[i] ? g * p.Cg + (j + i * lanes) * V : 0;
         }
-        const int64_t r0 = (int64_t)chunk * p.per;
-        end = (int)min((int64_t)p.T, r0 + p.per);
-        row = (int)r0 + (TEAM == 64 ? uniform(threadIdx.x >> 6) : 0);
-        step = norm_teams(TEAM);
+        // every so many rows: what all teams read at a time lies together
+        row = chunk * norm_teams(TEAM) + (TEAM == 64 ? uniform(threadIdx.x >> 6) : 0);
+        step = p.chunks * norm_teams(TEAM);
+        end = p.T;
     }
 };
 // A row's normalised values in place of x (0 where the lane has none), and 1 / sqrt(var + eps).

@@ -122,6 +122,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void norm_sum_kernel(NormParams p) 
     const int c = blockIdx.x * 64 + lane;
     float s = 0.0f;
     if (c < p.C)
+#pragma unroll 4
         for (int n = w; n < p.chunks; n += kSumWaves) s += p.part[((int64_t)n * 2 + k) * p.C + c];
     part[w][lane] = s;
     __syncthreads();
