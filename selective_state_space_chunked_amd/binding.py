@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import struct
 import warnings
@@ -1195,6 +1196,12 @@ def tokens_scan(*, delta, x, A, Bm, C, skip=None, z=None, delta_bias=None, delta
 # ---------------------------------------------------------------------------
 # gated linear recurrence
 # ---------------------------------------------------------------------------
+def _f32(v):
+    """A real argument as a float32 can hold it (an infinity past its range: the library says what is wrong with it)."""
+    v = float(v)
+    return v if not abs(v) > 3.4028234663852886e38 else math.copysign(math.inf, v)
+
+
 def _stream_of(t, name, dtype, shape, dev):
     """A (B, D, L) stream: (address, batch stride, channel stride); steps contiguous."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
@@ -1233,7 +1240,7 @@ def _gated_args(x, r, i, lam, r_bias, i_bias, power, h0, st):
         raise ValueError("lam is required")
     lp, rb, ib = (_dense(t, n, _F32, (D,), dev) for t, n in ((lam, "lam"), (r_bias, "r_bias"), (i_bias, "i_bias")))
     hp = _dense(h0, "h0", _F32, (Bsz, D), dev)
-    return _GATED_ARGS.pack(code, power, Bsz, D, L, xp, rp, ip, lp, rb, ib, hp, *sx, *sr, *si), shape, st, dev
+    return _GATED_ARGS.pack(code, _f32(power), Bsz, D, L, xp, rp, ip, lp, rb, ib, hp, *sx, *sr, *si), shape, st, dev
 
 
 def gated_fwd(*, x, r, i, lam, r_bias=None, i_bias=None, power=8.0, h0=None, want_y=True, want_h_last=False,
@@ -1344,7 +1351,7 @@ def tokens_gated(*, x, r, i, lam, r_bias=None, i_bias=None, power=8.0, pool, seq
     S, slots, spool, start, sl, fr = _sequences(T, pool.unsqueeze(2), (D, 1), _F32, dev, seq_start, slot, fresh)
     out = dict(out) if out else {}
     yp, sy = _y_rows(out, st, T, D, dev)
-    args = _TOKENS_GATED_ARGS.pack(code, power, T, D, S, slots, xp, rp, ip, lp, rb, ib, start, sl, fr, pool.data_ptr(),
+    args = _TOKENS_GATED_ARGS.pack(code, _f32(power), T, D, S, slots, xp, rp, ip, lp, rb, ib, start, sl, fr, pool.data_ptr(),
                                    yp, sx, sr, si, sy, spool)
     if dev.type != "cuda":
         _on_gpu(dev)
@@ -1362,6 +1369,8 @@ def _norm_args(x, groups, w, bias, eps, silu, z, st):
         raise ValueError("x must be a torch.Tensor")
     if x.dim() != 2:
         raise ValueError(f"x has shape {tuple(x.shape)}; expected (T, C)")
+    if not isinstance(groups, int):
+        raise TypeError("groups must be an int")
     T, C = x.shape
     if st is not None and x.dtype is not st:
         raise TypeError(f"x has dtype {x.dtype}, expected {st}")
@@ -1371,7 +1380,7 @@ def _norm_args(x, groups, w, bias, eps, silu, z, st):
     zp, sz = _rows(z, "z", st, T, C, dev) if z is not None else (0, 0)
     wp = _dense(w, "w", _F32, (C,), dev)
     bp = _dense(bias, "bias", _F32, (C,), dev)
-    return _GROUP_NORM_ARGS.pack(code, 1 if silu else 0, T, C, groups, xp, zp, wp, bp, sx, sz, eps), T, C, st, dev
+    return _GROUP_NORM_ARGS.pack(code, 1 if silu else 0, T, C, groups, xp, zp, wp, bp, sx, sz, _f32(eps)), T, C, st, dev
 
 
 def _out_rows(out, key, want, dtype, T, C, dev):

@@ -260,6 +260,16 @@ __device__ __forceinline__ void gated_fwd(const GatedParams& p, const RowOf<LANE
     if (p.h_last && at.l == 0 && at.live) p.h_last[at.row] = carry;
 }
 
+// a channel's sums to its parameters' gradients; sigmoid(lam) / softplus(lam) goes to 1 as lam falls
+__device__ __forceinline__ void put_sums(const GatedParams& p, int d, float E, float r, float i) {
+    if (p.grb) p.grb[d] = r;
+    if (p.gib) p.gib[d] = i;
+    if (p.glam) {
+        const float lam = p.lam[d], sp = softplus_t(lam);
+        p.glam[d] = E * (sp > 0.0f ? sigmoid_f(lam) / sp : 1.0f);
+    }
+}
+
 template <typename T, int LANES, bool SLOW, int NW>
 __device__ __forceinline__ void gated_bwd(const GatedParams& p, const RowOf<LANES>& at, const GateChannel& c, WaveMaps<NW>& maps) {
     constexpr int TILE = LANES * kRun;
@@ -395,7 +405,9 @@ __device__ __forceinline__ void gated_bwd(const GatedParams& p, const RowOf<LANE
             sumi += part[2][w];
         }
     }
-    if (at.l == 0 && at.live) {
+    if (at.l == 0 && at.live && p.B == 1) {   // nothing to add
+        put_sums(p, at.d, sumE, sumr, sumi);
+    } else if (at.l == 0 && at.live) {
         p.part[at.row] = sumE;
         p.part[(int64_t)p.B * p.D + at.row] = sumr;
         p.part[2 * (int64_t)p.B * p.D + at.row] = sumi;
@@ -420,27 +432,28 @@ __global__ __launch_bounds__(threads_of(LANES)) void gated_kernel(GatedParams p)
     }
 }
 
-// Sums of the rows' parts over the batch, in a fixed order: 16 waves of 64 channels take the batch rows in turn.
-constexpr int kSumWaves = 16;
+// Sums of the rows' parts over the batch, in a fixed order: a workgroup has 64 channels, its waves the batch rows in
+// turn.
+constexpr int kSumWaves = 8;
 __global__ __launch_bounds__(64 * kSumWaves) void gated_sum_kernel(GatedParams p) {
-    __shared__ float part[kSumWaves][64];
-    const int k = blockIdx.y, lane = lane_id(), w = threadIdx.x >> 6;
+    __shared__ float part[kSumWaves][3][64];
+    const int lane = lane_id(), w = threadIdx.x >> 6;
     const int d = blockIdx.x * 64 + lane;
-    float s = 0.0f;
+    const int64_t n = (int64_t)p.B * p.D;
+    float s[3] = {0.0f, 0.0f, 0.0f};
     if (d < p.D)
-        for (int b = w; b < p.B; b += kSumWaves) s += p.part[((int64_t)k * p.B + b) * p.D + d];
-    part[w][lane] = s;
+        for (int b = w; b < p.B; b += kSumWaves)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) s[k] += p.part[k * n + (int64_t)b * p.D + d];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) part[w][k][lane] = s[k];
     __syncthreads();
     if (w != 0 || d >= p.D) return;
-    s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kSumWaves; ++i) s += part[i][lane];
-    if (k == 1 && p.grb) p.grb[d] = s;
-    if (k == 2 && p.gib) p.gib[d] = s;
-    if (k == 0 && p.glam) {
-        const float lam = p.lam[d], sp = softplus_t(lam);
-        p.glam[d] = s * (sp > 0.0f ? sigmoid_f(lam) / sp : 1.0f);   // the quotient goes to 1 as lam falls
-    }
+    for (int i = 1; i < kSumWaves; ++i)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) s[k] += part[i][k][lane];
+    put_sums(p, d, s[0], s[1], s[2]);
 }
 
 template <typename T, int LANES>
@@ -467,7 +480,7 @@ hipError_t launch_gated(const GatedParams& p, bool bwd, int dtype, hipStream_t s
     return dtype ? launch_lanes<bf16_t>(p, bwd, st) : launch_lanes<float>(p, bwd, st);
 }
 hipError_t launch_gated_sum(const GatedParams& p, hipStream_t st) {
-    gated_sum_kernel<<<dim3((p.D + 63) / 64, 3), 64 * kSumWaves, 0, st>>>(p);
+    gated_sum_kernel<<<(unsigned)((p.D + 63) / 64), 64 * kSumWaves, 0, st>>>(p);
     return hipGetLastError();
 }
 

@@ -391,7 +391,9 @@ struct NormParams {
     int gblocks, chunks;             // teams' groups of a row; workgroups that share its rows
 };
 constexpr int kNormMost = 8192;   // channels of a group: 1024 lanes of eight
-constexpr int kNormWG = 512;     // workgroups the rows are divided over
+// Workgroups the rows are divided over: two a CU, as the backward's registers allow (16384 x 2048 in groups of 64, bf16
+// with a gate, forward and backward: 512 48 and 75 us, 1024 51 and 77).
+constexpr int kNormWG = 512;
 hipError_t launch_norm_fwd(const NormParams& p, int dtype, hipStream_t st);
 hipError_t launch_norm_bwd(const NormParams& p, int dtype, hipStream_t st);
 hipError_t launch_norm_sum(const NormParams& p, hipStream_t st);

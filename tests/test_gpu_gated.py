@@ -569,3 +569,325 @@ def test_mm8_outputs_and_empty():
     f = ssm.tokens_pack8(torch.zeros(4, 0, device=DEV))
     assert f["x8"].shape == (4, 0) and (f["x8_scale"] == 0).all()
     assert ssm.tokens_pack8(torch.zeros(0, 9, device=DEV))["x8"].shape == (0, 9)
+
+
+# ---------------------------------------------------------------------------
+# together, on streams, in graphs, through both ways of the binding
+# ---------------------------------------------------------------------------
+def quantised(w):
+    q, s = R.pack(w)
+    return torch.from_numpy(q).to(DEV), dev(s)
+
+
+def serving_weights(E, D, r):
+    """A layer's projections in 8 bits (input and the two gates; output), its convolution, recurrence and norm."""
+    p = {k: quantised(r.normal(size=(D, E)) / np.sqrt(E)) for k in ("x", "r", "i", "z")}
+    p["o"] = quantised(r.normal(size=(E, D)) / np.sqrt(D))
+    p["conv"], p["cbias"] = dev(r.normal(size=(D, 4)) / 2), dev(0.1 * r.normal(size=D))
+    p["lam"] = dev(np.log(np.expm1(-np.log(r.uniform(0.9, 0.999, D)))))
+    p["w"], p["b"] = dev(1 + 0.1 * r.normal(size=D)), dev(0.1 * r.normal(size=D))
+    return p
+
+
+def serve(p, rows, cpool, pool, where, dtype, groups):
+    """rows -> 8 bits -> projections -> convolution -> gated recurrence -> gated norm -> 8 bits -> output projection."""
+    q = ssm.tokens_pack8(rows)
+    at = dict(x8=q["x8"], x8_scale=q["x8_scale"], dtype=dtype)
+    x, r, i, z = (ssm.tokens_mm8(w8=p[k][0], w8_scale=p[k][1], **at)["y"] for k in ("x", "r", "i", "z"))
+    u = ssm.tokens_conv(x=x, w=p["conv"], bias=p["cbias"], silu=True, pool=cpool, **where)["y"]
+    h = ssm.tokens_gated(x=u, r=r, i=i, lam=p["lam"], pool=pool, **where)["y"]
+    y = ssm.group_norm_fwd(x=h, groups=groups, w=p["w"], bias=p["b"], z=z)["y"]
+    q = ssm.tokens_pack8(y)
+    return ssm.tokens_mm8(x8=q["x8"], x8_scale=q["x8_scale"], w8=p["o"][0], w8_scale=p["o"][1], dtype=dtype)["y"]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompts_then_tokens_of_a_gated_layer(dtype):
+    """A whole serving layer over prompts and then token by token against the same layer in float64, every stage taking
+    the stage before as the GPU rounded it; and each token alone gives what the token inside a prompt gives."""
+    r = gen(40)
+    E, D, G, lens = 96, 160, 5, [70, 1, 133]
+    p = serving_weights(E, D, r)
+    S, start = len(lens), [0, *np.cumsum(lens)]
+    T = int(start[-1])
+    rows = dev(r.normal(size=(T, E)), dtype)
+    slot = torch.tensor([2, 0, 3], dtype=torch.int32, device=DEV)
+    pools = [torch.zeros(5, D, 3, dtype=DT[dtype], device=DEV), torch.zeros(5, D, device=DEV)]
+    where = dict(seq_start=torch.tensor(start, dtype=torch.int32, device=DEV), slot=slot,
+                 fresh=torch.ones(S, dtype=torch.bool, device=DEV))
+    whole = serve(p, rows, *pools, where, DT[dtype], G)
+    ends = [v.clone() for v in pools]
+    # the prompts but for their last five tokens, then those one by one
+    cut = [max(n - 5, 0) for n in lens]
+    take = torch.cat([torch.arange(start[s], start[s] + cut[s]) for s in range(S)]).to(DEV)
+    pools = [torch.zeros_like(v) for v in pools]
+    where["seq_start"] = torch.tensor([0, *np.cumsum(cut)], dtype=torch.int32, device=DEV)
+    first = serve(p, rows[take].contiguous(), *pools, where, DT[dtype], G)
+    same = [(first, whole[take])]
+    for k in range(5):
+        live = [s for s in range(S) if k >= 5 - min(lens[s], 5)]
+        one = dict(slot=torch.tensor([int(slot[s]) if s in live else -1 for s in range(S)], dtype=torch.int32, device=DEV),
+                   fresh=torch.tensor([lens[s] <= 5 and k == 5 - lens[s] for s in range(S)], device=DEV))
+        at = torch.tensor([start[s + 1] - 5 + k if s in live else 0 for s in range(S)], device=DEV)
+        # (places that are empty keep what the tensors they come in hold: those are given)
+        x8 = ssm.tokens_pack8(rows[at].contiguous())
+        g = {n: ssm.tokens_mm8(x8=x8["x8"], x8_scale=x8["x8_scale"], w8=p[n][0], w8_scale=p[n][1], dtype=DT[dtype])["y"]
+             for n in ("x", "r", "i", "z")}
+        zero = {"y": torch.zeros(S, D, dtype=DT[dtype], device=DEV)}
+        u = ssm.tokens_conv(x=g["x"], w=p["conv"], bias=p["cbias"], silu=True, pool=pools[0], out=zero, **one)["y"]
+        h = ssm.tokens_gated(x=u, r=g["r"], i=g["i"], lam=p["lam"], pool=pools[1], out={"y": torch.zeros_like(u)}, **one)["y"]
+        y = ssm.group_norm_fwd(x=h, groups=G, w=p["w"], bias=p["b"], z=g["z"])["y"]
+        q = ssm.tokens_pack8(y)
+        o = ssm.tokens_mm8(x8=q["x8"], x8_scale=q["x8_scale"], w8=p["o"][0], w8_scale=p["o"][1], dtype=DT[dtype])["y"]
+        same.append((o[live], whole[at[live]]))
+    # The two ways differ by what fp32 rounds along a scan (or the next value of bf16), and so by a step of 8 bits here and
+    # there: of at most 1/127 of a row's largest magnitude in each of D terms, added with random signs.
+    for a, b in same:
+        a, b = a.double(), b.double()
+        assert float((a - b).norm() / b.norm()) < (2e-3 if dtype == "f32" else 2e-2)
+    for a, b in zip(pools, ends):
+        assert float((a.double() - b.double()).norm() / b.double().norm()) < (1e-5 if dtype == "f32" else 2e-2)
+    # stage by stage against the references
+    q = ssm.tokens_pack8(rows)
+    v = {k: ssm.tokens_mm8(x8=q["x8"], x8_scale=q["x8_scale"], w8=p[k][0], w8_scale=p[k][1], dtype=DT[dtype])["y"] for k in "xriz"}
+    x8, xs = q["x8"].cpu().numpy(), q["x8_scale"].cpu().numpy()
+    for k in "xriz":
+        R.check(k, v[k], *R.mm8(x8, xs, p[k][0].cpu().numpy(), p[k][1].cpu().numpy(), None), dtype)
+    t = dict(x=v["x"], r=v["r"], i=v["i"], lam=p["lam"], r_bias=None, i_bias=None)
+    tok_check(t, [int(s) for s in start], [2, 0, 3], [True] * 3, 5, dtype, r)
+    h = ssm.gated_fwd(**{k: a.T.contiguous()[None] if k in "xri" else a for k, a in t.items()})["y"][0].T.contiguous()
+    n = dict(x=h, z=v["z"], w=p["w"], bias=p["b"])
+    norm_check(n, dev(r.normal(size=(T, D)), dtype), G, dtype, False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_training_step_of_a_gated_layer(dtype):
+    """Convolution, gated recurrence and norm forward and back: the gradients that arrive at the input and at every
+    parameter, against differences of the layer's loss in float64 and, stage by stage, against the references."""
+    from . import _layer_ref as C
+    r = gen(41)
+    B, D, L, G, W = 2, 24, 200, 3, 4
+    x = dev(r.normal(size=(B, D, L)), dtype)
+    gates = {k: dev(r.normal(size=(B, D, L)), dtype) for k in "ri"}
+    z, gy = dev(r.normal(size=(B * L, D)), dtype), dev(r.normal(size=(B * L, D)), dtype)
+    w, cb = dev(r.normal(size=(D, W)) / 2), dev(0.1 * r.normal(size=D))
+    lam = dev(np.log(np.expm1(-np.log(r.uniform(0.9, 0.999, D)))))
+    nw, nb = dev(1 + 0.1 * r.normal(size=D)), dev(0.1 * r.normal(size=D))
+    rows = lambda t: t.transpose(1, 2).reshape(B * L, D).contiguous()                      # noqa: E731
+    streams = lambda t: t.reshape(B, L, D).transpose(1, 2).contiguous()                    # noqa: E731
+    f = ssm.conv_fwd(x=x, w=w, bias=cb, silu=True, want_ckpt8=True)
+    rec = dict(x=f["y"], lam=lam, **gates)
+    h = ssm.gated_fwd(want_ckpt=True, **rec)
+    n = dict(x=rows(h["y"]), groups=G, w=nw, bias=nb, z=z)
+    y = ssm.group_norm_fwd(**n)["y"]
+    gn = ssm.group_norm_bwd(gy=gy, **n)
+    gr = ssm.gated_bwd(gy=streams(gn["gx"]), ckpt=h["ckpt"], **rec)
+    gc = ssm.conv_bwd(gy=gr["gx"], x=x, w=w, bias=cb, silu=True)
+    v, err, _ = C.conv_fwd(f64(x), f64(w), f64(cb), None, True)
+    R.check("u", f["y"], v, err, dtype)
+    a = [f64(f["y"]), f64(gates["r"]), f64(gates["i"]), f64(lam), None, None]
+    R.check("h", h["y"], *R.gated_fwd(*a, 8.0, None)["y"], dtype)
+    ref = R.norm(f64(n["x"]), G, f64(nw), f64(nb), 1e-5, False, f64(z), f64(gy))
+    for k, g in {"y": y, **gn}.items():
+        R.check(k, g, *ref[k], "f32" if k in ("gw", "gbias") else dtype)
+    for k, v in R.gated_bwd(*a, 8.0, None, f64(streams(gn["gx"])), None).items():
+        R.check(k, gr[k], *v, "f32" if k in GATED_OUT else dtype)
+
+    def loss(x, w, cb, r_, i_, lam, nw, nb, z):
+        u, _, _ = C.conv_fwd(x, w, cb, None, True)
+        h = R.gated_fwd(u, r_, i_, lam, None, None, 8.0, None)["y"][0]
+        return (f64(gy) * R.norm(h.transpose(0, 2, 1).reshape(B * L, D), G, nw, nb, 1e-5, False, z)["y"][0]).sum()
+
+    base = [f64(v) for v in (x, w, cb, gates["r"], gates["i"], lam, nw, nb, z)]
+    got = [gc["gx"], gc["gw"], gc["gbias"], gr["gr"], gr["gi"], gr["glam"], gn["gw"], gn["gbias"], gn["gz"]]
+    for k, g in enumerate(got):
+        d = r.normal(size=base[k].shape)
+        far = [[v + s * 1e-5 * d if j == k else v for j, v in enumerate(base)] for s in (1, -1)]
+        num = (loss(*far[0]) - loss(*far[1])) / 2e-5
+        # streams between the stages are rounded to their type: relative to the gradient's size that many half steps, and
+        # the chain is three stages long, forward and back
+        assert abs(num - (f64(g) * d).sum()) <= 12 * R.HALF[dtype] * np.linalg.norm(f64(g)) * np.linalg.norm(d) + \
+            1e-4 * np.linalg.norm(f64(g)) * np.linalg.norm(d), k
+
+
+def every_call(seed):
+    """Every function of this file once, with plain tensors: a function that runs them on the same buffers again, and the
+    buffers that other inputs may be copied to."""
+    r = gen(seed)
+    D, T, S = 72, 300, 5
+    t, gy, gl = gated_inputs(2, 9, 1100, "bf16", r)
+    tok = tok_inputs(T, D, "bf16", r)
+    start = torch.tensor([0, 3, 3, 140, 290, 300], dtype=torch.int32, device=DEV)
+    slot = torch.tensor([4, 1, -1, 0, 6], dtype=torch.int32, device=DEV)
+    fresh = torch.tensor([0, 1, 0, 1, 0], dtype=torch.bool, device=DEV)
+    keep, pool = dev(r.normal(size=(7, D))), torch.empty(7, D, device=DEV)
+    n, ngy = norm_inputs(333, 64, "bf16", r)
+    m = mm8_inputs(70, 256, 96, r)
+    xr = dev(r.normal(size=(70, 256)), "bf16")
+
+    def run():
+        o = {}
+
+        def put(name, d):
+            o.update({f"{name} {k}": v for k, v in d.items()})
+            return d
+
+        f = put("gated", ssm.gated_fwd(want_h_last=True, want_ckpt=True, **t))
+        put("gated bwd", ssm.gated_bwd(gy=gy, gh_last=gl, ckpt=f["ckpt"], **t))
+        put("gated some", ssm.gated_bwd(gy=gy, want=("gi", "glam"), **t))
+        pool.copy_(keep)
+        put("tokens", ssm.tokens_gated(pool=pool, seq_start=start, slot=slot, fresh=fresh,
+                                       out={"y": torch.zeros(T, D, dtype=torch.bfloat16, device=DEV)}, **tok))
+        put("step", ssm.tokens_gated(pool=pool, slot=slot, **{k: v[:S] if k in "xri" else v for k, v in tok.items()},
+                                     out={"y": torch.zeros(S, D, dtype=torch.bfloat16, device=DEV)}))
+        o["pool"] = pool.clone()
+        put("norm", ssm.group_norm_fwd(groups=4, silu=True, **n))
+        put("norm bwd", ssm.group_norm_bwd(gy=ngy, groups=4, silu=True, **n))
+        put("norm some", ssm.group_norm_bwd(gy=ngy, groups=2, want=("gx",), x=n["x"]))
+        q = put("pack", ssm.tokens_pack8(xr))
+        put("mm8", ssm.tokens_mm8(**m))
+        put("mm8 f32", ssm.tokens_mm8(**{**m, **q}, dtype=torch.float32))
+        put("mm8 few", ssm.tokens_mm8(**{**m, "x8": m["x8"][:3], "x8_scale": m["x8_scale"][:3]}))
+        return o
+
+    return run, [t["x"], t["r"], gy, tok["x"], tok["i"], keep, n["x"], n["z"], ngy, xr]
+
+
+def test_gated_streams_and_graphs():
+    """Calls on a stream of their own, and captured calls replayed with other inputs, eager work and waits between them:
+    every replay equals the eager call bit for bit."""
+    run, buffers = every_call(50)
+    ref = run()
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        own = run()
+    torch.cuda.synchronize()
+    for k in ref:
+        assert torch.equal(ref[k], own[k]), k
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap = run()
+    r = gen(51)
+    for i in range(4):
+        for b in buffers:
+            b.copy_(torch.from_numpy(r.normal(size=tuple(b.shape))))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {k: v.clone() for k, v in cap.items()}
+        eager = run()
+        torch.cuda.synchronize()
+        for k in eager:
+            assert torch.equal(eager[k], got[k]), (i, k)
+
+
+def test_gated_native_calls_are_the_bindings():
+    """Without an installed allocator plain calls go through the native module: the same keys and the same bits."""
+    a = every_call(52)[0]()
+    ssm.set_allocator(None)
+    from selective_state_space_chunked_amd import binding
+    made = []
+    orig = binding._done
+
+    def count(r):
+        made.append(r is not NotImplemented)
+        return orig(r)
+
+    binding._done = count
+    try:
+        b = every_call(52)[0]()
+    finally:
+        binding._done = orig
+    assert made and all(made)
+    assert a.keys() == b.keys()
+    for k in a:
+        assert a[k].dtype == b[k].dtype and a[k].shape == b[k].shape and torch.equal(a[k], b[k]), k
+
+
+def test_gated_native_calls_refuse_as_the_binding():
+    """Arguments the native module leaves alone raise the binding's errors; those the library refuses, the library's."""
+    ssm.set_allocator(None)
+    x, lam = torch.zeros(2, 3, 10, device=DEV), torch.zeros(3, device=DEV)
+    rows, i8 = torch.zeros(6, 3, device=DEV), dict(dtype=torch.int8, device=DEV)
+    g, k = dict(x=x, r=x, i=x, lam=lam), dict(x=rows, r=rows, i=rows, lam=lam)
+    m = dict(x8=torch.zeros(4, 6, **i8), x8_scale=torch.zeros(4, device=DEV), w8=torch.zeros(3, 6, **i8),
+             w8_scale=torch.zeros(3, device=DEV))
+    err = ssm.binding.SSMError
+    for f, kw, exc in ((ssm.gated_fwd, dict(g, power=-1.0), err), (ssm.gated_fwd, dict(g, power=-1), err),
+                       (ssm.gated_fwd, dict(g, power=1e60), err), (ssm.gated_fwd, dict(g, lam=torch.zeros(2, device=DEV)), ValueError),
+                       (ssm.gated_fwd, dict(g, r=x.double()), TypeError), (ssm.gated_fwd, dict(g, lam=lam.cpu()), ValueError),
+                       (ssm.gated_bwd, dict(g, gy=x[..., :9]), ValueError), (ssm.gated_bwd, dict(g, gy=x, want=("gz",)), ValueError),
+                       (ssm.gated_bwd, dict(g, gy=x, ckpt=torch.zeros(2, 3, 2, device=DEV)), ValueError),
+                       (ssm.tokens_gated, dict(k, pool=torch.zeros(4, 3, device=DEV)), err),           # 6 rows, 4 slots
+                       (ssm.tokens_gated, dict(k, pool=torch.zeros(6, 3, 1, device=DEV)), ValueError),
+                       (ssm.tokens_gated, dict(k, pool=torch.zeros(6, 3, device=DEV), out={"y": rows}), err),   # y over x
+                       (ssm.group_norm_fwd, dict(x=rows, groups=2), err), (ssm.group_norm_fwd, dict(x=rows, groups=3, eps=-1.0), err),
+                       (ssm.group_norm_fwd, dict(x=rows, groups="3"), TypeError),
+                       (ssm.group_norm_bwd, dict(gy=rows, x=rows, groups=3, want=("gz",)), err),       # no z
+                       (ssm.group_norm_bwd, dict(gy=rows[:5], x=rows, groups=3), ValueError),
+                       (ssm.tokens_pack8, dict(x=rows.half()), TypeError),
+                       (ssm.tokens_mm8, dict(m, w8=torch.zeros(3, 5, **i8)), ValueError),
+                       (ssm.tokens_mm8, dict(m, x8_scale=None), ValueError),
+                       (ssm.tokens_mm8, dict(m, dtype=torch.float64), TypeError)):
+        with pytest.raises(exc):
+            f(**kw)
+
+
+def test_gated_offsets_past_32_bits():
+    """Rows, streams and slots of wide strides, so that they lie past 2^32 bytes: as the same tensors laid out densely."""
+    r = gen(60)
+    T, D, S = 70, 24, 3
+    wide, wide_out = (torch.empty(T * 2**26, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+
+    def spread(v, at):
+        o = wide.as_strided(v.shape, (2**26 - 1, 1), at)
+        o.copy_(v)
+        return o
+
+    t = tok_inputs(T, D, "bf16", r)
+    far = {k: spread(t[k], 100 * n) for n, k in enumerate("xri")}
+    out = wide_out.as_strided((T, D), (2**26 - 1, 1), 900)
+    at = dict(seq_start=torch.tensor([0, 33, 34, T], dtype=torch.int32, device=DEV),
+              slot=torch.tensor([2, 0, 1], dtype=torch.int32, device=DEV))
+    first = torch.randn(S, D, device=DEV)
+    base = torch.empty(2 * (2**30 + 4) + D, device=DEV)
+    res = []
+    for f in (False, True):
+        for step in (False, True):
+            pool = base.as_strided(first.shape, (2**30 + 4, 1)) if f else torch.empty_like(first)
+            pool.copy_(first)
+            a = {k: v[:S] if step and k in far else v for k, v in ({**t, **far} if f else t).items()}
+            y = ssm.tokens_gated(pool=pool, out={"y": out[:len(a["x"])]} if f else {}, **a,
+                                 **(dict(slot=at["slot"]) if step else at))["y"]
+            res += [y.clone(), pool.clone()]
+    for p, q in zip(res[:4], res[4:]):
+        assert torch.equal(p, q)
+    del base, pool
+    n = dict(groups=3, w=dev(r.normal(size=D)), silu=True)
+    dense, wide_ = dict(x=t["x"], z=t["r"], **n), dict(x=far["x"], z=far["r"], **n)
+    assert torch.equal(ssm.group_norm_fwd(out={"y": out}, **wide_)["y"], ssm.group_norm_fwd(**dense)["y"])
+    p, q = ssm.group_norm_bwd(gy=t["i"], **dense), ssm.group_norm_bwd(gy=far["i"], out={"gx": out}, **wide_)
+    assert all(torch.equal(p[k], q[k]) for k in p)
+    b8, out8 = wide.view(torch.int8), wide_out.view(torch.int8).as_strided((T, D), (2**26 + 3, 1), 900)
+    p, q = ssm.tokens_pack8(t["x"]), ssm.tokens_pack8(far["x"], out={"x8": out8})
+    assert all(torch.equal(p[k], q[k]) for k in p)
+    for rows_, K in ((T, 40), (20, 128), (T, 128)):
+        m = mm8_inputs(rows_, K, 50, r)
+        w8 = b8.as_strided((50, K), (2**27, 1), 2**26)
+        x8 = out8.as_strided((rows_, K), (2**26, 1), 16)
+        w8.copy_(m["w8"])
+        x8.copy_(m["x8"])
+        ref = ssm.tokens_mm8(**m)["y"]
+        assert torch.equal(ssm.tokens_mm8(**{**m, "w8": w8, "x8": x8})["y"], ref)
+    x = {k: dev(r.normal(size=(2, 3, 700)), "bf16") for k in ("x", "r", "i", "gy")}
+    g = {k: wide.as_strided((2, 3, 700), (2**32, 2**20, 1), 5000 * n) for n, k in enumerate(x)}
+    for k in g:
+        g[k].copy_(x[k])
+    fo = wide_out.as_strided((2, 3, 700), (2**32, 2**20, 1), 3)
+    lam = t["lam"][:3].contiguous()
+    a = ssm.gated_bwd(lam=lam, **x)
+    b = ssm.gated_bwd(lam=lam, out={"gr": fo}, **g)
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    assert torch.equal(ssm.gated_fwd(lam=lam, **{k: v for k, v in g.items() if k != "gy"}, out={"y": fo})["y"],
+                       ssm.gated_fwd(lam=lam, **{k: v for k, v in x.items() if k != "gy"})["y"])
