@@ -7,8 +7,8 @@
 // recurrence, whatever the sequences' lengths.
 // Waves compose their rows' maps, the workgroup its waves' through LDS, and tiles theirs through memory: a tile leaves
 // the map of its rows as soon as it has it (for each channel one word of 64 bits, so that no reader sees half of it), the
-// state at its end as soon as it knows that, and reads the tiles before its own, from the last one back, up to one whose
-// state is there.  The tiles of the same
+// state at its end as soon as it knows that, and goes back to the last tile whose state is there and from it
+// through the maps, so that every state is the same function of the rows whatever is there when.  The tiles of the same
 // channels are taken in the order of a counter, so a workgroup waits only for ones that run already, and for
 // nothing that these wait for; all the same the wait is bounded, and gives NaN where the bound is reached.
 //
@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kTileWaves = 8, kWaveRows = kGatedTile / kTileWaves;
 constexpr uint32_t kNone = 0xffffffffu;   // a word that is not there yet; of the NaNs that a state may be, not one
-constexpr int kPolls = 1 << 20;           // a second and more
+constexpr int kPolls = 1 << 16;           // a tenth of a second and more
 
 __device__ __forceinline__ uint32_t word_of(float v) {
     const uint32_t u = __float_as_uint(v);
@@ -91,7 +91,8 @@ struct RowInfo {
             if (st >= end) break;
             const int en = q.end(s);
             if (st < 0 || en <= max(st, r0)) continue;
-            const int v = uniform(p.slots[s]);
+            int v = uniform(p.slots[s]);
+            if (v >= p.q.slots) v = -1;   // (only in a workspace that another call has written to meanwhile)
             const bool f = q.fresh(s);
             if (t >= st && t < min(en, end)) {
                 slot = v;
@@ -200,64 +201,61 @@ __device__ __forceinline__ void gated_tile(const TokGatedParams& p, int tile, in
             }
         }
         if (tile > 0 && !(cut & 1)) {   // otherwise no row takes what comes in
-            float Pa[V], Sa[V];
-            bool open[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                Pa[e] = 1.0f;
-                Sa[e] = 0.0f;
-                open[e] = e < n;
-            }
+            // Back to the last tile before this one whose state is known, with all maps between there, eight tiles' words
+            // under way together.
+            constexpr int AHEAD = 8;
+            const auto place = [&](int k, int e) { return (int64_t)(max(k, 0) - tile) * p.D + min(d + e, p.D - 1); };
             int k = tile - 1, polls = 0;
-            while (k >= 0) {
-                // the words of up to four tiles are under way together
-                constexpr int AHEAD = 4;
-                uint64_t m[AHEAD][V];
-                uint32_t h[AHEAD][V];
+            for (bool found = false; !found;) {
+                uint32_t h[AHEAD][V], m[AHEAD][V];
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        const int64_t o = (int64_t)(max(k - i, 0) - tile) * p.D + min(d + e, p.D - 1);
-                        m[i][e] = get_word(map + o);
-                        h[i][e] = get_word(state + o);
+                        h[i][e] = get_word(state + place(k - i, e));
+                        m[i][e] = get_word((const uint32_t*)(map + place(k - i, e)));   // half of a map: all of it is there
                     }
                 bool wait = false;
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
-                    if (k < 0 || wait) continue;
-                    bool none = false;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) none |= open[e] && h[i][e] == kNone && (uint32_t)m[i][e] == kNone;
-                    wait = __ballot(none) != 0;
-                    if (wait) continue;
-                    polls = 0;
-                    bool more = false;
+                    bool nostate = false, nomap = false;
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        if (!open[e]) continue;
-                        const bool known = h[i][e] != kNone;
-                        Sa[e] = fmaf(Pa[e], __uint_as_float(known ? h[i][e] : (uint32_t)(m[i][e] >> 32)), Sa[e]);
-                        Pa[e] *= __uint_as_float((uint32_t)m[i][e]);
-                        open[e] = !known;
-                        more |= !known;
+                        nostate |= h[i][e] == kNone;
+                        nomap |= m[i][e] == kNone;
                     }
-                    k = __ballot(more) ? k - 1 : -1;
+                    if (found || wait) continue;
+                    if (!__ballot(nostate)) found = true;
+                    else if (k <= 0 || __ballot(nomap)) wait = true;   // (before the first tile there is none)
+                    else --k;
                 }
                 if (wait) {
-                    if (++polls > kPolls) {
-#pragma unroll
-                        for (int e = 0; e < V; ++e) Sa[e] = __uint_as_float(0x7fc00000u);
-                        break;
-                    }
+                    if (++polls > kPolls) break;
                     __builtin_amdgcn_s_sleep(1);
+                } else {
+                    polls = 0;
                 }
             }
+            // From there on through the maps: the same products and sums whichever tile it is, so the same bits.
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                C[e] = Sa[e];
-                if (e < n && !forgets) put_word(state + d + e, word_of(fmaf(P[e], C[e], S[e])));
+            for (int e = 0; e < V; ++e) C[e] = polls > kPolls ? __uint_as_float(0x7fc00000u) : __uint_as_float(get_word(state + place(k, e)));
+            while (++k < tile) {
+                uint64_t m[AHEAD][V];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) m[i][e] = get_word(map + place(min(k + i, tile - 1), e));
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        if (k + i < tile)
+                            C[e] = fmaf(__uint_as_float((uint32_t)m[i][e]), C[e], __uint_as_float((uint32_t)(m[i][e] >> 32)));
+                k += AHEAD - 1;
             }
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (e < n && !forgets) put_word(state + d + e, word_of(fmaf(P[e], C[e], S[e])));
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -304,6 +302,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 4) void tok_gated_kernel(TokGatedP
     const bool slow = __ballot(fast) == 0, even = p.D % V == 0 || d0 + 64 * V <= p.D;
     __syncthreads();
     const int tile = uniform(taken);
+    if (tile < 0 || tile >= p.tiles) return;   // (as above)
     if (even && slow) gated_tile<T, true, true>(p, tile, d0, c, seqs, maps);
     else if (even) gated_tile<T, true, false>(p, tile, d0, c, seqs, maps);
     else gated_tile<T, false, false>(p, tile, d0, c, seqs, maps);

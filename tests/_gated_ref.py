@@ -209,7 +209,7 @@ def pack(x):
 
 def mm8(x8, xs, w8, ws, bias):
     """The sum is exact, its rounding to float32 u, the scales' product u, the last step u of the result."""
-    acc = (x8.astype(np.int64) @ w8.astype(np.int64).T).astype(np.float64)
+    acc = x8.astype(np.float64) @ w8.astype(np.float64).T   # whole numbers below 2^53: exact
     p = acc * xs.astype(np.float64)[:, None] * ws.astype(np.float64)
     y = p + (0 if bias is None else bias)
     return y, 2.1 * U * np.abs(p) + U * np.abs(y)

@@ -36,7 +36,7 @@ def gated_args(**over):
 @pytest.mark.parametrize("over,want", [
     (dict(dtype=2), "DTYPE"), (dict(batch=-1), "SHAPE"), (dict(channels=-1), "SHAPE"), (dict(length=-1), "SHAPE"),
     (dict(batch=65536), "SHAPE"), (dict(length=1 << 31), "SHAPE"), (dict(channels=1 << 24), "SHAPE"),
-    (dict(power=0.0), "SHAPE"), (dict(power=-1.0), "SHAPE"), (dict(power=float("nan")), "SHAPE"),
+    (dict(batch=32, channels=(1 << 23) + 64, length=2), "SHAPE"), (dict(power=0.0), "SHAPE"), (dict(power=-1.0), "SHAPE"), (dict(power=float("nan")), "SHAPE"),
     (dict(power=float("inf")), "SHAPE"), (dict(x=None), "NULL"), (dict(r=None), "NULL"), (dict(i=None), "NULL"),
     (dict(lam=None), "NULL"), (dict(x_stride=(800, -1)), "LAYOUT"), (dict(r_stride=(1 << 40, 100)), "LAYOUT"),
     (dict(i=3 * FAKE + 2), "LAYOUT"), (dict(lam=4 * FAKE + 2), "LAYOUT"), (dict(r_bias=5 * FAKE + 1), "LAYOUT"),
@@ -175,13 +175,13 @@ def mm8_args(**over):
 def test_mm8_refusals():
     L = B.lib()
     for over, want in ((dict(dtype=3), "DTYPE"), (dict(tokens=-1), "SHAPE"), (dict(channels=1 << 17, x_stride=1 << 17, x8_stride=1 << 17), "SHAPE"),
-                       (dict(tokens=1 << 30), "SHAPE"), (dict(x=None), "NULL"), (dict(x8=None), "NULL"),
+                       (dict(tokens=1 << 24), "SHAPE"), (dict(x=None), "NULL"), (dict(x8=None), "NULL"),
                        (dict(x8_scale=None), "NULL"), (dict(x8_stride=19), "LAYOUT"), (dict(x_stride=-1), "LAYOUT"),
                        (dict(x=FAKE + 2), "LAYOUT"), (dict(x8=FAKE + 8), "LAYOUT"), (dict(x8_scale=2 * FAKE + 4), "LAYOUT"),
                        (dict(x8_scale=3 * FAKE + 2), "LAYOUT")):
         assert L.ssm_tokens_pack8(ctypes.byref(pack8_args(**over)), None) == code(want), over
     for over, want in ((dict(dtype=3), "DTYPE"), (dict(outputs=-1), "SHAPE"), (dict(inputs=1 << 17, x8_stride=1 << 17, w8_stride=1 << 17), "SHAPE"),
-                       (dict(outputs=1 << 30), "SHAPE"), (dict(tokens=1 << 29, outputs=1 << 29, y_stride=1 << 29), "LAYOUT"),
+                       (dict(outputs=1 << 26, y_stride=1 << 26), "SHAPE"), (dict(tokens=1 << 20, outputs=1 << 17, y_stride=1 << 17), "SHAPE"),
                        (dict(x8=None), "NULL"), (dict(w8=None), "NULL"), (dict(x8_scale=None), "NULL"),
                        (dict(w8_scale=None), "NULL"), (dict(y=None), "NULL"), (dict(y_stride=5), "LAYOUT"),
                        (dict(w8_stride=-1), "LAYOUT"), (dict(y=FAKE + 32), "LAYOUT"), (dict(y=5 * FAKE + 2), "LAYOUT"),
