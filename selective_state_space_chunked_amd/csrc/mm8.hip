@@ -82,6 +82,12 @@ __device__ __forceinline__ uint32_t lds_place(const void* p) {
 __device__ __forceinline__ void to_lds16(const void* from, const void* to) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds_place(to)) : "memory", "m0");
 }
+// The same at a row's end: zeros from the lanes that are past it.  (Each of a load's rows has 16 bytes at least, so the
+// load goes out whatever the lanes: waits may count it.)
+__device__ __forceinline__ void to_lds16_until(const void* from, i4* to, bool inside) {
+    if (inside) to_lds16(from, to);
+    else to[lane_id()] = i4(0);
+}
 __device__ __forceinline__ void to_lds4(const void* from, const void* to) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(lds_place(to)) : "memory", "m0");
 }
@@ -156,7 +162,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void mm8_few_kernel(Mm8Params p) {
     finish4<T>(p, s, t0 + 16 * w + l % 16, n, sw, bias);
 }
 
-// The same for rows aligned to 16 bytes and K a multiple of 128: a wave's steps come by loads of whole lines to LDS (a
+// The same for rows aligned to 16 bytes and K a multiple of 16: a wave's steps come by loads of whole lines to LDS (a
 // line by eight neighbouring lanes; as the matrix instructions hold them, every lane's 16 bytes are a request of their
 // own, 64 x 4096 x 2048: 8.7 us), two steps under way.  The waves' stages are their own, so there is no barrier
 // before the sums.
@@ -165,7 +171,7 @@ template <typename T, int TT>
 __global__ __launch_bounds__(64 * kFewDirect) void mm8_few_direct_kernel(Mm8Params p) {
     constexpr int ROWS = 16 + 16 * TT, LD = ROWS / 8;
     __shared__ __align__(16) i4 lds[kFewDirect][2][ROWS * 8];
-    const int l = lane_id(), w = uniform(threadIdx.x >> 6), steps = p.K / kFewStep;
+    const int l = lane_id(), w = uniform(threadIdx.x >> 6), steps = (p.K + kFewStep - 1) / kFewStep;
     const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 16 * TT;
     const int8_t* src[LD];
 #pragma unroll
@@ -176,7 +182,11 @@ __global__ __launch_bounds__(64 * kFewDirect) void mm8_few_direct_kernel(Mm8Para
     }
     auto load = [&](int k, int stage) {
 #pragma unroll
-        for (int j = 0; j < LD; ++j) to_lds16(src[j] + (int64_t)k * kFewStep, &lds[w][stage][64 * j]);
+        for (int j = 0; j < LD; ++j) {
+            if ((k + 1) * kFewStep <= p.K) to_lds16(src[j] + (int64_t)k * kFewStep, &lds[w][stage][64 * j]);
+            else to_lds16_until(src[j] + (int64_t)k * kFewStep, &lds[w][stage][64 * j],
+                                ((l % 8) ^ ((8 * j + l / 8) / 2 % 8)) * 16 < p.K - k * kFewStep);
+        }
     };
     i4 acc[TT];
 #pragma unroll
@@ -350,7 +360,7 @@ __global__ __launch_bounds__(64 * WN * WT) void mm8_tile_kernel(Mm8Params p, int
     finish_tiles<T, MN, MT>(p, acc, n0, t0, wn, wt, sc, lds + wave * ((BN + BT) * 8 / (WN * WT)));
 }
 
-// Many rows whose starts are aligned to 16 bytes and K a multiple of 128: the same with loads that go from memory to
+// Many rows whose starts are aligned to 16 bytes and K a multiple of 16: the same with loads that go from memory to
 // LDS directly, a step ahead of the products, and one barrier a step.  A workgroup
 // goes on from tile to tile: the next tile's first step comes while a tile's results go out.
 constexpr int kDirectStep = 128;
@@ -374,19 +384,28 @@ __global__ __launch_bounds__(64 * WN * WT) void mm8_direct_kernel(Mm8Params p, i
     const int64_t stride = of_w ? p.sw : p.sx;
     const int8_t* src;
     uint32_t off[LD];
-    int n0, t0;
-    const int steps = p.K / kDirectStep;
+    int n0, t0, first;
+    const int steps = (p.K + kDirectStep - 1) / kDirectStep;
+    const bool ragged = p.K % kDirectStep != 0;
     auto load = [&](int k, int j0, int j1) {
 #pragma unroll
-        for (int j = j0; j < j1; ++j)
-            to_lds16(src + (int64_t)k * kDirectStep + off[j], &lds[k & 1][(r0 + 8 * j) * 8]);
+        for (int j = j0; j < j1; ++j) to_lds16(src + (int64_t)k * kDirectStep + off[j], &lds[k & 1][(r0 + 8 * j) * 8]);
+    };
+    auto load_last = [&]() {   // the last step, where the row ends inside of it
+        const int k = steps - 1, left = p.K - k * kDirectStep;
+#pragma unroll 1
+        for (int j = 0; j < LD; ++j) {
+            const int r = 8 * j + l / 8, c = (l % 8) ^ ((r0 + r) / 2 % 8);
+            to_lds16_until(src + (int64_t)k * kDirectStep + 16 * c + (int64_t)(max(0, min(first + r, last) - min(first, last))) * stride,
+                           &lds[k & 1][(r0 + 8 * j) * 8], 16 * c < left);
+        }
     };
     // tile `id`, its scales and its first step
     auto begin = [&](int id, Scales<BN, BT>& sc) {
         const int2 tile = tile_of(id, nblocks, tblocks);
         n0 = tile.x * BN;
         t0 = tile.y * BT;
-        const int first = of_w ? n0 + r0 : t0 + r0 - BN;
+        first = of_w ? n0 + r0 : t0 + r0 - BN;
         src = (of_w ? p.w : p.x) + min(first, last) * stride;
 #pragma unroll
         for (int j = 0; j < LD; ++j) {
@@ -401,7 +420,8 @@ __global__ __launch_bounds__(64 * WN * WT) void mm8_direct_kernel(Mm8Params p, i
             const int at = 64 * (wave - BN / 64);
             to_lds4(p.xs + min(t0 + at + l, p.T - 1), &sc.x[at]);
         }
-        load(0, 0, LD);
+        if (steps > 1 || !ragged) load(0, 0, LD);
+        else load_last();
     };
     const int fa = (wn + l % 32) * 8, fb = (BN + wt + l % 32) * 8, sw = l / 2 % 8;
     i4 a[2][MN], b[2][MT];   // of two quarters of a step
@@ -424,22 +444,24 @@ __global__ __launch_bounds__(64 * WN * WT) void mm8_direct_kernel(Mm8Params p, i
     };
     // A quarter's products run while the next quarter's operands are read, the first few before the reads so that what
     // they wait for is behind them already; the next step's loads go out between those of the first quarter.
-    auto step = [&](int k, bool more) {
+    // next: 0 none, 1 a whole step, 2 the last one
+    auto step = [&](int k, int next) {
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
             products(s, 0, 1);
             fragments(k, s + 1);
-            if (MN == 1 && s == 0 && more) load(k + 1, 0, LD);
+            if (MN == 1 && s == 0 && next == 1) load(k + 1, 0, LD);
+            if (s == 0 && next == 2) load_last();
 #pragma unroll
             for (int i = 1; i < MN; ++i) {
-                if (s == 0 && more) load(k + 1, LD * (i - 1) / (MN - 1), LD * i / (MN - 1));
+                if (s == 0 && next == 1) load(k + 1, LD * (i - 1) / (MN - 1), LD * i / (MN - 1));
                 products(s, i, i + 1);
             }
         }
         products(3, 0, 1);
         wait_barrier();   // step k + 1 has come, and every wave has read step k
         products(3, 1, MN / 2 + 1);
-        if (more) fragments(k + 1, 0);
+        if (next) fragments(k + 1, 0);
         products(3, MN / 2 + 1, MN);
     };
     int buf = 0;
@@ -452,8 +474,9 @@ __global__ __launch_bounds__(64 * WN * WT) void mm8_direct_kernel(Mm8Params p, i
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[i][j] = i16v(0);
         fragments(0, 0);
-        for (int k = 0; k + 1 < steps; ++k) step(k, true);
-        step(steps - 1, false);
+        for (int k = 0; k + 1 + ragged < steps; ++k) step(k, 1);
+        if (ragged && steps > 1) step(steps - 2, 2);
+        step(steps - 1, 0);
         // The next tile's first step comes while this one's results go out, by way of the other stage.
         const int n = n0, t = t0;
         id += gridDim.x;

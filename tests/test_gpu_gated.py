@@ -548,7 +548,7 @@ def mm8_check(t, dtype, **kw):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("K", [1, 3, 15, 16, 17, 64, 100, 127, 128, 129, 515, 1024, 1100])
+@pytest.mark.parametrize("K", [1, 3, 15, 16, 17, 64, 100, 127, 128, 129, 144, 240, 400, 515, 1024, 1100, 1152, 2032])
 @pytest.mark.parametrize("T,N", [(1, 1), (2, 17), (16, 16), (17, 33), (40, 30), (64, 250), (65, 63), (130, 129), (300, 5)])
 def test_mm8(T, N, K, dtype):
     r = gen(T + N + K)
@@ -557,7 +557,8 @@ def test_mm8(T, N, K, dtype):
 
 @pytest.mark.parametrize("T,K,N", [(2100, 640, 2000), (2049, 384, 4100), (1000, 200, 8200), (512, 4096, 512), (4096, 256, 264),
                                    (70, 8192, 500), (200, 131071, 40), (4000, 192, 3900), (3800, 64, 3700), (4096, 128, 4352), (4100, 384, 4300), (70000, 256, 128),
-                                   (65664, 128, 64), (65664, 384, 61), (1030, 256, 1000)])
+                                   (65664, 128, 64), (65664, 384, 61), (1030, 256, 1000), (1030, 208, 1000),
+                                   (4096, 16, 4352), (4096, 336, 4352), (70000, 80, 128), (65664, 176, 64)])
 def test_mm8_large(T, K, N):
     mm8_check(mm8_inputs(T, K, N, gen(31)), "bf16")
     mm8_check(mm8_inputs(T, K, N, gen(32), view=True), "f32")
