@@ -43,8 +43,6 @@ __device__ __forceinline__ i4 row_chunk(const int8_t* row, int k, int K) {
     return i4{(int)(uint32_t)lo, (int)(lo >> 32), (int)(uint32_t)hi, (int)(hi >> 32)};
 }
 
-constexpr int kFewWaves = 16;
-
 // four channels of a row of y, the first n of them
 template <typename T>
 __device__ __forceinline__ void put4(T* y, const float (&v)[4], int n) {
@@ -92,127 +90,73 @@ __device__ __forceinline__ void to_lds4(const void* from, const void* to) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(lds_place(to)) : "memory", "m0");
 }
 // Few rows: bound by reading the weights once.  A workgroup takes 16 channels and 16 TT rows, its waves the k of a row in
-// turns of 128 bytes -- whole lines of the weights -- and the waves' sums are added in LDS.
-constexpr int kFewStep = 128;
-template <typename T, int TT>
+// turns of 128 bytes -- whole lines of the weights -- and the waves' sums are added in LDS.  A wave's steps come by way of
+// LDS of its own, a line by eight neighbouring lanes, so there is no barrier before the sums; loaded as the matrix
+// instructions hold them, every lane's 16 bytes are a request of their own (64 x 4096 x 2048: 8.7 us, this way 5.3).
+// DIRECT: rows aligned to 16 bytes and K a multiple of 16 go to LDS directly, two steps under way; others through
+// registers, one step ahead.
+constexpr int kFewWaves = 8, kFewStep = 128;
+template <typename T, int TT, bool DIRECT>
 __global__ __launch_bounds__(64 * kFewWaves) void mm8_few_kernel(Mm8Params p) {
-    __shared__ i4 part[kFewWaves][TT][64];
-    const int l = lane_id(), w = uniform(threadIdx.x >> 6), waves = blockDim.x >> 6, K = p.K;
-    const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 16 * TT;
-    const int8_t* const wr = p.w + (int64_t)min(n0 + l % 16, p.N - 1) * p.sw;
-    const int8_t* xr[TT];
-    i4 acc[TT];
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-        xr[i] = p.x + (int64_t)min(t0 + 16 * i + l % 16, p.T - 1) * p.sx;
-        acc[i] = i4(0);
-    }
-    const int kl = (l / 16) * 16, turn = waves * kFewStep;
-    // one step's operands, and its products
-    struct Step {
-        i4 a[2], b[2][TT];
-    };
-    auto load = [&](Step& s, int k) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            s.a[h] = *reinterpret_cast<const i4u*>(wr + k + 64 * h + kl);
-#pragma unroll
-            for (int i = 0; i < TT; ++i) s.b[h][i] = *reinterpret_cast<const i4u*>(xr[i] + k + 64 * h + kl);
-        }
-    };
-    auto products = [&](const Step& s) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < TT; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(s.a[h], s.b[h][i], acc[i], 0, 0, 0);
-    };
-    int k = w * kFewStep;
-    for (; k + turn + kFewStep <= K; k += 2 * turn) {   // two steps' loads under way together
-        Step s, u;
-        load(s, k);
-        load(u, k + turn);
-        products(s);
-        products(u);
-    }
-    if (k + kFewStep <= K) {
-        Step s;
-        load(s, k);
-        products(s);
-        k += turn;
-    }
-    if (k < K) {   // the row's end
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const i4 a = row_chunk(wr, k + 64 * h + kl, K);
-#pragma unroll
-            for (int i = 0; i < TT; ++i)
-                acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, row_chunk(xr[i], k + 64 * h + kl, K), acc[i], 0, 0, 0);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < TT; ++i) part[w][i][l] = acc[i];
-    // wave i finishes the i-th 16 rows: lane l has row l % 16 and channels 4 (l / 16) ..
-    const int n = n0 + 4 * (l / 16);
-    float sw[4], bias[4];
-    if (w < TT) channels4(p, n, sw, bias);
-    __syncthreads();
-    if (w >= TT) return;
-    i4 s(0);
-    for (int v = 0; v < waves; ++v) s += part[v][w][l];
-    finish4<T>(p, s, t0 + 16 * w + l % 16, n, sw, bias);
-}
-
-// The same for rows aligned to 16 bytes and K a multiple of 16: a wave's steps come by loads of whole lines to LDS (a
-// line by eight neighbouring lanes; as the matrix instructions hold them, every lane's 16 bytes are a request of their
-// own, 64 x 4096 x 2048: 8.7 us), two steps under way.  The waves' stages are their own, so there is no barrier
-// before the sums.
-constexpr int kFewDirect = 8;   // waves
-template <typename T, int TT>
-__global__ __launch_bounds__(64 * kFewDirect) void mm8_few_direct_kernel(Mm8Params p) {
     constexpr int ROWS = 16 + 16 * TT, LD = ROWS / 8;
-    __shared__ __align__(16) i4 lds[kFewDirect][2][ROWS * 8];
+    __shared__ __align__(16) i4 lds[kFewWaves][2][ROWS * 8];
     const int l = lane_id(), w = uniform(threadIdx.x >> 6), steps = (p.K + kFewStep - 1) / kFewStep;
     const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 16 * TT;
-    const int8_t* src[LD];
+    const int8_t* row[LD];
+    int at[LD];   // the lane's byte of a step: chunk c of row r lies at c ^ r / 2 % 8
 #pragma unroll
     for (int j = 0; j < LD; ++j) {
         const int r = 8 * j + l / 8;
-        src[j] = (j < 2 ? p.w + (int64_t)min(n0 + r, p.N - 1) * p.sw : p.x + (int64_t)min(t0 + r - 16, p.T - 1) * p.sx) +
-                 ((l % 8) ^ (r / 2 % 8)) * 16;   // chunk c of row r lies at c ^ r / 2 % 8
+        row[j] = j < 2 ? p.w + (int64_t)min(n0 + r, p.N - 1) * p.sw : p.x + (int64_t)min(t0 + r - 16, p.T - 1) * p.sx;
+        at[j] = ((l % 8) ^ (r / 2 % 8)) * 16;
     }
+    i4 held[LD];   // not DIRECT: the next step's
     auto load = [&](int k, int stage) {
+        const int k0 = k * kFewStep;
 #pragma unroll
         for (int j = 0; j < LD; ++j) {
-            if ((k + 1) * kFewStep <= p.K) to_lds16(src[j] + (int64_t)k * kFewStep, &lds[w][stage][64 * j]);
-            else to_lds16_until(src[j] + (int64_t)k * kFewStep, &lds[w][stage][64 * j],
-                                ((l % 8) ^ ((8 * j + l / 8) / 2 % 8)) * 16 < p.K - k * kFewStep);
+            if (!DIRECT) held[j] = row_chunk(row[j], k0 + at[j], p.K);
+            else if (k0 + kFewStep <= p.K) to_lds16(row[j] + k0 + at[j], &lds[w][stage][64 * j]);
+            else to_lds16_until(row[j] + k0 + at[j], &lds[w][stage][64 * j], k0 + at[j] < p.K);
         }
     };
     i4 acc[TT];
 #pragma unroll
     for (int i = 0; i < TT; ++i) acc[i] = i4(0);
+    constexpr int AHEAD = DIRECT ? 2 * kFewWaves : kFewWaves;
     if (w < steps) load(w, 0);
-    if (w + kFewDirect < steps) load(w + kFewDirect, 1);
+    if (DIRECT && w + kFewWaves < steps) load(w + kFewWaves, 1);
     const int r = l % 16, sw = r / 2 % 8;
     int stage = 0;
-    for (int k = w; k < steps; k += kFewDirect, stage ^= 1) {
-        if (k + kFewDirect < steps) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LD) : "memory");   // the next step may be under way
-        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (int k = w; k < steps; k += kFewWaves, stage ^= 1) {
+        if (!DIRECT) {
+#pragma unroll
+            for (int j = 0; j < LD; ++j) lds[w][stage][64 * j + l] = held[j];
+        } else if (k + kFewWaves < steps) {
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LD) : "memory");   // the next step may be under way
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        if (!DIRECT && k + AHEAD < steps) load(k + AHEAD, stage);
+        if (DIRECT) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // zeros past a row's end
         i4 a[2], b[2][TT];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const i4* const at = lds[w][stage] + r * 8 + ((4 * h + l / 16) ^ sw);
-            a[h] = at[0];
+            const i4* const from = lds[w][stage] + r * 8 + ((4 * h + l / 16) ^ sw);
+            a[h] = from[0];
 #pragma unroll
-            for (int i = 0; i < TT; ++i) b[h][i] = at[128 * (i + 1)];
+            for (int i = 0; i < TT; ++i) b[h][i] = from[128 * (i + 1)];
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage is read
-        if (k + 2 * kFewDirect < steps) load(k + 2 * kFewDirect, stage);
+        if (DIRECT) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage is read
+            if (k + AHEAD < steps) load(k + AHEAD, stage);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < TT; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[h], b[h][i], acc[i], 0, 0, 0);
     }
+    // wave i finishes the i-th 16 rows: lane l has row l % 16 and channels 4 (l / 16) ..
     i4* const part = lds[w][0];   // the wave's own: nothing is under way to it
 #pragma unroll
     for (int i = 0; i < TT; ++i) part[64 * i + l] = acc[i];
@@ -223,7 +167,7 @@ __global__ __launch_bounds__(64 * kFewDirect) void mm8_few_direct_kernel(Mm8Para
     if (w >= TT) return;
     i4 s(0);
 #pragma unroll
-    for (int v = 0; v < kFewDirect; ++v) s += lds[v][0][64 * w + l];
+    for (int v = 0; v < kFewWaves; ++v) s += lds[v][0][64 * w + l];
     finish4<T>(p, s, t0 + 16 * w + l % 16, n, scale, bias);
 }
 
@@ -572,19 +516,12 @@ __global__ __launch_bounds__(256) void pack8_kernel(Pack8Params p) {
 template <typename T>
 hipError_t launch(const Mm8Params& p, hipStream_t st) {
     if (p.tile == 0) {
-        const int nb = (p.N + 15) / 16, few = (p.T + 15) / 16;
-        // waves of a workgroup: as many as have a step, at least one for each 16 rows it finishes
-        const int TT = few == 1 ? 1 : few == 2 || nb < 256 ? 2 : 4;
-        const int waves = std::max(TT, std::min(kFewWaves, (p.K + kFewStep - 1) / kFewStep));
-        if (p.direct) {
-            if (few == 1) mm8_few_direct_kernel<T, 1><<<dim3(nb, 1), 64 * kFewDirect, 0, st>>>(p);
-            else mm8_few_direct_kernel<T, 2><<<dim3(nb, (few + 1) / 2), 64 * kFewDirect, 0, st>>>(p);
-            return hipGetLastError();
-        }
-        const dim3 grid(nb, (few + TT - 1) / TT);
-        if (TT == 1) mm8_few_kernel<T, 1><<<grid, 64 * waves, 0, st>>>(p);
-        else if (TT == 2) mm8_few_kernel<T, 2><<<grid, 64 * waves, 0, st>>>(p);
-        else mm8_few_kernel<T, 4><<<grid, 64 * waves, 0, st>>>(p);
+        const int few = (p.T + 15) / 16;
+        const dim3 grid((p.N + 15) / 16, few == 1 ? 1 : (few + 1) / 2);
+        if (few == 1 && p.direct) mm8_few_kernel<T, 1, true><<<grid, 64 * kFewWaves, 0, st>>>(p);
+        else if (few == 1) mm8_few_kernel<T, 1, false><<<grid, 64 * kFewWaves, 0, st>>>(p);
+        else if (p.direct) mm8_few_kernel<T, 2, true><<<grid, 64 * kFewWaves, 0, st>>>(p);
+        else mm8_few_kernel<T, 2, false><<<grid, 64 * kFewWaves, 0, st>>>(p);
     } else {
         const int nb = (p.N + p.tile - 1) / p.tile, tb = (p.T + p.tile - 1) / p.tile;
         const unsigned blocks = (unsigned)nb * (unsigned)tb;
