@@ -12,7 +12,13 @@
 // channels are taken in the order of a counter, so a workgroup waits only for ones that run already, and for
 // nothing that these wait for; all the same the wait is bounded, and gives NaN where the bound is reached.
 //
-// Single tokens: a row a sequence, four channels a lane.
+// 8192 rows of 4096 channels in 13 sequences, bf16, 280 MB, take 80 us (3.5 TB/s), of which the gates' 39 instructions an
+// element issue for 46 %: reading, the gates and the wait for the rows before it follow each other in a tile and are
+// hidden by the other tiles of a CU only in part.  A plan before it takes 3 to 6 us, a launch and the words' clearing.
+// Two passes over ranges of rows, as the selective scan makes, formed the gates twice: 116 us.  Tiles of 64 rows took
+// 87 to 91 us, 16 waves of eight rows 97, four waves 82: less of the launch is rows then, or less is under way.
+//
+// Single tokens: a row a sequence, four channels a lane; 64 places of 2048 channels 4.1 us, a launch and its loads' latency.
 #include <algorithm>
 
 #include "gated.hpp"
@@ -46,7 +52,7 @@ __global__ __launch_bounds__(256) void tok_gated_plan_kernel(TokGatedParams p, i
     }
 }
 
-// Two channels of bf16 or one of fp32: 256 or 128 .. bytes of a row a wave.  EVEN: the lane's channels are all channels of
+// Two channels of bf16 or one of fp32, so that a wave reads 256 bytes of a row.  EVEN: the lane's channels are all channels of
 // the layer, or, past the last one, the last ones again, whose results go nowhere; otherwise one by one.
 template <typename T> struct Few;
 template <> struct Few<bf16_t> {
