@@ -615,7 +615,9 @@ int ssm_tokens_scan(const ssm_tokens_scan_args* args, void* ws, size_t ws_bytes,
  *   q = power * softplus(lam) * rho,  a = exp(-q),
  *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) iota_t x_t,   y_t = h_t,   h_{-1} = h0.
  * The states and everything that forms them are float32.  Where a gate's input
- * lies below about -87 its sigmoid is 0.  Strides are in elements: batch, then
+ * lies below about -87 its sigmoid is 0.  power * softplus(lam) is to stay below
+ * 2^64 and the states below 2^60: past them products of float32 overflow.
+ * Strides are in elements: batch, then
  * channel; steps are contiguous; 0 (broadcast) for inputs only, whose gradients
  * come back for every position.  batch, channels and length may be 0 (h_last is
  * then h0 or 0, gh0 is gh_last or 0, parameter gradients are 0).
@@ -663,7 +665,9 @@ int ssm_gated_bwd(const ssm_gated_args* args, const ssm_gated_bwd_in* in, const 
                   void* ws, size_t ws_bytes, void* stream);
 
 /* The gated recurrence over packed rows, with sequences, pool and rows as in ssm_tokens_conv above.  The workspace
- * (SSM_OP_TOKENS_GATED) holds what one tile of rows hands on to the next; the step form needs none. */
+ * (SSM_OP_TOKENS_GATED) holds what one tile of rows hands on to the next; the step form needs none.  Of calls that
+ * overlap in time each needs a workspace of its own: in one that another call writes to meanwhile the wait for the tile
+ * before is bounded and ends in NaN, and no access leaves the buffers. */
 typedef struct {
     int32_t dtype;             /* of x, r, i and y                                           */
     float   power;
@@ -723,8 +727,9 @@ int ssm_group_norm_bwd(const ssm_group_norm_args* args, const void* gy, int64_t 
  * that have a scale for each output:
  *   y[t][n] = x8_scale[t] w8_scale[n] sum_k x8[t][k] w8[n][k] + bias[n].
  * The sums are whole numbers in 32 bits (inputs below 2^17: they cannot overflow),
- * rounded once to float32 before the scales.  Rows may have any stride from 0 (inputs) or
- * their own width (outputs) to 2^40 - 1.  With no inputs y is bias.
+ * rounded once to float32 before the scales, whose product is formed first: where that leaves float32's range y is
+ * infinite or NaN.  Rows may have any stride from 0 (inputs) or their own width (outputs) to 2^40 - 1.  With no inputs
+ * y is bias.  SSM_ERR_SHAPE for 2^17 inputs, 2^24 tokens or 2^26 outputs and more.
  */
 typedef struct {
     int32_t dtype;             /* of x                                                       */

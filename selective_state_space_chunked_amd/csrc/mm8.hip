@@ -531,6 +531,7 @@ hipError_t launch(const Mm8Params& p, hipStream_t st) {
     } else {
         const int nb = (p.N + p.tile - 1) / p.tile, tb = (p.T + p.tile - 1) / p.tile;
         const unsigned blocks = (unsigned)nb * (unsigned)tb;
+        // as many workgroups as the 256 CUs hold at a time: one, two or four by their LDS (137, 69 and 34 KB of 160)
         if (p.direct && p.tile == 256)
             mm8_direct_kernel<T, 256, 256, 2, 4><<<std::min(blocks, 256u), 512, 0, st>>>(p, nb, tb);
         else if (p.direct && p.tile == 128)

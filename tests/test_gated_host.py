@@ -39,6 +39,8 @@ def gated_args(**over):
     (dict(batch=32, channels=(1 << 23) + 64, length=2), "SHAPE"), (dict(power=0.0), "SHAPE"), (dict(power=-1.0), "SHAPE"), (dict(power=float("nan")), "SHAPE"),
     (dict(power=float("inf")), "SHAPE"), (dict(x=None), "NULL"), (dict(r=None), "NULL"), (dict(i=None), "NULL"),
     (dict(lam=None), "NULL"), (dict(x_stride=(800, -1)), "LAYOUT"), (dict(r_stride=(1 << 40, 100)), "LAYOUT"),
+    (dict(batch=1, channels=1 << 23, i_stride=(0, (1 << 40) - 1)), "LAYOUT"),   # a span that passes 64 bits
+    (dict(batch=1, channels=1 << 23, x_stride=(0, 1 << 24)), "LAYOUT"),
     (dict(i=3 * FAKE + 2), "LAYOUT"), (dict(lam=4 * FAKE + 2), "LAYOUT"), (dict(r_bias=5 * FAKE + 1), "LAYOUT"),
     (dict(h0=5 * FAKE + 2), "LAYOUT"), (dict(i_bias=7 * FAKE + 3), "LAYOUT"),
 ])
