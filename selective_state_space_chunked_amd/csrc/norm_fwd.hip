@@ -22,51 +22,38 @@ __global__ __launch_bounds__(norm_threads(TEAM)) void norm_fwd_kernel(NormParams
             b[i][e] = p.bias ? p.bias[at.at[i] + e] : 0.0f;
         }
     if (at.row >= at.end) return;
-    // Rows under way together: the loads of two rows a wave are in flight while two are worked on, where a lane has one
-    // vector of each (16384 x 2048 in groups of 64, bf16 with a gate: 47.9 us, one row at a time 52).
-    constexpr int K = R * V <= 8 && TEAM == 64 ? 2 : 1;
-    Chan<T, V> cx[K][R], cz[K][R];
+    Chan<T, V> cx[R], cz[R];
     const T* const x = (const T*)p.x;
     const T* const z = (const T*)p.z;
+    // The next row comes while one is worked on.  (Two rows at a time are no faster where a lane has one vector of each,
+    // and slower where it has single elements: 16384 x 2080 in groups of 65, bf16, 60 us and 73.)
     auto load = [&](int row) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int r = min(row + k * at.step, at.end - 1);
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                cx[k][i].load(x + r * p.sx + at.at[i]);
-                if (z) cz[k][i].load(z + r * p.sz + at.at[i]);
-            }
+        for (int i = 0; i < R; ++i) {
+            cx[i].load(x + row * p.sx + at.at[i]);
+            if (z) cz[i].load(z + row * p.sz + at.at[i]);
         }
     };
     load(at.row);
-    for (int row = at.row; row < at.end; row += K * at.step) {
-        float v[K][R][V], g[K][R][V];
+    for (int row = at.row; row < at.end; row += at.step) {
+        float v[R][V], g[R][V];
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int i = 0; i < R; ++i) {
+            cx[i].get(v[i]);
+            if (z) cz[i].get(g[i]);
+        }
+        load(min(row + at.step, at.end - 1));
+        normalise<TEAM, V, R>(v, at.has, p, lds);
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                cx[k][i].get(v[k][i]);
-                if (z) cz[k][i].get(g[k][i]);
+        for (int i = 0; i < R; ++i) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                float u = fmaf(v[i][e], w[i][e], b[i][e]);
+                if (p.silu) u *= sigmoid_f(u);
+                if (z) u *= g[i][e] * sigmoid_f(g[i][e]);
+                v[i][e] = u;
             }
-        load(row + K * at.step);
-#pragma unroll
-        for (int k = 0; k < K; ++k) normalise<TEAM, V, R>(v[k], at.has, p, lds);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int r = row + k * at.step;
-            if (r >= at.end) break;
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    float u = fmaf(v[k][i][e], w[i][e], b[i][e]);
-                    if (p.silu) u *= sigmoid_f(u);
-                    if (z) u *= g[k][i][e] * sigmoid_f(g[k][i][e]);
-                    v[k][i][e] = u;
-                }
-                if (at.has[i]) Chan<T, V>::store((T*)p.y + r * p.sy + at.at[i], v[k][i]);
-            }
+            if (at.has[i]) Chan<T, V>::store((T*)p.y + row * p.sy + at.at[i], v[i]);
         }
     }
 }

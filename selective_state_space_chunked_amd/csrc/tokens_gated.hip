@@ -15,8 +15,9 @@
 // 8192 rows of 4096 channels in 13 sequences, bf16, 280 MB, take 80 us (3.5 TB/s), of which the gates' 39 instructions an
 // element issue for 46 %: reading, the gates and the wait for the rows before it follow each other in a tile and are
 // hidden by the other tiles of a CU only in part.  A plan before it takes 3 to 6 us, a launch and the words' clearing.
-// Two passes over ranges of rows, as the selective scan makes, formed the gates twice: 116 us.  Tiles of 64 rows took
-// 87 to 91 us, 16 waves of eight rows 97, four waves 82: less of the launch is rows then, or less is under way.
+// Two passes over ranges of rows, as the selective scan makes, formed the gates twice: 116 us.  Eight waves of eight
+// rows took 91 us, four of 16 rows 82, 16 of eight rows 97, when this form took 75 (before it went forward through the
+// maps): a tile has less under way then, or more waves to compose.
 //
 // Single tokens: a row a sequence, four channels a lane; 64 places of 2048 channels 4.1 us, a launch and its loads' latency.
 #include <algorithm>

@@ -436,7 +436,7 @@ def test_norm(T, G, per, silu, gate, dtype):
     norm_check(t, gy, G, dtype, silu)
 
 
-@pytest.mark.parametrize("T, G, per, dtype", [(2111, 31, 65, "f32"), (2111, 31, 65, "bf16"), (4099, 75, 14, "bf16"),
+@pytest.mark.parametrize("T, G, per, dtype", [(2111, 31, 65, "f32"), (2111, 31, 65, "bf16"), (4099, 75, 14, "bf16"), (3001, 7, 27, "f32"),
                                               (16400, 3, 127, "f32"), (40001, 10, 11, "f32")])
 def test_norm_many_rows_of_odd_groups(T, G, per, dtype):
     t, gy = norm_inputs(T, G * per, dtype, gen(T + G + per))
