@@ -374,7 +374,6 @@ struct TokGatedParams {
     int* slots;                      // (S) the sequences' slots, -1 for empty places
 };
 constexpr int kGatedTile = 128;
-template <int DTYPE> constexpr int kGatedFew = DTYPE == 1 ? 2 : 1;   // channels of a lane: two of bf16, one of fp32
 hipError_t launch_tok_gated_plan(const TokGatedParams& p, hipStream_t st);
 hipError_t launch_tok_gated(const TokGatedParams& p, int dtype, hipStream_t st);
 hipError_t launch_tok_gated_step(const TokGatedParams& p, int dtype, hipStream_t st);

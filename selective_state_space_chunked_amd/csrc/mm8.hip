@@ -9,7 +9,7 @@
 // lane's results are consecutive channels of one row of y.
 //
 // 8192 x 4096 x 8192 to bf16 takes 244 us while the card is cool (2.2 Pop/s; the library's product of the same operands,
-// without scales, 252) and about 285 with one product after the other, when its power limit lowers the clock.  The
+// without scales, 252) and 275 to 285 with one product after the other, when its power limit lowers the clock.  The
 // matrix instructions are busy for 54 to 62 % of the cycles; of 424 thousand, the results' scaling and stores are 34, the
 // loads 64.  64 x 4096 x 2048 takes 5.3 us and 1 x 2048 x 4096 3.5, where the weights alone are 1.8 us of traffic: latency.
 // Rows to 8 bits: 8192 x 4096 bf16 in 20 to 22 us (101 MB, 4.6 to 5.0 TB/s).

@@ -1,6 +1,6 @@
 // The gated linear recurrence (gated.hpp) over packed rows, with a pool of states.
 //
-// Prompts, in one pass.  A workgroup takes a tile of 128 rows and 64 lanes' channels, each of its eight waves 16 of the
+// Prompts, in one pass.  A workgroup takes a tile of 128 rows and 64 channels, each of its eight waves 16 of the
 // rows: the streams are read once, along the channels as the projections write them, and what the gates make of them,
 // a and b of h <- a h + b, stays in registers.  Where a sequence begins, its first state goes into b and
 // nothing comes in from the row before, nor does it where no sequence owns a row: so from there on the rows are one
@@ -12,12 +12,13 @@
 // channels are taken in the order of a counter, so a workgroup waits only for ones that run already, and for
 // nothing that these wait for; all the same the wait is bounded, and gives NaN where the bound is reached.
 //
-// 8192 rows of 4096 channels in 13 sequences, bf16, 280 MB, take 80 us (3.5 TB/s), of which the gates' 39 instructions an
-// element issue for 46 %: reading, the gates and the wait for the rows before it follow each other in a tile and are
-// hidden by the other tiles of a CU only in part.  A plan before it takes 3 to 6 us, a launch and the words' clearing.
-// Two passes over ranges of rows, as the selective scan makes, formed the gates twice: 116 us.  Eight waves of eight
-// rows took 91 us, four of 16 rows 82, 16 of eight rows 97, when this form took 75 (before it went forward through the
-// maps): a tile has less under way then, or more waves to compose.
+// 8192 rows of 4096 channels in 13 sequences, bf16, 276 MB, take 74 us (3.7 TB/s), of which the gates' 41 instructions an
+// element issue for 53 %: reading, the gates and the wait for the rows before it follow each other in a tile and are
+// hidden by the other tiles of a CU only in part.  A lane has one channel, so three workgroups fit a CU (two channels of
+// bf16: two workgroups, 80 us).  Tiles by four waves take 82, by 16 waves of 16 rows 95, of eight rows 124, by eight waves
+// of eight rows 100: fewer rows are under way for each wait, or more maps to compose.  Two passes over ranges of rows,
+// as the selective scan makes, formed the gates twice: 116 us.  The plan before it takes 3 to 5 us, a launch and
+// the words' clearing.
 //
 // Single tokens: a row a sequence, four channels a lane; 64 places of 2048 channels 4.1 us, a launch and its loads' latency.
 #include <algorithm>
@@ -53,38 +54,6 @@ __global__ __launch_bounds__(256) void tok_gated_plan_kernel(TokGatedParams p, i
     }
 }
 
-// Two channels of bf16 or one of fp32, so that a wave reads 256 bytes of a row.  EVEN: the lane's channels are all channels of
-// the layer, or, past the last one, the last ones again, whose results go nowhere; otherwise one by one.
-template <typename T> struct Few;
-template <> struct Few<bf16_t> {
-    static constexpr int V = kGatedFew<1>;
-    typedef uint32_t raw __attribute__((aligned(2)));
-    uint32_t r;
-    template <bool EVEN> __device__ __forceinline__ void load(const bf16_t* row, int d, int D) {
-        if (EVEN) r = *reinterpret_cast<const raw*>(row + d);
-        else r = (uint32_t)row[min(d, D - 1)] | (uint32_t)row[min(d + 1, D - 1)] << 16;
-    }
-    __device__ __forceinline__ float get(int e) const { return __uint_as_float(e ? r & 0xffff0000u : r << 16); }
-    template <bool EVEN> __device__ __forceinline__ static void store(bf16_t* row, int d, int n, const float (&v)[2]) {
-        if (EVEN) {
-            if (n > 0) *reinterpret_cast<raw*>(row + d) = (uint32_t)to_stream<bf16_t>(v[0]) | (uint32_t)to_stream<bf16_t>(v[1]) << 16;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (e < n) row[d + e] = to_stream<bf16_t>(v[e]);
-        }
-    }
-};
-template <> struct Few<float> {
-    static constexpr int V = kGatedFew<0>;
-    float r;
-    template <bool EVEN> __device__ __forceinline__ void load(const float* row, int d, int D) { r = row[min(d, D - 1)]; }
-    __device__ __forceinline__ float get(int) const { return r; }
-    template <bool EVEN> __device__ __forceinline__ static void store(float* row, int d, int n, const float (&v)[1]) {
-        if (n > 0) row[d] = v[0];
-    }
-};
-
 // What a wave's rows are, in lane j that of row j: the slot of the sequence that owns it (-1: none), whether the row is
 // its first one, its last one, and whether it begins with zeros.
 struct RowInfo {
@@ -112,36 +81,33 @@ struct RowInfo {
 };
 
 // The waves' maps, whether a wave's map forgets what comes in, and the state that comes into the tile.
-template <int V> struct TileMaps {
-    float P[kTileWaves][64 * V], S[kTileWaves][64 * V], carry[64 * V];
+struct TileMaps {
+    float P[kTileWaves][64], S[kTileWaves][64], carry[64];
     int cut[kTileWaves];
 };
 
-template <typename T, bool EVEN, bool SLOW>
-__device__ __forceinline__ void gated_tile(const TokGatedParams& p, int tile, int d0, const GateChannel (&c)[Few<T>::V],
-                                           const SeqTable& seqs, TileMaps<Few<T>::V>& maps) {
-    constexpr int V = Few<T>::V, R = kWaveRows;
+// A lane has one channel d, or, past the last one, the last one again, whose results go nowhere.
+template <typename T, bool SLOW>
+__device__ __forceinline__ void gated_tile(const TokGatedParams& p, int tile, int d, bool live, const GateChannel& c,
+                                           const SeqTable& seqs, TileMaps& maps) {
+    constexpr int R = kWaveRows;
     const int l = lane_id(), w = uniform(threadIdx.x >> 6), r0 = tile * kGatedTile + w * R;
-    const int d = d0 + V * l, at = EVEN ? min(d, p.D - V) : d, n = max(0, min(V, p.D - d));
-    float a[R][V], b[R][V];
+    float a[R], b[R];
     RowInfo info;
     {
-        Few<T> x[R], r[R], g[R];
+        T x[R], r[R], g[R];
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             const int t = min(r0 + j, p.q.T - 1);
-            x[j].template load<EVEN>((const T*)p.x + t * p.sx, at, p.D);
-            r[j].template load<EVEN>((const T*)p.r + t * p.sr, at, p.D);
-            g[j].template load<EVEN>((const T*)p.i + t * p.si, at, p.D);
+            x[j] = ((const T*)p.x + t * p.sx)[d];
+            r[j] = ((const T*)p.r + t * p.sr)[d];
+            g[j] = ((const T*)p.i + t * p.si)[d];
         }
         info = RowInfo(p, seqs, r0);   // while the rows come
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float v = gate_rest<SLOW>(c[e].rate * gate_open(r[j].get(e), c[e].rb), a[j][e]);
-                b[j][e] = __builtin_amdgcn_sqrtf(v) * (gate_open(g[j].get(e), c[e].ib) * x[j].get(e));
-            }
+            const float v = gate_rest<SLOW>(c.rate * gate_open(to_f32(r[j]), c.rb), a[j]);
+            b[j] = __builtin_amdgcn_sqrtf(v) * (gate_open(to_f32(g[j]), c.ib) * to_f32(x[j]));
         }
     }
     // cut: rows that nothing comes into from the row before.  They are chosen, not multiplied by 0: a sequence's NaN or
@@ -152,88 +118,61 @@ __device__ __forceinline__ void gated_tile(const TokGatedParams& p, int tile, in
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             if (!(owned >> j & 1)) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) b[j][e] = 0.0f;
+                b[j] = 0.0f;
             } else if (first >> j & 1) {
                 const float* const h0 = p.pool + __builtin_amdgcn_readlane(info.slot, j) * p.spool;
-                if (!__builtin_amdgcn_readlane(info.fresh, j)) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) b[j][e] = fmaf(a[j][e], h0[min(d + e, p.D - 1)], b[j][e]);
-                }
+                if (!__builtin_amdgcn_readlane(info.fresh, j)) b[j] = fmaf(a[j], h0[d], b[j]);
             }
         }
     }
-    float P[V], S[V];
+    float P = a[0], S = b[0];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        P[e] = a[0][e];
-        S[e] = b[0][e];
-#pragma unroll
-        for (int j = 1; j < R; ++j) {
-            S[e] = cut >> j & 1 ? b[j][e] : fmaf(a[j][e], S[e], b[j][e]);
-            P[e] *= a[j][e];
-        }
-        maps.P[w][V * l + e] = P[e];
-        maps.S[w][V * l + e] = S[e];
+    for (int j = 1; j < R; ++j) {
+        S = cut >> j & 1 ? b[j] : fmaf(a[j], S, b[j]);
+        P *= a[j];
     }
+    maps.P[w][l] = P;
+    maps.S[w][l] = S;
     if (l == 0) maps.cut[w] = cut != 0;
     __syncthreads();
     // the map of the rows of the workgroup before the wave's own; the first wave: of all, for the tiles behind
     bool forgets = false;   // nothing comes through: S is a state
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        P[e] = 1.0f;
-        S[e] = 0.0f;
-    }
+    P = 1.0f;
+    S = 0.0f;
     for (int k = 0; k < (w ? w : kTileWaves); ++k) {
         const bool c = uniform(maps.cut[k]) != 0;
         forgets |= c;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float m = maps.P[k][V * l + e], v = maps.S[k][V * l + e];
-            S[e] = c ? v : fmaf(m, S[e], v);
-            P[e] *= m;
-        }
+        const float m = maps.P[k][l], v = maps.S[k][l];
+        S = c ? v : fmaf(m, S, v);
+        P *= m;
     }
     if (w == 0) {
-        uint64_t* const map = p.maps + (int64_t)tile * p.D;
-        uint32_t* const state = (uint32_t*)(p.maps + (int64_t)p.tiles * p.D) + (int64_t)tile * p.D;
-        float C[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            C[e] = 0.0f;
-            if (e < n) {   // (into the first tile nothing comes)
-                if (tile == 0 || forgets) put_word(state + d + e, word_of(S[e]));
-                else put_word(map + d + e, (uint64_t)word_of(S[e]) << 32 | word_of(P[e]));
-            }
+        uint64_t* const map = p.maps + (int64_t)tile * p.D + d;
+        uint32_t* const state = (uint32_t*)(p.maps + (int64_t)p.tiles * p.D) + (int64_t)tile * p.D + d;
+        float C = 0.0f;
+        if (live) {   // (into the first tile nothing comes)
+            if (tile == 0 || forgets) put_word(state, word_of(S));
+            else put_word(map, (uint64_t)word_of(S) << 32 | word_of(P));
         }
         if (tile > 0 && !(cut & 1)) {   // otherwise no row takes what comes in
             // Back to the last tile before this one whose state is known, with all maps between there, eight tiles' words
             // under way together.
             constexpr int AHEAD = 8;
-            const auto place = [&](int k, int e) { return (int64_t)(max(k, 0) - tile) * p.D + min(d + e, p.D - 1); };
+            const auto place = [&](int k) { return (int64_t)(max(k, 0) - tile) * p.D; };
             int k = tile - 1, polls = 0;
             for (bool found = false; !found;) {
-                uint32_t h[AHEAD][V], m[AHEAD][V];
+                uint32_t h[AHEAD], m[AHEAD];
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i)
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        h[i][e] = get_word(state + place(k - i, e));
-                        m[i][e] = get_word((const uint32_t*)(map + place(k - i, e)));   // half of a map: all of it is there
-                    }
+                for (int i = 0; i < AHEAD; ++i) {
+                    h[i] = get_word(state + place(k - i));
+                    m[i] = get_word((const uint32_t*)(map + place(k - i)));   // half of a map: all of it is there
+                }
                 bool wait = false;
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
-                    bool nostate = false, nomap = false;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        nostate |= h[i][e] == kNone;
-                        nomap |= m[i][e] == kNone;
-                    }
                     if (found || wait) continue;
-                    if (!__ballot(nostate)) found = true;
-                    else if (k <= 0 || __ballot(nomap)) wait = true;   // (before the first tile there is none)
+                    if (!__ballot(h[i] == kNone)) found = true;
+                    else if (k <= 0 || __ballot(m[i] == kNone)) wait = true;   // (before the first tile there is none)
                     else --k;
                 }
                 if (wait) {
@@ -244,80 +183,54 @@ __device__ __forceinline__ void gated_tile(const TokGatedParams& p, int tile, in
                 }
             }
             // From there on through the maps: the same products and sums whichever tile it is, so the same bits.
-#pragma unroll
-            for (int e = 0; e < V; ++e) C[e] = polls > kPolls ? __uint_as_float(0x7fc00000u) : __uint_as_float(get_word(state + place(k, e)));
+            C = polls > kPolls ? __uint_as_float(0x7fc00000u) : __uint_as_float(get_word(state + place(k)));
             while (++k < tile) {
-                uint64_t m[AHEAD][V];
+                uint64_t m[AHEAD];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) m[i] = get_word(map + place(min(k + i, tile - 1)));
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i)
-#pragma unroll
-                    for (int e = 0; e < V; ++e) m[i][e] = get_word(map + place(min(k + i, tile - 1), e));
-#pragma unroll
-                for (int i = 0; i < AHEAD; ++i)
-#pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        if (k + i < tile)
-                            C[e] = fmaf(__uint_as_float((uint32_t)m[i][e]), C[e], __uint_as_float((uint32_t)(m[i][e] >> 32)));
+                    if (k + i < tile)
+                        C = fmaf(__uint_as_float((uint32_t)m[i]), C, __uint_as_float((uint32_t)(m[i] >> 32)));
                 k += AHEAD - 1;
             }
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (e < n && !forgets) put_word(state + d + e, word_of(fmaf(P[e], C[e], S[e])));
+            if (live && !forgets) put_word(state, word_of(fmaf(P, C, S)));
         }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            maps.carry[V * l + e] = C[e];
-            P[e] = 1.0f;
-            S[e] = 0.0f;
-        }
+        maps.carry[l] = C;
+        P = 1.0f;
+        S = 0.0f;
     }
     __syncthreads();
     // the state that the wave's rows begin with
-    float h[V];
-    const bool through = w == 0 || !forgets;
-#pragma unroll
-    for (int e = 0; e < V; ++e) h[e] = through ? fmaf(P[e], maps.carry[V * l + e], S[e]) : S[e];
+    float h = w == 0 || !forgets ? fmaf(P, maps.carry[l], S) : S;
     const uint32_t last = (uint32_t)__ballot(info.last != 0) & owned;
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = cut >> j & 1 ? b[j][e] : fmaf(a[j][e], h[e], b[j][e]);
-        if (owned >> j & 1) Few<T>::template store<EVEN>((T*)p.y + (r0 + j) * p.sy, at, n, h);
-        if (last >> j & 1) {
-            float* const pool = p.pool + __builtin_amdgcn_readlane(info.slot, j) * p.spool;
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (e < n) pool[d + e] = h[e];
-        }
+        h = cut >> j & 1 ? b[j] : fmaf(a[j], h, b[j]);
+        if (live && (owned >> j & 1)) ((T*)p.y + (r0 + j) * p.sy)[d] = to_stream<T>(h);
+        if (live && (last >> j & 1)) p.pool[__builtin_amdgcn_readlane(info.slot, j) * p.spool + d] = h;
     }
 }
 template <typename T>
-__global__ __launch_bounds__(64 * kTileWaves, 4) void tok_gated_kernel(TokGatedParams p) {
-    constexpr int V = Few<T>::V;
-    __shared__ TileMaps<V> maps;
+__global__ __launch_bounds__(64 * kTileWaves, 6) void tok_gated_kernel(TokGatedParams p) {
+    __shared__ TileMaps maps;
     __shared__ int taken;
-    const int column = blockIdx.x % p.columns, d0 = column * 64 * V;
+    const int column = blockIdx.x % p.columns, d = column * 64 + lane_id();
     const SeqTable seqs(p.q);
     if (threadIdx.x == 0) taken = __hip_atomic_fetch_add(p.ticket + column, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    GateChannel c[V];
-    bool fast = false;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        c[e] = gate_channel(p.lam, p.rb, p.ib, p.power, min(d0 + V * lane_id() + e, p.D - 1));
-        fast |= !(c[e].rate < kGateSlow);
-    }
-    const bool slow = __ballot(fast) == 0, even = p.D % V == 0 || d0 + 64 * V <= p.D;
+    const GateChannel c = gate_channel(p.lam, p.rb, p.ib, p.power, min(d, p.D - 1));
+    const bool slow = __ballot(!(c.rate < kGateSlow)) == 0;
     __syncthreads();
     const int tile = uniform(taken);
     if (tile < 0 || tile >= p.tiles) return;   // (as above)
-    if (even && slow) gated_tile<T, true, true>(p, tile, d0, c, seqs, maps);
-    else if (even) gated_tile<T, true, false>(p, tile, d0, c, seqs, maps);
-    else gated_tile<T, false, false>(p, tile, d0, c, seqs, maps);
+    if (slow) gated_tile<T, true>(p, tile, min(d, p.D - 1), d < p.D, c, seqs, maps);
+    else gated_tile<T, false>(p, tile, min(d, p.D - 1), d < p.D, c, seqs, maps);
 }
 
 constexpr int kCh = 4;    // channels of a lane of the step kernel
 
-// One row a sequence.  EVEN: as above, of four channels a lane.
+// One row a sequence, four channels a lane.  EVEN: the lane's channels are all channels of the layer, or, past the last
+// one, the last ones again, whose results go nowhere; otherwise one by one.
 template <typename T, bool EVEN>
 __device__ __forceinline__ void step_row(const TokGatedParams& p, int s, int slot, int d0) {
     const bool live = d0 < p.D;
