@@ -56,7 +56,7 @@ __global__ __launch_bounds__(norm_threads(TEAM)) void norm_bwd_kernel(NormParams
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float v = fmaf(xh[i][e], w[i][e], b[i][e]);
-                    float gv = at.has[i] ? g[i][e] : 0.0f;
+                    float gv = g[i][e];
                     const float sv = p.silu ? sigmoid_f(v) : 1.0f;
                     if (z) {
                         const float zz = zv[i][e], sz = sigmoid_f(zz);
@@ -66,7 +66,9 @@ __global__ __launch_bounds__(norm_threads(TEAM)) void norm_bwd_kernel(NormParams
                     if (p.silu) gv *= sv * fmaf(v, 1.0f - sv, 1.0f);
                     gw[i][e] = fmaf(gv, xh[i][e], gw[i][e]);
                     gb[i][e] += gv;
-                    g[i][e] = gv * w[i][e];
+                    // chosen, not multiplied by 0: a lane without channels has read the row's first ones, which may be of
+                    // another group and not finite
+                    g[i][e] = at.has[i] ? gv * w[i][e] : 0.0f;
                     m[0] += g[i][e];
                     m[1] = fmaf(g[i][e], xh[i][e], m[1]);
                 }
