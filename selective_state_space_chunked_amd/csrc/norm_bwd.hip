@@ -144,7 +144,10 @@ hipError_t launch(const NormParams& p, hipStream_t st) {
     const unsigned blocks = (unsigned)p.gblocks * (unsigned)p.chunks;
     if (p.team == 64) norm_bwd_kernel<T, 64, V, R><<<blocks, norm_threads(64), 0, st>>>(p);
     else if (p.team == 256) norm_bwd_kernel<T, 256, V, R><<<blocks, 256, 0, st>>>(p);
-    else norm_bwd_kernel<T, 1024, V, R><<<blocks, 1024, 0, st>>>(p);
+    else if constexpr (V * R <= 8)
+        norm_bwd_kernel<T, 1024, V, R><<<blocks, 1024, 0, st>>>(p);
+    else   // (a group has at most kNormMost channels: 1024 lanes of one vector of eight)
+        return hipErrorInvalidValue;
     return hipGetLastError();
 }
 template <typename T, int V>
