@@ -1371,6 +1371,8 @@ def _norm_args(x, groups, w, bias, eps, silu, z, st):
         raise ValueError(f"x has shape {tuple(x.shape)}; expected (T, C)")
     if not isinstance(groups, int):
         raise TypeError("groups must be an int")
+    if not -2**63 <= groups < 2**63:
+        raise ValueError(f"groups={groups} is out of range")
     T, C = x.shape
     if st is not None and x.dtype is not st:
         raise TypeError(f"x has dtype {x.dtype}, expected {st}")

@@ -1,6 +1,10 @@
-"""Host side of the gated layer's operators: which kernels the library holds.  No GPU."""
+"""Host side of the gated layer's operators: which kernels the library holds, arguments that no field holds.  No GPU."""
 import re
 
+import pytest
+import torch
+
+import selective_state_space_chunked_amd as ssm
 from selective_state_space_chunked_amd import binding as B
 
 
@@ -31,3 +35,12 @@ def norm_forms(most):
 def test_every_group_norm_kernel_is_reached():
     for name in ("norm_fwd_kernel", "norm_bwd_kernel"):
         assert kernels(name) == norm_forms(8) | norm_forms(4), name
+
+
+@pytest.mark.parametrize("groups", [2**63, -2**63 - 1, 10**30])
+def test_norm_refuses_counts_of_groups_past_64_bits(groups):
+    x = torch.zeros(4, 6)
+    with pytest.raises(ValueError, match="groups"):
+        ssm.group_norm_fwd(x=x, groups=groups)
+    with pytest.raises(ValueError, match="groups"):
+        ssm.group_norm_bwd(gy=x, x=x, groups=groups)
