@@ -1,13 +1,55 @@
-"""The gated layer's operators on the GPU where their kernels take other ways than at the sizes of test_gpu_gated.py: values
-that are not finite beside lanes without channels."""
+"""The gated layer's operators on the GPU where their kernels take other ways than at the sizes of test_gpu_gated.py: rows of
+several tiles, values that are not finite beside lanes without channels.  Which kernel a call runs is asked of the library's
+diagnostics, so that a size whose kernel changes fails its test."""
+import ctypes
+
 import pytest
 import torch
 
 import selective_state_space_chunked_amd as ssm
+from selective_state_space_chunked_amd import binding
 
-from .test_gpu_gated import DEV, gen, norm_inputs
+from . import _gated_ref as R
+from .test_gpu_gated import GATED_OUT, f64, gated_inputs, gen, norm_inputs
 
 pytestmark = pytest.mark.gpu
+
+
+def launched(f):
+    """f's result and the names of the kernels its calls enqueued."""
+    L, n, names = binding.lib(), ctypes.c_int(0), (ctypes.c_char_p * 64)()
+    assert L.ssm_profile_begin(ctypes.c_int(64)) == 0
+    try:
+        r = f()
+    finally:
+        rc = L.ssm_profile_end(ctypes.byref(n), (ctypes.c_float * 64)(), names, ctypes.c_int(64))
+    assert rc == 0
+    return r, [names[i].decode() for i in range(n.value)]
+
+
+# ---------------------------------------------------------------------------
+# gated recurrence
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,D,L,lanes", [(8, 8200, 299, 16), (8, 2051, 1100, 64), (5, 900, 4500, 256), (3, 40, 20011, 1024)])
+def test_gated_rows_of_several_tiles(B, D, L, lanes, dtype):
+    """Each number of lanes a row goes round its tiles three times, the last time with a part of one: states and mu are
+    carried from tile to tile, in slow channels over all of the row.  Against the reference for some of the channels."""
+    r = gen(B + L)
+    t, gy, gl = gated_inputs(B, D, L, dtype, r)
+    t["lam"][::2] -= 6.0
+    f, names = launched(lambda: ssm.gated_fwd(want_h_last=True, want_ckpt=True, **t))
+    assert names == [f"gated recurrence, {lanes} lanes a row"] and 2 * lanes * 8 < L < 3 * lanes * 8
+    g, names = launched(lambda: ssm.gated_bwd(gy=gy, gh_last=gl, ckpt=f["ckpt"], **t))
+    assert names[0] == f"gated recurrence backward, {lanes} lanes a row"
+    some = sorted({0, 1, 2, 3, D // 2, D - 2, D - 1, *(int(v) for v in r.integers(0, D, 5))})
+    v = [f64(t[k][some] if k in ("lam", "r_bias", "i_bias") else t[k][:, some]) for k in ("x", "r", "i", "lam", "r_bias", "i_bias")]
+    v += [8.0, f64(t["h0"][:, some])]
+    ref = {**R.gated_fwd(*v), **R.gated_bwd(*v, f64(gy[:, some]), f64(gl[:, some]))}
+    for k, got in {"y": f["y"], "h_last": f["h_last"], **g}.items():
+        R.check(k, got[some] if got.dim() == 1 else got[:, some], *ref[k], "f32" if k in GATED_OUT else dtype)
+    again = ssm.gated_bwd(gy=gy, gh_last=gl, **t)   # the states formed again
+    assert all(torch.equal(g[k], again[k]) for k in g)
 
 
 # ---------------------------------------------------------------------------
