@@ -81,3 +81,30 @@ def test_norm_non_finite_values_stay_in_their_group(G, per, dtype):
                     else:
                         keep[rows, own] = False
                     assert torch.equal(got[k][keep], ref[k][keep]), (name, at, bad, k)
+
+
+VECTOR, TWO, EIGHT = "a vector each", "two vectors each", "eight channels each"
+
+
+@pytest.mark.parametrize("dtype,per,lanes,form", [
+    ("bf16", 64, 64, VECTOR), ("f32", 64, 64, VECTOR), ("bf16", 520, 64, TWO), ("f32", 264, 64, TWO), ("bf16", 1032, 256, VECTOR),
+    ("f32", 1020, 256, VECTOR), ("bf16", 2056, 256, TWO), ("f32", 1032, 256, TWO), ("bf16", 4104, 1024, VECTOR),
+    ("f32", 2056, 1024, VECTOR), ("f32", 4100, 1024, TWO), ("bf16", 519, 256, EIGHT), ("f32", 519, 256, EIGHT),
+    ("bf16", 2051, 1024, EIGHT), ("f32", 2501, 1024, EIGHT)])
+def test_norm_teams_of_several_rows(dtype, per, lanes, form):
+    """Every team of every kernel takes three rows and some a fourth: the row after is loaded meanwhile, the sums of a team
+    of several waves go through the same places again, the parameters' gradients add up over a team's rows."""
+    G = 3 if lanes == 64 else 1
+    C = G * per
+    # chunks of workgroups share the rows, as many as the backward keeps partial sums of
+    chunks = binding._norm_bwd_bytes(binding._STREAM[torch.float32 if dtype == "f32" else torch.bfloat16], 1 << 20, C, G) // (8 * C)
+    step = chunks * (8 if lanes == 64 else 1)
+    T = 3 * step + step // 3 + 1
+    t, gy = norm_inputs(T, C, dtype, gen(per))
+    f, names = launched(lambda: ssm.group_norm_fwd(groups=G, silu=True, **t))
+    assert names == [f"group norm, {lanes} lanes, {form}"]
+    g, names = launched(lambda: ssm.group_norm_bwd(gy=gy, groups=G, silu=True, **t))
+    assert names[0] == f"group norm backward, {lanes} lanes, {form}"
+    ref = R.norm(f64(t["x"]), G, f64(t["w"]), f64(t["bias"]), 1e-5, True, f64(t["z"]), f64(gy))
+    for k, v in {**f, **g}.items():
+        R.check(k, v, *ref[k], "f32" if k in ("gw", "gbias") else dtype)
