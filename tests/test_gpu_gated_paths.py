@@ -10,7 +10,7 @@ import selective_state_space_chunked_amd as ssm
 from selective_state_space_chunked_amd import binding
 
 from . import _gated_ref as R
-from .test_gpu_gated import GATED_OUT, f64, gated_inputs, gen, norm_inputs
+from .test_gpu_gated import GATED_OUT, f64, gated_inputs, gen, mm8_check, mm8_inputs, norm_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,25 @@ def test_norm_teams_of_several_rows(dtype, per, lanes, form):
     ref = R.norm(f64(t["x"]), G, f64(t["w"]), f64(t["bias"]), 1e-5, True, f64(t["z"]), f64(gy))
     for k, v in {**f, **g}.items():
         R.check(k, v, *ref[k], "f32" if k in ("gw", "gbias") else dtype)
+
+
+# ---------------------------------------------------------------------------
+# products in 8-bit integers
+# ---------------------------------------------------------------------------
+def product(tile, whole):
+    return "product in 8-bit integers, " + (f"tiles of {tile}" if tile else "few rows") + ("" if whole else ", through registers")
+
+
+@pytest.mark.parametrize("T,K,N,tile,side", [
+    (4096, 128, 4352, 256, 128), (4096, 336, 4352, 256, 128), (4096, 16, 4352, 256, 128), (4100, 384, 4300, 256, 128),
+    (3800, 64, 3700, 256, 128), (70000, 256, 128, 128, 128), (70000, 80, 128, 128, 128), (2049, 384, 2100, 128, 128),
+    (65664, 128, 64, 64, 64), (65664, 176, 64, 64, 64), (65664, 384, 61, 64, 64), (1030, 208, 1000, 64, 64),
+    (333, 515, 1999, 64, 64), (333, 512, 1999, 64, 64), (70, 8192, 500, 0, 0), (1000, 208, 61, 0, 0)])
+@pytest.mark.parametrize("view", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_mm8_every_kernel(T, K, N, tile, side, view, dtype):
+    """Every kernel with both types of result, which leave the sums by other ways: tiles of all sides whose workgroups go on
+    to a next tile and to a last one, rows that end inside a step, tiles that end outside y."""
+    whole = not view and K % 16 == 0
+    _, names = launched(lambda: mm8_check(mm8_inputs(T, K, N, gen(T + K), view=view), dtype))
+    assert names == [product(tile if whole else side, whole)]
