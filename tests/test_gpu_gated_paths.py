@@ -3,6 +3,7 @@ several tiles, values that are not finite beside lanes without channels.  Which 
 diagnostics, so that a size whose kernel changes fails its test."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -10,7 +11,8 @@ import selective_state_space_chunked_amd as ssm
 from selective_state_space_chunked_amd import binding
 
 from . import _gated_ref as R
-from .test_gpu_gated import GATED_OUT, f64, gated_inputs, gen, mm8_check, mm8_inputs, norm_inputs
+from . import _layer_ref as C
+from .test_gpu_gated import GATED_OUT, dev, f64, gated_inputs, gen, mm8_check, mm8_inputs, norm_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -61,11 +63,11 @@ def test_norm_non_finite_values_stay_in_their_group(G, per, dtype):
     """What is not finite in x, z or gy of one group of one row, or in w and bias of one channel, reaches that group's (that
     channel's group's) results and no other's: groups whose last lanes have no channels among them."""
     r = gen(G + per)
-    T, C = 9, G * per
-    t, gy = norm_inputs(T, C, dtype, r)
+    T, width = 9, G * per
+    t, gy = norm_inputs(T, width, dtype, r)
     ref = {**ssm.group_norm_fwd(groups=G, silu=True, **t), **ssm.group_norm_bwd(gy=gy, groups=G, silu=True, **t)}
     for name in ("x", "z", "gy", "w", "bias"):
-        for at in (0, per, C - 1):
+        for at in (0, per, width - 1):
             for bad in (float("nan"), float("inf"), -float("inf")):
                 u = {**t, "gy": gy}
                 u[name] = u[name].clone()
@@ -95,12 +97,12 @@ def test_norm_teams_of_several_rows(dtype, per, lanes, form):
     """Every team of every kernel takes three rows and some a fourth: the row after is loaded meanwhile, the sums of a team
     of several waves go through the same places again, the parameters' gradients add up over a team's rows."""
     G = 3 if lanes == 64 else 1
-    C = G * per
+    width = G * per
     # chunks of workgroups share the rows, as many as the backward keeps partial sums of
-    chunks = binding._norm_bwd_bytes(binding._STREAM[torch.float32 if dtype == "f32" else torch.bfloat16], 1 << 20, C, G) // (8 * C)
+    chunks = binding._norm_bwd_bytes(binding._STREAM[torch.float32 if dtype == "f32" else torch.bfloat16], 1 << 20, width, G) // (8 * width)
     step = chunks * (8 if lanes == 64 else 1)
     T = 3 * step + step // 3 + 1
-    t, gy = norm_inputs(T, C, dtype, gen(per))
+    t, gy = norm_inputs(T, width, dtype, gen(per))
     f, names = launched(lambda: ssm.group_norm_fwd(groups=G, silu=True, **t))
     assert names == [f"group norm, {lanes} lanes, {form}"]
     g, names = launched(lambda: ssm.group_norm_bwd(gy=gy, groups=G, silu=True, **t))
@@ -130,3 +132,50 @@ def test_mm8_every_kernel(T, K, N, tile, side, view, dtype):
     whole = not view and K % 16 == 0
     _, names = launched(lambda: mm8_check(mm8_inputs(T, K, N, gen(T + K), view=view), dtype))
     assert names == [product(tile if whole else side, whole)]
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_through_a_gated_layer(dtype):
+    """Convolution, gated recurrence and gated norm forward and back: the gradients that arrive at every input and
+    parameter against the layer's in float64, which differences of its loss along themselves confirm."""
+    r = gen(70)
+    B, D, L, G = 2, 24, 700, 3
+    x, ri, ii = (dev(r.normal(size=(B, D, L)), dtype) for _ in range(3))
+    z, gy = (dev(r.normal(size=(B * L, D)), dtype) for _ in range(2))
+    w, cb, nw, nb = dev(r.normal(size=(D, 4)) / 2), dev(0.1 * r.normal(size=D)), dev(1 + 0.1 * r.normal(size=D)), dev(0.1 * r.normal(size=D))
+    lam = dev(np.log(np.expm1(-np.log(r.uniform(0.9, 0.999, D)))))
+    rows = lambda v: v.transpose(1, 2).reshape(B * L, D).contiguous() if torch.is_tensor(v) else v.transpose(0, 2, 1).reshape(B * L, D)  # noqa: E731
+    streams = lambda v: (v.reshape(B, L, D).transpose(1, 2).contiguous() if torch.is_tensor(v)  # noqa: E731
+                         else v.reshape(B, L, D).transpose(0, 2, 1))
+    u = ssm.conv_fwd(x=x, w=w, bias=cb, silu=True)["y"]
+    h = ssm.gated_fwd(x=u, r=ri, i=ii, lam=lam, want_ckpt=True)
+    norm = dict(x=rows(h["y"]), groups=G, w=nw, bias=nb, z=z, silu=True)
+    gn = ssm.group_norm_bwd(gy=gy, **norm)
+    gr = ssm.gated_bwd(gy=streams(gn["gx"]), x=u, r=ri, i=ii, lam=lam, ckpt=h["ckpt"])
+    gc = ssm.conv_bwd(gy=gr["gx"], x=x, w=w, bias=cb, silu=True)
+    got = [gc["gx"], gc["gw"], gc["gbias"], gr["gr"], gr["gi"], gr["glam"], gn["gw"], gn["gbias"], gn["gz"]]
+    base = [f64(v) for v in (x, w, cb, ri, ii, lam, nw, nb, z)]
+
+    def layer(x, w, cb, ri, ii, lam, nw, nb, z, back=False):
+        u = C.conv_fwd(x, w, cb, None, True)[0]
+        h = R.gated_fwd(u, ri, ii, lam, None, None, 8.0, None)["y"][0]
+        n = R.norm(rows(h), G, nw, nb, 1e-5, True, z, f64(gy))
+        if not back:
+            return (f64(gy) * n["y"][0]).sum()
+        g = R.gated_bwd(u, ri, ii, lam, None, None, 8.0, None, streams(n["gx"][0]), None)
+        c = C.conv_bwd(x, w, cb, None, True, g["gx"][0], None)
+        return [v[0] for v in (c["gx"], c["gw"], c["gbias"], g["gr"], g["gi"], g["glam"], n["gw"], n["gbias"], n["gz"])]
+
+    for k, (g, v) in enumerate(zip(layer(*base, back=True), got)):
+        # along itself the loss rises by |g| a unit, and an unrelated direction would not be noticed to be one; differences
+        # of 1e-4 are off by 1e-8 times the loss's third derivatives, the loss itself by 1e-16 of it: 1e-12 / 1e-4
+        d = g / np.linalg.norm(g)
+        far = [[b + s * 1e-4 * d if j == k else b for j, b in enumerate(base)] for s in (1, -1)]
+        num = (layer(*far[0]) - layer(*far[1])) / 2e-4
+        assert abs(num - np.linalg.norm(g)) <= 1e-5 * np.linalg.norm(g), k
+        # six roundings of streams between the stages and at the end, each at most twice as large at the gradient as where
+        # it is made; fp32's own
+        assert np.linalg.norm(f64(v) - g) <= (12 * R.HALF[dtype] + 1e-4) * np.linalg.norm(g), k
