@@ -12,7 +12,7 @@ from selective_state_space_chunked_amd import binding
 
 from . import _gated_ref as R
 from . import _layer_ref as C
-from .test_gpu_gated import GATED_OUT, dev, f64, gated_inputs, gen, mm8_check, mm8_inputs, norm_inputs
+from .test_gpu_gated import DEV, DT, GATED_OUT, dev, f64, gated_inputs, gen, mm8_check, mm8_inputs, norm_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -179,3 +179,28 @@ def test_gradients_through_a_gated_layer(dtype):
         # six roundings of streams between the stages and at the end, each at most twice as large at the gradient as where
         # it is made; fp32's own
         assert np.linalg.norm(f64(v) - g) <= (12 * R.HALF[dtype] + 1e-4) * np.linalg.norm(g), k
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_no_rows_of_any_stride(dtype):
+    """Packed rows of which there are none, whatever their strides: no output rows, and the pool stays."""
+    D, S = 6, 3
+    none = torch.empty(0, 4 * D, dtype=DT[dtype], device=DEV)[:, ::4]
+    start = torch.zeros(S + 1, dtype=torch.int32, device=DEV)
+    one = dev(np.ones(D))
+    for native in (False, True):   # the binding's own path (outputs come from the tests' allocator), the native calls
+        if native:
+            ssm.set_allocator(None)
+        for f, inner, kw in (
+                (ssm.tokens_conv, (D, 3), dict(x=none, w=dev(np.ones((D, 4))))),
+                (ssm.tokens_scan, (D, 4), dict(delta=none, x=none, z=none, A=dev(-np.ones((D, 4))), Bm=none[:, :4], C=none[:, :4])),
+                (ssm.tokens_gated, (D,), dict(x=none, r=none, i=none, lam=one))):
+            pool = torch.full((S, *inner), 3.0, dtype=DT[dtype] if f is ssm.tokens_conv else torch.float32, device=DEV)
+            y = f(pool=pool, seq_start=start, **kw)["y"]
+            assert y.shape == (0, D) and y.dtype == DT[dtype] and (pool == 3).all()
+            out = torch.empty(0, 4 * D, dtype=DT[dtype], device=DEV)[:, ::4]
+            assert f(pool=pool, seq_start=start, out={"y": out}, **kw)["y"] is out and (pool == 3).all()
+        assert ssm.group_norm_fwd(x=none, groups=2, z=none)["y"].shape == (0, D)
+        g = ssm.group_norm_bwd(gy=none, x=none, groups=2)
+        assert g["gx"].shape == (0, D) and (g["gw"] == 0).all() and (g["gbias"] == 0).all()
+        assert ssm.tokens_pack8(none)["x8"].shape == (0, D)
