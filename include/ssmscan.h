@@ -78,6 +78,9 @@ extern "C" {
 /* Entry points added since with structs of their own leave the version as it is:
  * the gated recurrence (ssm_gated_*, ssm_tokens_gated), the group norm
  * (ssm_group_norm_*) and products in 8-bit integers (ssm_tokens_pack8, _mm8).
+ * An older library of version 8 has not got these symbols, so what calls them does
+ * not link or load with it; where they are looked up at run time, the symbol tells, or
+ * ssm_workspace_bytes of SSM_OP_GATED_FWD, which it answers with SSM_ERR_UNSUPPORTED.
  * 8: adds the short causal convolution (ssm_conv_*), 8-bit activation
  * checkpoints (ssm_ckpt8_*) and the serving forms over packed rows
  * (ssm_tokens_*); structs of 7 unchanged.  7 added SSM_HEAD_SCALAR
@@ -620,7 +623,9 @@ int ssm_tokens_scan(const ssm_tokens_scan_args* args, void* ws, size_t ws_bytes,
  * Strides are in elements: batch, then
  * channel; steps are contiguous; 0 (broadcast) for inputs only, whose gradients
  * come back for every position.  batch, channels and length may be 0 (h_last is
- * then h0 or 0, gh0 is gh_last or 0, parameter gradients are 0).
+ * then h0 or 0, gh0 is gh_last or 0, parameter gradients are 0).  SSM_ERR_SHAPE for
+ * a batch of more than 65535, as in the other calls over streams, for 2^24 channels,
+ * 2^31 - 2^16 steps or 2^28 - 64 rows (batch times channels) and more.
  */
 #define SSM_GATED_CHUNK 128
 typedef struct {
@@ -694,8 +699,10 @@ int ssm_tokens_gated(const ssm_tokens_gated_args* args, void* ws, size_t ws_byte
  *   xh = (x - mean) / sqrt(var + eps),  v = xh w + bias,
  *   u = v, or v sigmoid(v) with silu = 1,   y = u, or u z sigmoid(z) with z.
  * The backward forms the statistics again from x.  Row strides as in the packed
- * forms above.  rows may be 0 (gw, gbias are then 0).  Errors: SSM_ERR_SHAPE where
- * groups does not divide channels, SSM_ERR_UNSUPPORTED for groups of more than 8192
+ * forms above.  The statistics are float32: the values of a group are to stay below
+ * 2^114, their differences to the mean below 2^57, and var + eps is to be at least
+ * 2^-126 (with eps = 0 a group without spread has no value: NaN).  rows may be 0
+ * (gw, gbias are then 0).  Errors: SSM_ERR_SHAPE where groups does not divide channels, SSM_ERR_UNSUPPORTED for groups of more than 8192
  * channels.
  */
 typedef struct {
@@ -728,8 +735,8 @@ int ssm_group_norm_bwd(const ssm_group_norm_args* args, const void* gy, int64_t 
  *   y[t][n] = x8_scale[t] w8_scale[n] sum_k x8[t][k] w8[n][k] + bias[n].
  * The sums are whole numbers in 32 bits (inputs below 2^17: they cannot overflow),
  * rounded once to float32 before the scales, whose product is formed first: where that leaves float32's range y is
- * infinite or NaN.  Rows may have any stride from 0 (inputs) or their own width (outputs) to 2^40 - 1.  With no inputs
- * y is bias.  SSM_ERR_SHAPE for 2^17 inputs, 2^24 tokens or 2^26 outputs and more.
+ * infinite or NaN, and where it falls below it bias.  Rows may have any stride from 0 (inputs) or their own width
+ * (outputs) to 2^40 - 1.  With no inputs y is bias (where the scales' product is finite).  SSM_ERR_SHAPE for 2^17 inputs, 2^24 tokens or 2^26 outputs and more.
  */
 typedef struct {
     int32_t dtype;             /* of x                                                       */

@@ -1400,8 +1400,9 @@ def group_norm_fwd(*, x, groups, w=None, bias=None, eps=1e-5, silu=False, z=None
     """Group norm of the rows x (T, C), channels last: y = act((x - mean) / sqrt(var + eps) * w + bias), times
     z * sigmoid(z) with a gate ``z`` (T, C); act is the identity, or with ``silu`` v * sigmoid(v).
 
-    The statistics are those of one group (C / groups consecutive channels) of one row.  ``x`` and ``z`` may be slices
-    of wider rows; ``w``, ``bias`` (C,) float32.  Returns a dict with y (T, C)."""
+    The statistics are those of one group (C / groups consecutive channels) of one row, in float32: a group's differences
+    to its mean are to stay below 2^57 and var + eps at least 2^-126.  ``x`` and ``z`` may be slices of wider rows; ``w``,
+    ``bias`` (C,) float32.  Returns a dict with y (T, C)."""
     if nat := _native(x):
         m, di, stream = nat
         y = out.get("y") if out else None

@@ -12,7 +12,7 @@ from selective_state_space_chunked_amd import binding
 
 from . import _gated_ref as R
 from . import _layer_ref as C
-from .test_gpu_gated import DEV, DT, GATED_OUT, dev, f64, gated_inputs, gen, mm8_check, mm8_inputs, norm_inputs
+from .test_gpu_gated import DEV, DT, GATED_OUT, dev, f64, gated_inputs, gen, mm8_check, mm8_inputs, norm_check, norm_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -204,3 +204,12 @@ def test_no_rows_of_any_stride(dtype):
         g = ssm.group_norm_bwd(gy=none, x=none, groups=2)
         assert g["gx"].shape == (0, D) and (g["gw"] == 0).all() and (g["gbias"] == 0).all()
         assert ssm.tokens_pack8(none)["x8"].shape == (0, D)
+
+
+@pytest.mark.parametrize("eps,spread", [(0.0, 2.0 ** -62), (0.0, 1.0), (1e-5, 2.0 ** -62), (1e-5, 2.0 ** 54), (0.0, 2.0 ** 54)])
+@pytest.mark.parametrize("G,per", [(3, 65), (2, 2056), (1, 8192)])
+def test_norm_at_the_ends_of_its_range(G, per, eps, spread):
+    """Deviations whose squares' sum is just inside float32's range, and spreads whose variance is, without an eps."""
+    t, gy = norm_inputs(5, G * per, "f32", gen(per))
+    t["x"] = t["x"] * spread
+    norm_check(t, gy, G, "f32", True, eps)
