@@ -18,12 +18,14 @@ __global__ __launch_bounds__(norm_threads(TEAM)) void norm_bwd_kernel(NormParams
     __shared__ float lds[2][16];
     const Share<TEAM, V, R> at(p);
     float w[R][V], b[R][V], gw[R][V], gb[R][V];
+    // A lane without channels has read the first ones of the weights and of each row, which may be another group's and not
+    // finite: what comes of them is chosen to be 0, not multiplied by it.
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            w[i][e] = p.w ? p.w[at.at[i] + e] : 1.0f;
-            b[i][e] = p.bias ? p.bias[at.at[i] + e] : 0.0f;
+            w[i][e] = p.w && at.has[i] ? p.w[at.at[i] + e] : 1.0f;
+            b[i][e] = p.bias && at.has[i] ? p.bias[at.at[i] + e] : 0.0f;
             gw[i][e] = gb[i][e] = 0.0f;
         }
     const T* const x = (const T*)p.x;
@@ -64,11 +66,10 @@ __global__ __launch_bounds__(norm_threads(TEAM)) void norm_bwd_kernel(NormParams
                         gv *= zz * sz;
                     }
                     if (p.silu) gv *= sv * fmaf(v, 1.0f - sv, 1.0f);
+                    gv = at.has[i] ? gv : 0.0f;
                     gw[i][e] = fmaf(gv, xh[i][e], gw[i][e]);
                     gb[i][e] += gv;
-                    // chosen, not multiplied by 0: a lane without channels has read the row's first ones, which may be of
-                    // another group and not finite
-                    g[i][e] = at.has[i] ? gv * w[i][e] : 0.0f;
+                    g[i][e] = gv * w[i][e];
                     m[0] += g[i][e];
                     m[1] = fmaf(g[i][e], xh[i][e], m[1]);
                 }
