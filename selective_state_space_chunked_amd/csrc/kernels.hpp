@@ -354,8 +354,8 @@ struct GatedParams {
     float power;
     int B, D, L, nchunk, lanes, sums;   // lanes of a row: 16, 64, 256 or 1024
 };
-// Waves the lanes of a row are chosen for: 16 on each of the 1024 SIMDs.  B=8 D=2048 L=4096 bf16, a length of whole tiles
-// whatever the lanes (gated_lanes has others), forward and backward:
+// Waves the lanes of a row are chosen for: 16 on each of the 1024 SIMDs.  B=8 D=2048 L=4096 bf16, whole tiles with
+// each of these lanes (gated_lanes has other lengths), forward and backward:
 // 4096 waves of 16 lanes a row 141 and 195 us, 16384 of 64 lanes 123 and 186, 65536 of 256 lanes 117 and 207.
 constexpr int kGatedWaves = 16384;
 hipError_t launch_gated(const GatedParams& p, bool bwd, int dtype, hipStream_t st);
